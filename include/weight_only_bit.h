@@ -252,6 +252,102 @@ int mxfp4_moe_gemm_noalloc(const void *x, const int32_t *topk_ids, const uint8_t
                            int64_t N, int64_t K, int act, void *stream);
 
 /*
+ * MXFP4 quantisation: rows of x -> E2M1 codes and E8M0 scales in the layout
+ * of the weights above (OCP Microscaling Formats: MXFP4).  For each block of
+ * 32 elements v_i of a row, amax = max |v_i|:
+ *   X    = clamp(floor(log2 amax) - 2, -127, 127),  scale byte b = X + 127
+ *   code = the E2M1 value nearest to v_i * 2^-X (ties to the even code, held
+ *          at +-6; the sign is kept, also that of a zero)
+ * A block of zeros gets b = 0.  A block that holds a NaN or an infinity gets
+ * b = 255 (NaN) and codes 0: it reads back as NaN.
+ *
+ *  x: R rows of K elements, `ldx` elements from one row's start to the next's
+ *    (ldx >= K); x_dtype WOB_F16, WOB_BF16 or WOB_F32 (else WOB_DTYPE).
+ *  codes [R][K/2] uint8 (even element in the low nibble), scale [R][K/32]
+ *  uint8; both contiguous.
+ *  K % 32 == 0, K >= 32, R >= 0, R*K at most 2^34; rows start 16-byte
+ *  aligned: ldx % 8 == 0 (% 4 for WOB_F32) (else WOB_INVALID_ARG).
+ *  R == 0 is a no-op returning WOB_OK.
+ */
+int mxfp4_quantize(const void *x, int x_dtype, int64_t ldx, uint8_t *codes, uint8_t *scale,
+                   int64_t R, int64_t K, void *stream);
+
+/*
+ * Bytes of device workspace mxfp4_gemm needs (0 when it needs none, and for
+ * arguments it refuses on sight: a negative size, K < 32).
+ */
+size_t mxfp4_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/*
+ * MXFP4 x MXFP4 product: y[m][n] = sum_k x(m,k) * w(n,k), both operands E2M1
+ * codes with an E8M0 scale per 32 along K:
+ *   x_fp4 [M][K/2], x_scale [M][K/32], w_fp4 [N][K/2], w_scale [N][K/32] uint8,
+ *   y [M][N] of y_dtype WOB_F16, WOB_BF16 or WOB_F32 (else WOB_DTYPE).
+ *  Products are exact and summed in fp32; y is rounded once, to nearest even.
+ *  A scale byte of 255 (NaN) makes every output of its row (of x) or column
+ *  (of w) NaN.
+ *  K % 32 == 0, K >= 32, N % 8 == 0, M >= 0, N >= 0, M*K/2 and N*K/2 below
+ *  2^32 (else WOB_INVALID_ARG).  M == 0 or N == 0 is a no-op returning WOB_OK.
+ *  workspace: device memory of at least mxfp4_gemm_workspace_size(M, N, K)
+ *  bytes, 16-byte aligned (may be NULL when that is 0, else WOB_INVALID_ARG);
+ *  its contents on entry do not matter.  Calls that share one workspace must
+ *  be ordered on one stream.
+ */
+int mxfp4_gemm(const uint8_t *x_fp4, const uint8_t *x_scale, const uint8_t *w_fp4,
+               const uint8_t *w_scale, void *y, int y_dtype, int64_t M, int64_t N, int64_t K,
+               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Choice of experts: for each of T tokens with l_e = logits[t][e] + bias[e]
+ * in fp32 (bias NULL: l_e = logits[t][e]; NaN counts as -inf),
+ *   ids     [T][topk] int32: the topk largest l_e above -inf, largest first,
+ *           ties to the lowest e
+ *   weights [T][topk] fp32: exp(l - max l) / sum of exp(l - max l), the sum
+ *           over the chosen experts (renormalize != 0) or over all of them
+ * A place for which no expert above -inf is left gets id -1 and weight 0, so
+ * it adds nothing in the stages below (a masked expert holds -inf; a row may
+ * be masked whole).  Where the maximum is +inf, the experts at +inf share the
+ * weight equally.
+ *
+ *  logits [T][E] of logits_dtype WOB_F16, WOB_BF16 or WOB_F32 (else
+ *  WOB_DTYPE), bias [E] fp32 or NULL.
+ *  T >= 0, 1 <= E <= 4096, 1 <= topk <= 64, topk <= E, T*topk below 2^31
+ *  (else WOB_INVALID_ARG).  T == 0 is a no-op returning WOB_OK.
+ */
+int moe_topk(const void *logits, int logits_dtype, const float *bias, int32_t *ids, float *weights,
+             int64_t T, int64_t E, int64_t topk, int renormalize, void *stream);
+
+/*
+ * Bytes of device workspace mxfp4_moe_layer needs.  0 for arguments it
+ * refuses on sight (T < 0, topk outside 1..64, E outside 1..4096, H or I
+ * negative).
+ */
+size_t mxfp4_moe_layer_workspace_size(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I);
+
+/*
+ * A whole mixture-of-experts layer, BF16 x MXFP4, from the router's scores:
+ *   (id_s, p_s) = moe_topk(logits[t], bias, topk, renormalize)
+ *   a_s = silu(W1g_e x[t]) * (W1u_e x[t]),  e = id_s, rounded to bf16
+ *   y[t] = sum over s with id_s >= 0 of p_s * (W2_e a_s)
+ *  x [T][H] bf16; logits, bias as for moe_topk; w1_fp4 [E][2I][H/2],
+ *  w1_scale [E][2I][H/32] (gate rows 0 .. I-1, up rows I .. 2I-1); w2_fp4
+ *  [E][H][I/2], w2_scale [E][H][I/32]; y [T][H] bf16.
+ *  The function of moe_topk, mxfp4_moe_gemm (WOB_ACT_SILU_MUL) and
+ *  mxfp4_moe_stage2 in turn; the sums are fp32 and their order may differ.
+ *  H % 64 == 0, H >= 64, I % 64 == 0, I >= 64, T >= 0, 1 <= topk <= 64,
+ *  topk <= E, 1 <= E <= 4096, T*H*2, T*topk*I*2, I*H and H*I/2 below 2^32
+ *  (else WOB_INVALID_ARG).  T == 0 is a no-op returning WOB_OK.
+ *  workspace: device memory of at least mxfp4_moe_layer_workspace_size(T,
+ *  topk, E, H, I) bytes, 16-byte aligned; contents on entry do not matter.
+ *  Calls that share one workspace must be ordered on one stream.
+ */
+int mxfp4_moe_layer(const void *x, const void *logits, int logits_dtype, const float *bias,
+                    const uint8_t *w1_fp4, const uint8_t *w1_scale, const uint8_t *w2_fp4,
+                    const uint8_t *w2_scale, void *y, int64_t T, int64_t topk, int64_t E, int64_t H,
+                    int64_t I, int renormalize, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/*
  * Dequantization probes: write out the weights as the GEMM kernels form them,
  * through the same device helpers, so the unpack / dequantize stage can be
  * compared bit for bit with its definition.  Source: zero-point page above,

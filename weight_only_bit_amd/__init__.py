@@ -9,6 +9,10 @@ fallback.
     y = gemm_grouped(x, m_offsets, qweight, scales, qzeros, group_size)
     y = mxfp4_moe_gemm(x, topk_ids, w_fp4, w_scale)         # MoE stage 1
     y = mxfp4_moe_stage2(a, topk_ids, topk_weights, w2_fp4, w2_scale)  # MoE stage 2
+    ids, weights = moe_topk(logits, topk)                   # the choice of experts
+    y = mxfp4_moe_layer(x, logits, topk, w1_fp4, w1_scale, w2_fp4, w2_scale)  # a whole MoE layer
+    codes, scale = mxfp4_quantize(x)                        # 16/32-bit rows -> MXFP4
+    y = mxfp4_gemm(x_fp4, x_scale, w_fp4, w_scale)          # MXFP4 x MXFP4
 
 Layouts are those of ``include/weight_only_bit.h``.
 """
@@ -23,7 +27,8 @@ from ._lib import (ACT_NONE, ACT_SILU_MUL, BF16, DTYPE, F16, F32, INVALID_ARG, O
 
 __all__ = [
     "gemm", "gemm_grouped", "mxfp4_moe_gemm", "moe_workspace_size", "mxfp4_moe_stage2",
-    "moe_stage2_workspace_size", "w4a16_dequant",
+    "moe_stage2_workspace_size", "moe_topk", "mxfp4_moe_layer", "moe_layer_workspace_size",
+    "mxfp4_quantize", "mxfp4_gemm", "mxfp4_gemm_workspace_size", "w4a16_dequant",
     "mxfp4_dequant", "stream_read", "device_check", "WobError", "WobDtypeError", "WobArgError",
     "PATH_AUTO", "PATH_SKINNY", "PATH_TILED", "ACT_NONE", "ACT_SILU_MUL",
 ]
@@ -252,6 +257,168 @@ def mxfp4_moe_stage2(a, topk_ids, topk_weights, w2_fp4, w2_scale, out=None, work
             _ptr(a), _ptr(topk_ids), _ptr(topk_weights), _ptr(w2_fp4), _ptr(w2_scale), _ptr(out),
             T, topk, E, H, I, _ptr(workspace), ws_bytes, _stream(dev))
     _lib.check(st, "mxfp4_moe_stage2")
+    return out
+
+
+def _value_dtypes():
+    torch = _torch()
+    return (torch.float16, torch.bfloat16, torch.float32)
+
+
+def _workspace(workspace, need, device):
+    """A caller's workspace, checked, or a new one: (tensor, bytes)."""
+    torch = _torch()
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    if ws_bytes < need:
+        raise ValueError(f"workspace holds {ws_bytes} bytes; {need} are needed")
+    return workspace, ws_bytes
+
+
+def mxfp4_quantize(x, out=None, out_scale=None):
+    """MXFP4 quantisation along the last dimension: x [..., K] fp16/bf16/fp32 ->
+    (codes [..., K/2] uint8, scale [..., K/32] uint8 E8M0), the layout the MXFP4
+    products read.  x is contiguous, or 2-D with contiguous elements in each row
+    and rows any 16-byte aligned distance apart (a column slice)."""
+    torch = _torch()
+    if x.dim() < 1:
+        raise ValueError("x must be [..., K]")
+    _want(x, "x", tuple(x.shape), _value_dtypes())
+    K = x.shape[-1]
+    if K < 32 or K % 32 != 0:
+        raise ValueError(f"K={K} must be a multiple of 32 (one E8M0 scale per 32)")
+    lead = tuple(x.shape[:-1])
+    R = 1
+    for n in lead:
+        R *= n
+    if x.is_contiguous():
+        ldx = K
+    elif x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= K:
+        ldx = x.stride(0)
+    else:
+        raise ValueError("x must be contiguous, or a 2-D column slice of a contiguous tensor")
+    if out is None:
+        out = torch.empty((*lead, K // 2), dtype=torch.uint8, device=x.device)
+    if out_scale is None:
+        out_scale = torch.empty((*lead, K // 32), dtype=torch.uint8, device=x.device)
+    _want(out, "out", (*lead, K // 2), (torch.uint8,))
+    _want(out_scale, "out_scale", (*lead, K // 32), (torch.uint8,))
+    dev = _check_device(out, out_scale)
+    if x.device != dev:
+        raise ValueError("operands live on different devices")
+    with torch.cuda.device(dev):
+        st = _lib.lib().mxfp4_quantize(_ptr(x), _tag(x), ldx, _ptr(out), _ptr(out_scale), R, K,
+                                       _stream(dev))
+    _lib.check(st, "mxfp4_quantize")
+    return out, out_scale
+
+
+def mxfp4_gemm_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes of workspace mxfp4_gemm needs (0 also for arguments it refuses)."""
+    return int(_lib.lib().mxfp4_gemm_workspace_size(M, N, K))
+
+
+def mxfp4_gemm(x_fp4, x_scale, w_fp4, w_scale, out=None, out_dtype=None, workspace=None):
+    """MXFP4 x MXFP4 product: x_fp4 [M,K/2], x_scale [M,K/32], w_fp4 [N,K/2] and
+    w_scale [N,K/32] uint8 -> y [M,N] = x . w^T in out_dtype (bfloat16 when
+    neither it nor out is given; float16 and float32 too)."""
+    torch = _torch()
+    if x_fp4.dim() != 2 or w_fp4.dim() != 2:
+        raise ValueError("x_fp4 must be [M, K/2] and w_fp4 [N, K/2]")
+    M, K = x_fp4.shape[0], x_fp4.shape[1] * 2
+    N = w_fp4.shape[0]
+    if K < 32 or K % 32 != 0:
+        raise ValueError(f"K={K} must be a multiple of 32 (one E8M0 scale per 32)")
+    _want(x_fp4, "x_fp4", (M, K // 2), (torch.uint8,))
+    _want(x_scale, "x_scale", (M, K // 32), (torch.uint8,))
+    _want(w_fp4, "w_fp4", (N, K // 2), (torch.uint8,))
+    _want(w_scale, "w_scale", (N, K // 32), (torch.uint8,))
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    if out_dtype not in _value_dtypes():
+        raise TypeError(f"out_dtype {out_dtype} must be float16, bfloat16 or float32")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=x_fp4.device)
+    _want(out, "out", (M, N), (out_dtype,))
+    workspace, ws_bytes = _workspace(workspace, mxfp4_gemm_workspace_size(M, N, K), x_fp4.device)
+    dev = _check_device(x_fp4, x_scale, w_fp4, w_scale, out, workspace)
+    with torch.cuda.device(dev):
+        st = _lib.lib().mxfp4_gemm(_ptr(x_fp4), _ptr(x_scale), _ptr(w_fp4), _ptr(w_scale), _ptr(out),
+                                   _tag(out), M, N, K, _ptr(workspace), ws_bytes, _stream(dev))
+    _lib.check(st, "mxfp4_gemm")
+    return out
+
+
+def _check_choice(logits, topk, bias):
+    """logits [T, E], bias [E] or None -> (T, E)."""
+    torch = _torch()
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    _want(logits, "logits", tuple(logits.shape), _value_dtypes())
+    T, E = logits.shape
+    if not 1 <= topk <= min(E, 64):
+        raise ValueError(f"topk={topk} must be between 1 and min(E={E}, 64)")
+    if bias is not None:
+        _want(bias, "bias", (E,), (torch.float32,))
+    return T, E
+
+
+def moe_topk(logits, topk: int, bias=None, renormalize: bool = True, ids=None, weights=None):
+    """Choice of experts: logits [T,E] fp16/bf16/fp32 (+ bias [E] float32) ->
+    (ids [T,topk] int32, weights [T,topk] float32), largest first, ties to the
+    lowest expert.  weights: softmax over the chosen (renormalize) or over all
+    experts.  Places without an expert above -inf hold id -1 and weight 0."""
+    torch = _torch()
+    T, E = _check_choice(logits, topk, bias)
+    if ids is None:
+        ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+    _want(ids, "ids", (T, topk), (torch.int32,))
+    _want(weights, "weights", (T, topk), (torch.float32,))
+    dev = _check_device(logits, bias, ids, weights)
+    with torch.cuda.device(dev):
+        st = _lib.lib().moe_topk(_ptr(logits), _tag(logits), _ptr(bias), _ptr(ids), _ptr(weights),
+                                 T, E, topk, int(bool(renormalize)), _stream(dev))
+    _lib.check(st, "moe_topk")
+    return ids, weights
+
+
+def moe_layer_workspace_size(T: int, topk: int, E: int, H: int, I: int) -> int:
+    """Bytes of workspace mxfp4_moe_layer needs (0 for arguments it refuses)."""
+    return int(_lib.lib().mxfp4_moe_layer_workspace_size(T, topk, E, H, I))
+
+
+def mxfp4_moe_layer(x, logits, topk: int, w1_fp4, w1_scale, w2_fp4, w2_scale, bias=None,
+                    renormalize: bool = True, out=None, workspace=None):
+    """A whole MoE layer from the router's scores: x [T,H] bf16, logits [T,E]
+    (bias [E]) as for moe_topk, w1_fp4 [E,2I,H/2], w1_scale [E,2I,H/32], w2_fp4
+    [E,H,I/2], w2_scale [E,H,I/32] uint8 -> y [T,H] bf16 = sum over the chosen
+    experts of weight * W2(silu(W1g x) * (W1u x))."""
+    torch = _torch()
+    if x.dim() != 2 or w1_fp4.dim() != 3 or w2_fp4.dim() != 3:
+        raise ValueError("x must be [T, H], w1_fp4 [E, 2I, H/2] and w2_fp4 [E, H, I/2]")
+    T, E = _check_choice(logits, topk, bias)
+    H, I = x.shape[1], w2_fp4.shape[2] * 2
+    if H < 64 or I < 64 or H % 64 != 0 or I % 64 != 0:
+        raise ValueError(f"H={H} and I={I} must be multiples of 64")
+    _want(x, "x", (T, H), (torch.bfloat16,))
+    _want(w1_fp4, "w1_fp4", (E, 2 * I, H // 2), (torch.uint8,))
+    _want(w1_scale, "w1_scale", (E, 2 * I, H // 32), (torch.uint8,))
+    _want(w2_fp4, "w2_fp4", (E, H, I // 2), (torch.uint8,))
+    _want(w2_scale, "w2_scale", (E, H, I // 32), (torch.uint8,))
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    _want(out, "out", (T, H), (torch.bfloat16,))
+    workspace, ws_bytes = _workspace(workspace, moe_layer_workspace_size(T, topk, E, H, I), x.device)
+    dev = _check_device(x, logits, bias, w1_fp4, w1_scale, w2_fp4, w2_scale, out, workspace)
+    with torch.cuda.device(dev):
+        st = _lib.lib().mxfp4_moe_layer(
+            _ptr(x), _ptr(logits), _tag(logits), _ptr(bias), _ptr(w1_fp4), _ptr(w1_scale),
+            _ptr(w2_fp4), _ptr(w2_scale), _ptr(out), T, topk, E, H, I, int(bool(renormalize)),
+            _ptr(workspace), ws_bytes, _stream(dev))
+    _lib.check(st, "mxfp4_moe_layer")
     return out
 
 

@@ -23,6 +23,8 @@ EXPORTS = [
     "mxfp4_moe_gemm_workspace_size", "mxfp4_moe_gemm", "mxfp4_moe_gemm_tile_m",
     "mxfp4_moe_gemm_noalloc",
     "mxfp4_moe_stage2_workspace_size", "mxfp4_moe_stage2",
+    "mxfp4_quantize", "mxfp4_gemm_workspace_size", "mxfp4_gemm",
+    "moe_topk", "mxfp4_moe_layer_workspace_size", "mxfp4_moe_layer",
     "w4a16_dequant", "mxfp4_dequant", "wob_stream_read",
 ]
 
@@ -49,6 +51,13 @@ _SIGNATURES = {
     "mxfp4_moe_stage2_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i64]),
     "mxfp4_moe_stage2": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _sz,
                               _vp]),
+    "mxfp4_quantize": (_i, [_vp, _i, _i64, _vp, _vp, _i64, _i64, _vp]),
+    "mxfp4_gemm_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "mxfp4_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i64, _i64, _i64, _vp, _sz, _vp]),
+    "moe_topk": (_i, [_vp, _i, _vp, _vp, _vp, _i64, _i64, _i64, _i, _vp]),
+    "mxfp4_moe_layer_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "mxfp4_moe_layer": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
+                             _i64, _i, _vp, _sz, _vp]),
     "w4a16_dequant": (_i, [_vp, _vp, _i, _vp, _i, _vp, _i, _i64, _i64, _i64, _vp]),
     "mxfp4_dequant": (_i, [_vp, _vp, _vp, _i64, _i64, _vp]),
     "wob_stream_read": (_i, [_vp, _sz, _vp, _vp]),

@@ -414,6 +414,174 @@ int mxfp4_moe_gemm_noalloc(const void *x, const int32_t *topk_ids, const uint8_t
                     "mxfp4 moe (static scratch)");
 }
 
+int mxfp4_quantize(const void *x, int x_dtype, int64_t ldx, uint8_t *codes, uint8_t *scale,
+                   int64_t R, int64_t K, void *stream)
+{
+    if (x_dtype != WOB_F16 && x_dtype != WOB_BF16 && x_dtype != WOB_F32)
+        return fail(WOB_DTYPE, "x dtype tag %d is not F16, BF16 or F32", x_dtype);
+    if (R < 0 || K < 32 || K % 32 != 0)
+        return fail(WOB_INVALID_ARG, "bad shape R=%lld K=%lld (K must be a multiple of 32)",
+                    (long long)R, (long long)K);
+    if (ldx < K || ldx % (x_dtype == WOB_F32 ? 4 : 8) != 0)
+        return fail(WOB_INVALID_ARG, "row stride %lld is below K=%lld or leaves rows unaligned",
+                    (long long)ldx, (long long)K);
+    constexpr int64_t most = (int64_t)1 << 34;
+    if (K > most || R > most / K || ldx > ((int64_t)1 << 40) || (R && ldx > ((int64_t)1 << 60) / R))
+        return fail(WOB_INVALID_ARG, "shape too large");
+    if (R == 0)
+        return ok();
+    if (!x || !codes || !scale)
+        return fail(WOB_INVALID_ARG, "null operand pointer");
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scale))
+        return fail(WOB_INVALID_ARG, "operand pointers must be 16-byte aligned");
+    int s = arch_gate();
+    if (s != WOB_OK)
+        return s;
+    return launched(wob::launch_mxfp4_quantize(x, x_dtype, ldx, codes, scale, R, K,
+                                               static_cast<hipStream_t>(stream)),
+                    "mxfp4 quantize");
+}
+
+size_t mxfp4_gemm_workspace_size(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 0 || N < 0 || K < 32 || M > INT_MAX / 2 || N > INT_MAX / 2 || K > INT_MAX / 2)
+        return 0;
+    return wob::mxfp4_gemm_workspace_bytes(M, N, K);
+}
+
+int mxfp4_gemm(const uint8_t *x_fp4, const uint8_t *x_scale, const uint8_t *w_fp4,
+               const uint8_t *w_scale, void *y, int y_dtype, int64_t M, int64_t N, int64_t K,
+               void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (y_dtype != WOB_F16 && y_dtype != WOB_BF16 && y_dtype != WOB_F32)
+        return fail(WOB_DTYPE, "y dtype tag %d is not F16, BF16 or F32", y_dtype);
+    if (M < 0 || N < 0 || K < 32)
+        return fail(WOB_INVALID_ARG, "bad shape M=%lld N=%lld K=%lld", (long long)M, (long long)N,
+                    (long long)K);
+    if (K % 32 != 0 || N % 8 != 0)
+        return fail(WOB_INVALID_ARG, "need K %% 32 == 0 and N %% 8 == 0 (K=%lld N=%lld)",
+                    (long long)K, (long long)N);
+    // 32-bit in-kernel offsets into each operand's codes
+    if (M > INT_MAX / 2 || N > INT_MAX / 2 || K > INT_MAX / 2 || M * (K / 2) > (int64_t)UINT32_MAX ||
+        N * (K / 2) > (int64_t)UINT32_MAX)
+        return fail(WOB_INVALID_ARG, "shape too large");
+    if (M == 0 || N == 0)
+        return ok();
+    if (!x_fp4 || !x_scale || !w_fp4 || !w_scale || !y)
+        return fail(WOB_INVALID_ARG, "null operand pointer");
+    if (!aligned16(x_fp4) || !aligned16(x_scale) || !aligned16(w_fp4) || !aligned16(w_scale) ||
+        !aligned16(y))
+        return fail(WOB_INVALID_ARG, "operand pointers must be 16-byte aligned");
+    const size_t need = wob::mxfp4_gemm_workspace_bytes(M, N, K);
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+        return fail(WOB_INVALID_ARG, "workspace needs %zu bytes, 16-byte aligned (got %zu)", need,
+                    workspace_bytes);
+    int s = arch_gate();
+    if (s != WOB_OK)
+        return s;
+    return launched(wob::launch_mxfp4_gemm(x_fp4, x_scale, w_fp4, w_scale, y, y_dtype, (int)M,
+                                           (int)N, (int)K, workspace,
+                                           static_cast<hipStream_t>(stream)),
+                    "mxfp4 gemm");
+}
+
+namespace {
+
+// The choice's argument checks, shared by moe_topk and the layer.
+int check_choice(int logits_dtype, int64_t T, int64_t E, int64_t topk)
+{
+    if (logits_dtype != WOB_F16 && logits_dtype != WOB_BF16 && logits_dtype != WOB_F32)
+        return fail(WOB_DTYPE, "logits dtype tag %d is not F16, BF16 or F32", logits_dtype);
+    if (T < 0 || E < 1 || E > 4096 || topk < 1 || topk > 64 || topk > E)
+        return fail(WOB_INVALID_ARG, "bad shape T=%lld E=%lld topk=%lld", (long long)T,
+                    (long long)E, (long long)topk);
+    if (T > INT_MAX / 64)
+        return fail(WOB_INVALID_ARG, "shape too large");
+    return WOB_OK;
+}
+
+} // namespace
+
+int moe_topk(const void *logits, int logits_dtype, const float *bias, int32_t *ids, float *weights,
+             int64_t T, int64_t E, int64_t topk, int renormalize, void *stream)
+{
+    int s = check_choice(logits_dtype, T, E, topk);
+    if (s != WOB_OK)
+        return s;
+    if (T == 0)
+        return ok();
+    if (!logits || !ids || !weights)
+        return fail(WOB_INVALID_ARG, "null operand pointer");
+    if (!aligned16(logits) || !aligned16(ids) || !aligned16(weights) || !aligned16(bias))
+        return fail(WOB_INVALID_ARG, "operand pointers must be 16-byte aligned");
+    s = arch_gate();
+    if (s != WOB_OK)
+        return s;
+    return launched(wob::launch_moe_topk(logits, logits_dtype, bias, ids, weights, (int)T, (int)E,
+                                         (int)topk, renormalize != 0,
+                                         static_cast<hipStream_t>(stream)),
+                    "moe topk");
+}
+
+size_t mxfp4_moe_layer_workspace_size(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
+{
+    if (T < 0 || topk < 1 || E < 1 || H < 0 || I < 0 || T > INT_MAX / 64 || topk > 64 ||
+        E > 4096 || H > INT_MAX / 2 || I > INT_MAX / 4)
+        return 0;
+    return wob::moe_layer_workspace_bytes(T, topk, E, H, I);
+}
+
+int mxfp4_moe_layer(const void *x, const void *logits, int logits_dtype, const float *bias,
+                    const uint8_t *w1_fp4, const uint8_t *w1_scale, const uint8_t *w2_fp4,
+                    const uint8_t *w2_scale, void *y, int64_t T, int64_t topk, int64_t E, int64_t H,
+                    int64_t I, int renormalize, void *workspace, size_t workspace_bytes,
+                    void *stream)
+{
+    int s = check_choice(logits_dtype, T, E, topk);
+    if (s != WOB_OK)
+        return s;
+    if (H < 64 || I < 64 || H % 64 != 0 || I % 64 != 0)
+        return fail(WOB_INVALID_ARG, "need H and I multiples of 64 (H=%lld I=%lld)", (long long)H,
+                    (long long)I);
+    // 32-bit in-kernel offsets: x, the activated rows, one expert's codes
+    if (H > INT_MAX / 2 || I > INT_MAX / 4 || T * H * 2 > (int64_t)UINT32_MAX ||
+        T * topk * I * 2 > (int64_t)UINT32_MAX || I * H > (int64_t)UINT32_MAX ||
+        E * I * H > ((int64_t)1 << 40))
+        return fail(WOB_INVALID_ARG, "shape too large");
+    if (T == 0)
+        return ok();
+    if (!x || !logits || !w1_fp4 || !w1_scale || !w2_fp4 || !w2_scale || !y)
+        return fail(WOB_INVALID_ARG, "null operand pointer");
+    if (!aligned16(x) || !aligned16(logits) || !aligned16(bias) || !aligned16(w1_fp4) ||
+        !aligned16(w1_scale) || !aligned16(w2_fp4) || !aligned16(w2_scale) || !aligned16(y))
+        return fail(WOB_INVALID_ARG, "operand pointers must be 16-byte aligned");
+    const size_t need = wob::moe_layer_workspace_bytes(T, topk, E, H, I);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need)
+        return fail(WOB_INVALID_ARG, "workspace needs %zu bytes, 16-byte aligned (got %zu)", need,
+                    workspace_bytes);
+    s = arch_gate();
+    if (s != WOB_OK)
+        return s;
+    wob::MoeLayerArgs a;
+    a.x = x;
+    a.logits = logits;
+    a.logits_dt = logits_dtype;
+    a.bias = bias;
+    a.w1 = w1_fp4;
+    a.w1s = w1_scale;
+    a.w2 = w2_fp4;
+    a.w2s = w2_scale;
+    a.y = y;
+    a.T = (int)T;
+    a.topk = (int)topk;
+    a.E = (int)E;
+    a.H = (int)H;
+    a.I = (int)I;
+    a.renormalize = renormalize != 0;
+    return launched(wob::launch_mxfp4_moe_layer(a, workspace, static_cast<hipStream_t>(stream)),
+                    "mxfp4 moe layer");
+}
+
 int w4a16_dequant(const int32_t *qweight, const void *scales, int scales_dtype,
                   const void *qzeros, int zeros_dtype, void *out, int out_dtype, int64_t N,
                   int64_t K, int64_t group_size, void *stream)

@@ -74,6 +74,32 @@ hipError_t launch_mxfp4_moe(const void *x, const int32_t *ids, const uint8_t *w_
                             const uint8_t *w_scale, void *y, int T, int topk, int E, int N, int K,
                             int act, int tile_m, void *workspace, hipStream_t stream);
 
+// Whole mixture-of-experts layer and the choice of experts.
+struct MoeLayerArgs {
+    const void *x, *logits;
+    int logits_dt; // DT_F16 / DT_BF16 / DT_F32
+    const float *bias; // nullptr: none
+    const uint8_t *w1, *w1s, *w2, *w2s;
+    void *y;
+    int T, topk, E, H, I;
+    bool renormalize;
+};
+hipError_t launch_moe_topk(const void *logits, int dt, const float *bias, int32_t *ids,
+                           float *weights, int T, int E, int topk, bool renormalize,
+                           hipStream_t stream);
+size_t moe_layer_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I);
+hipError_t launch_mxfp4_moe_layer(const MoeLayerArgs &a, void *workspace, hipStream_t stream);
+
+// MXFP4 quantisation of rows `ldx` elements apart.
+hipError_t launch_mxfp4_quantize(const void *x, int dt, int64_t ldx, uint8_t *codes, uint8_t *scale,
+                                 int64_t R, int64_t K, hipStream_t stream);
+
+// MXFP4 x MXFP4 product; ydt: DT_F16 / DT_BF16 / DT_F32.
+size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t *w,
+                             const uint8_t *ws, void *y, int ydt, int M, int N, int K,
+                             void *workspace, hipStream_t stream);
+
 // Dequantization probes.
 hipError_t launch_w4a16_dequant(const uint32_t *qweight, const void *scales, const uint32_t *qzeros,
                                 void *out, int dt, bool out_f32, int N, int K, int g,
