@@ -28,7 +28,6 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int FMT_FP4 = 4; // operand format E2M1 of the f8f6f4 matrix instructions
-constexpr uint32_t ONE_X4 = 0x7F7F7F7Fu; // four scale bytes of 1.0
 
 __device__ __forceinline__ i32x8 fp4_operand(const u32x4 &v)
 {
@@ -199,50 +198,135 @@ hipError_t launch_few(const uint8_t *x, const uint8_t *xs, const uint8_t *w, con
 //
 // A workgroup of 4 waves (WN along n, 4 / WN along m) owns TN weight rows x TM
 // activation rows; a wave owns NB x MB blocks of 32 x 32 outputs.  K advances
-// in spans of 256 (128 code bytes and 8 scale bytes a row), double buffered in
-// LDS: the codes are copied by global_load_lds_dwordx4 (8 rows of 128 bytes,
-// whole cache lines, per wave instruction), the scales pass through registers.
-// A span is four MFMA steps of 64 k: in step s the lane half h = lane / 32
-// supplies block 4 h + s of its row, so the four scale bytes a lane needs in a
-// span are one dword of its row's eight, and the instruction selects byte s.
+// in stages of 128 (64 code bytes a row), NS = 4 of them in LDS at a time; four
+// stages, a span of 512, share the 16 scale bytes a row has per 512 k.  Codes and
+// scales are copied by global_load_lds (16 rows x 64 code bytes, or 16 rows x
+// 16 scale bytes, per wave instruction), NS - 1 stages ahead of their use.
+// Copied from rows K / 32 bytes apart, the scales cost as many cache look-ups a
+// row as the codes do.  PACKED: a kernel before this one lays the scales out span
+// by span, the 16 bytes of successive rows side by side, so that one copy takes
+// 64 rows.  2048 x 16384 x 5376: scales 8 bytes a row at a time 118 us, 16 bytes
+// 114, packed 110 with the packing; 100 x 5376 x 21504, where the scales are
+// a larger share, 29.7 us straight and 32.1 packed.  Rows that are not
+// 4-byte aligned (K % 128 != 0) are always packed.
 //
-// LDS row R (weight rows, then activation rows) is 128 bytes; its 16-byte
-// piece p lies at position p ^ ((R >> 1) & 7), so the 16 rows that one piece
-// is read from at a time cover all 64 banks.
-template <int WN_, int NB_, int MB_>
+// A stage is two MFMA steps of 64 k: in step j the lane half h = lane / 32
+// supplies block 2 h + j of its row, so a lane needs bytes 2 h, 2 h + 1 of each
+// of the span's four scale dwords: a byte permute packs those of two stages into
+// one register, and the instruction selects the byte.
+//
+// LDS row R (weight rows, then activation rows) holds 64 bytes of a stage; its
+// 16-byte piece p lies at position p ^ ((R >> 2) & 3), so the 16 rows that one
+// piece is read from at a time cover all 64 banks.
+//
+// Order within stage t (see run_span): step 0 reads step 1's operands and
+// multiplies; then stage t + 1's copies are waited for, a barrier makes them
+// visible and frees stage t's place (every wave has its last operands in
+// registers), and step 1 reads stage t + 1's first operands and starts the
+// copies of stage t + NS while it multiplies.  No operand read and no copy is
+// waited for in the step that issues it.
+template <int WN_, int NB_, int MB_, int NS_>
 struct MxTile {
-    static constexpr int WN = WN_, WM = 4 / WN_, NB = NB_, MB = MB_;
+    static constexpr int WN = WN_, WM = 4 / WN_, NB = NB_, MB = MB_, NS = NS_;
     static constexpr int TN = 32 * NB * WN, TM = 32 * MB * WM, ROWS = TN + TM;
-    static constexpr int BUF = ROWS * 128;          // codes of one span
-    static constexpr int LDS = 2 * BUF + 2 * ROWS * 8;
-    static constexpr int ND = ROWS / 32;            // copies per wave and span
-    static constexpr int SR = (ROWS + 255) / 256;   // scale rows per thread
-    static_assert(LDS <= 160 * 1024, "tile fits the LDS");
+    static constexpr int STAGE = ROWS * 64;              // code bytes of one stage
+    static constexpr int ND = ROWS / 64;                 // code copies per wave and stage
+    static constexpr int SROWS = (ROWS + 255) & ~255;    // scale rows in LDS
+    static constexpr int LDS = NS * STAGE + 2 * SROWS * 16;
+    static constexpr int WSTAGE = LDS / 4 & ~15;         // LDS of one wave in the epilogue
+    static_assert(ROWS % 64 == 0 && NS == 4 && LDS <= 160 * 1024, "tile geometry");
 };
 
-constexpr int MX_SPAN = 256;
+constexpr int MX_SPAN = 512;
 
-// The eight scale bytes of blocks b .. b + 7 of a row at p (KB blocks); bytes
-// past the row read as 1.0.
-__device__ __forceinline__ uint2 scale8(const uint8_t *row, int b, int KB)
+// As lds_dma16 with 4 bytes per lane (lane L's bytes land at `lds_addr` + 4 L).
+__device__ __forceinline__ void lds_dma4(const void *sbase_any, uint32_t voff, uint32_t lds_addr)
 {
-    uint2 v;
-    if (b + 8 <= KB) {
-        __builtin_memcpy(&v, row + b, 8); // K % 256 != 0 leaves rows unaligned
-    } else {
-        v = uint2{ONE_X4, ONE_X4};
-        for (int i = 0; b + i < KB; ++i) {
-            const uint32_t s = row[b + i];
-            if (i < 4)
-                v.x = (v.x & ~(0xFFu << (8 * i))) | (s << (8 * i));
-            else
-                v.y = (v.y & ~(0xFFu << (8 * i - 32))) | (s << (8 * i - 32));
-        }
-    }
-    return v;
+    const uint64_t b = reinterpret_cast<uint64_t>(sbase_any);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+    const void *sbase = reinterpret_cast<const void *>(((uint64_t)hi << 32) | (uint64_t)lo);
+    uint32_t saved;
+    asm volatile("s_mov_b32 %0, m0\n\t"
+                 "s_mov_b32 m0, %1\n\t"
+                 "global_load_lds_dword %2, %3\n\t"
+                 "s_mov_b32 m0, %0"
+                 : "=&s"(saved)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(voff), "s"(sbase)
+                 : "memory");
 }
 
-template <class T>
+// Packed scales: span u of row r at ((u * rows) + r) * 16, bytes past the row
+// zero (a finite scale, met by zero codes).  One thread per 16 bytes, the spans
+// of a row side by side, so the reads are contiguous.
+__global__ __launch_bounds__(256) void mxfp4_pack_scales_kernel(const uint8_t *__restrict__ ws,
+                                                                const uint8_t *__restrict__ xs,
+                                                                u32x4 *__restrict__ out, int N, int M,
+                                                                int KB, int spans)
+{
+    const int rows = N + M;
+    const uint32_t i0 = blockIdx.x * 256 + threadIdx.x;
+    const int r = (int)(i0 / (uint32_t)spans), u = (int)(i0 - (uint32_t)r * (uint32_t)spans);
+    if (r >= rows)
+        return;
+    const uint8_t *row = r < N ? ws + (size_t)r * KB : xs + (size_t)(r - N) * KB;
+    const int b = 16 * u;
+    u32x4 v = {0, 0, 0, 0};
+    if (b + 16 <= KB) {
+        __builtin_memcpy(&v, row + b, 16); // unaligned, which global loads allow
+    } else {
+        for (int i = b; i < KB; ++i) {
+            const uint32_t s = (uint32_t)row[i] << (8 * (i & 3));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) // no indexing by a variable: v stays in registers
+                v[e] |= (i - b) >> 2 == e ? s : 0u;
+        }
+    }
+    out[(size_t)u * rows + r] = v;
+}
+
+// A wave's outputs (n from nw, m from mw) through its part of LDS, 32 output
+// rows at a time: rows of 32 NB n are written as the accumulators hold them
+// (acc[i][k][4 g + e] is n = 32 i + 8 g + 4 h + e, m = 32 k + r) and read back
+// 16 bytes a lane, so a store covers whole runs of a row.  The LDS serves a
+// wave's accesses in order, and no other wave uses this part.
+template <class T, int DT>
+__device__ __forceinline__ void store_wave(const float16_t (&acc)[T::NB][T::MB], void *y, int M, int N,
+                                           int nw, int mw, uint8_t *stage)
+{
+    constexpr int ES = DT == DT_F32 ? 4 : 2, ROW = 32 * T::NB * ES, PITCH = ROW + 16;
+    constexpr int VECS = ROW / 16, RPI = 64 / VECS; // 16-byte pieces of a row; rows per instruction
+    static_assert(32 * PITCH <= T::WSTAGE && 64 % VECS == 0, "staging space");
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    const int n = nw + lane % VECS * (16 / ES);
+#pragma unroll
+    for (int k = 0; k < T::MB; ++k) {
+#pragma unroll
+        for (int i = 0; i < T::NB; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float4_t v{acc[i][k][4 * g], acc[i][k][4 * g + 1], acc[i][k][4 * g + 2],
+                                 acc[i][k][4 * g + 3]};
+                uint8_t *to = stage + r * PITCH + (32 * i + 8 * g + 4 * h) * ES;
+                if constexpr (DT == DT_F32)
+                    *reinterpret_cast<float4_t *>(to) = v;
+                else
+                    *reinterpret_cast<uint2 *>(to) =
+                        uint2{f32x2_to_act2<DT>(v[0], v[1]), f32x2_to_act2<DT>(v[2], v[3])};
+            }
+#pragma unroll
+        for (int q = 0; q < 32 / RPI; ++q) {
+            const int row = q * RPI + lane / VECS, m = mw + 32 * k + row;
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(stage + row * PITCH + lane % VECS * 16);
+            if (m < M && n < N) // N % 8 == 0: a piece is whole
+                *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(y) + ((size_t)m * N + n) * ES) = v;
+        }
+    }
+}
+
+// PACKED: ws holds the packed scales of weight rows, then activation rows; else
+// K % 128 == 0, so a row's scale bytes are whole dwords.
+template <class T, bool PACKED>
 __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
     const uint8_t *__restrict__ x, const uint8_t *__restrict__ xs, const uint8_t *__restrict__ w,
     const uint8_t *__restrict__ ws, void *__restrict__ y, int ydt, float *__restrict__ part, int M,
@@ -258,47 +342,62 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave % T::WN, wm = wave / T::WN;
-    const int KB = K >> 5, S = (KB + 7) >> 3;
+    const int KB = K >> 5, S = (KB + 15) >> 4; // blocks, spans of a row
     const int s_begin = (int)((int64_t)S * split / splits);
-    const int s_end = (int)((int64_t)S * (split + 1) / splits);
+    const int s_end = (int)((int64_t)S * (split + 1) / splits); // > s_begin: splits <= S
+    const int stages = 4 * (s_end - s_begin);
     const uint32_t rowb = (uint32_t)K >> 1;
+    constexpr int NS = T::NS, ND = T::ND;
+    constexpr int NSC = PACKED ? T::SROWS / 256 : T::ROWS / 64; // scale copies per wave and span
+    constexpr int ND0 = ND / 2; // code copies in a stage's first part
 
-    // Copy d of wave v fills LDS rows 8 (4 d + v) .. + 7: lane L the position
-    // L % 8 of row L / 8.  Rows past the matrix repeat its last row (never
-    // stored), pieces past the row its last piece (zeroed before use).
-    uint32_t row_at[T::ND];
+    // Code copy d of wave v fills LDS rows 16 (4 d + v) .. + 15: lane L the
+    // position L % 4 of row L / 4.  Rows past the matrix repeat its last row
+    // (never stored), pieces past the row its last piece (zeroed before use).
+    uint32_t row_at[ND];
 #pragma unroll
-    for (int d = 0; d < T::ND; ++d) {
-        const int R = 8 * (4 * d + wave) + (lane >> 3);
-        row_at[d] = (uint32_t)(32 * d < T::TN ? min(n0 + R, N - 1) : min(m0 + R - T::TN, M - 1)) * rowb;
+    for (int d = 0; d < ND; ++d) {
+        const int R = 16 * (4 * d + wave) + (lane >> 2);
+        row_at[d] = (uint32_t)(64 * d < T::TN ? min(n0 + R, N - 1) : min(m0 + R - T::TN, M - 1)) * rowb;
     }
-    const uint32_t piece = 16u * (uint32_t)((lane & 7) ^ ((lane >> 4) | ((wave & 1) << 2)));
+    static_assert(T::TN % 64 == 0, "a wave's copy has rows of one operand");
+    const uint32_t piece = 16u * (uint32_t)((lane & 3) ^ (lane >> 4));
     const uint32_t lds0 = (uint32_t)(size_t)(lds_ptr_t *)smem;
-    auto copy = [&](int d, int buf, uint32_t k) __attribute__((always_inline)) {
-        lds_dma16(32 * d < T::TN ? w : x, row_at[d] + k,
-                  lds0 + (uint32_t)(buf * T::BUF + (4 * d + wave) * 1024));
+    auto code_copy = [&](int t, int d) __attribute__((always_inline)) {
+        const int from = 4 * s_begin + min(t, stages - 1); // past the end: the last stage again
+        const uint32_t k = min((uint32_t)from * 64u + piece, rowb - 16u);
+        const uint32_t to = lds0 + (uint32_t)((t & (NS - 1)) * T::STAGE + wave * 1024);
+        lds_dma16(64 * d < T::TN ? w : x, row_at[d] + k, to + (uint32_t)(4096 * d));
     };
-    auto copy_at = [&](int span) { return min((uint32_t)span * 128u + piece, rowb - 16u); };
 
-    // Scales: thread t moves the eight bytes of rows t, t + 256.
-    const uint8_t *srow[T::SR];
+    // Scale copy i of wave v fills LDS scale rows 64 (4 i + v) .. + 63 (PACKED:
+    // lane L all 16 bytes of row L) or 16 (4 i + v) .. + 15 (lane L dword L % 4 of
+    // row L / 4, a dword past the row its last one: a finite scale or a NaN that
+    // the row's result has anyway).
+    constexpr int SC0 = NS * T::STAGE, SBUF = T::SROWS * 16;
+    uint32_t scale_at[NSC];
+    const uint32_t spr = (uint32_t)KB >> 2; // scale dwords per row
 #pragma unroll
-    for (int i = 0; i < T::SR; ++i) {
-        const int R = min(tid + 256 * i, T::ROWS - 1);
-        srow[i] = R < T::TN ? ws + (size_t)min(n0 + R, N - 1) * KB
-                            : xs + (size_t)min(m0 + R - T::TN, M - 1) * KB;
+    for (int i = 0; i < NSC; ++i) {
+        if constexpr (PACKED) {
+            const int R = 64 * (4 * i + wave) + lane;
+            scale_at[i] = 16u * (uint32_t)(R < T::TN ? min(n0 + R, N - 1) : N + min(m0 + R - T::TN, M - 1));
+        } else {
+            const int R = 16 * (4 * i + wave) + (lane >> 2);
+            scale_at[i] =
+                (uint32_t)(64 * i < T::TN ? min(n0 + R, N - 1) : min(m0 + R - T::TN, M - 1)) * (uint32_t)KB;
+        }
     }
-    uint2 *sl = reinterpret_cast<uint2 *>(smem + 2 * T::BUF);
-    auto scales_in = [&](int span, uint2 (&v)[T::SR]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < T::SR; ++i)
-            v[i] = scale8(srow[i], 8 * span, KB);
-    };
-    auto scales_out = [&](int buf, const uint2 (&v)[T::SR]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < T::SR; ++i)
-            if (T::ROWS % 256 == 0 || tid + 256 * i < T::ROWS)
-                sl[buf * T::ROWS + tid + 256 * i] = v[i];
+    auto scale_copy = [&](int u, int i) __attribute__((always_inline)) {
+        const int from = min(s_begin + u, s_end - 1);
+        const uint32_t to = lds0 + (uint32_t)(SC0 + (u & 1) * SBUF);
+        if constexpr (PACKED)
+            lds_dma16(ws + (size_t)from * (size_t)(N + M) * 16, scale_at[i],
+                      to + (uint32_t)(wave * 1024 + 4096 * i));
+        else
+            lds_dma4(64 * i < T::TN ? ws : xs,
+                     scale_at[i] + 4u * min(4u * (uint32_t)from + (uint32_t)(lane & 3), spr - 1u),
+                     to + (uint32_t)(wave * 256 + 1024 * i));
     };
 
     float16_t acc[T::NB][T::MB];
@@ -311,116 +410,160 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
                 acc[a][b][e] = 0.f;
 
     const int an = 32 * T::NB * wn + r, bm = T::TN + 32 * T::MB * wm + r; // this lane's first LDS rows
-    uint32_t at[4]; // position of piece 4 h + s in a row of this lane
+    uint32_t at[2]; // position of piece 2 h + j in a row of this lane
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-        at[s] = 16u * (uint32_t)((4 * h + s) ^ ((r >> 1) & 7));
+    for (int j = 0; j < 2; ++j)
+        at[j] = 16u * (uint32_t)((2 * h + j) ^ ((r >> 2) & 3));
 
-    auto operands = [&](int buf, int s, u32x4 (&a)[T::NB], u32x4 (&b)[T::MB]) __attribute__((always_inline)) {
-        const uint8_t *base = smem + buf * T::BUF + at[s];
-#pragma unroll
-        for (int i = 0; i < T::NB; ++i)
-            a[i] = *reinterpret_cast<const u32x4 *>(base + (an + 32 * i) * 128);
-#pragma unroll
-        for (int i = 0; i < T::MB; ++i)
-            b[i] = *reinterpret_cast<const u32x4 *>(base + (bm + 32 * i) * 128);
+    struct Operands {
+        u32x4 a[T::NB], b[T::MB];
+    };
+    constexpr int NR = T::NB + T::MB;
+    // operand i (weight blocks, then activation blocks) of step j of stage t
+    auto read_operand = [&](int t, int j, int i, Operands &o) __attribute__((always_inline)) {
+        const uint8_t *base = smem + (t & (NS - 1)) * T::STAGE + at[j];
+        if (i < T::NB)
+            o.a[i] = *reinterpret_cast<const u32x4 *>(base + (an + 32 * i) * 64);
+        else
+            o.b[i - T::NB] = *reinterpret_cast<const u32x4 *>(base + (bm + 32 * (i - T::NB)) * 64);
+    };
+    // A lane's scale bytes of span u, in step order.
+    struct Scales {
+        u32x4 v[NR];
+    };
+    const uint32_t pick = h ? 0x07060302u : 0x05040100u; // bytes 2 h, 2 h + 1 of both dwords
+    auto read_scale = [&](int u, int i, Scales &o) __attribute__((always_inline)) {
+        const u32x4 *base = reinterpret_cast<const u32x4 *>(smem + SC0 + (u & 1) * SBUF);
+        o.v[i] = base[i < T::NB ? an + 32 * i : bm + 32 * (i - T::NB)];
     };
 
-    if (s_begin < s_end) {
-        const uint32_t k = copy_at(s_begin);
+    Operands op[2];
+    Scales sc;
+    {
 #pragma unroll
-        for (int d = 0; d < T::ND; ++d)
-            copy(d, 0, k);
-        uint2 v[T::SR];
-        scales_in(s_begin, v);
-        scales_out(0, v);
-        __builtin_amdgcn_s_waitcnt(0);
+        for (int t = 0; t < NS - 1; ++t) {
+            if (t == 0)
+#pragma unroll
+                for (int i = 0; i < NSC; ++i)
+                    scale_copy(0, i);
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+                code_copy(t, d);
+        }
+#pragma unroll
+        for (int d = 0; d < ND0; ++d)
+            code_copy(NS - 1, d);
+        // stage 0 and the first scales have landed
+        wait_vmcnt<(NS - 2) * ND + ND0>();
         barrier_only();
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            read_scale(0, i, sc);
+            read_operand(0, 0, i, op[0]);
+        }
     }
-    auto run_span = [&](int span, auto tail) __attribute__((always_inline)) {
-        const int buf = (span - s_begin) & 1;
-        const int next = min(span + 1, s_end - 1); // the last span copies itself again
-        const uint32_t k = copy_at(next);
-        const int left = KB - 8 * span; // blocks of a partial span
-        uint32_t sa[T::NB], sb[T::MB];
+
+    // Span u of this part (stages 4 u .. 4 u + 3).  TAIL: the row's partial last
+    // span; nothing follows it.
+    auto run_span = [&](int u, auto tail) __attribute__((always_inline)) {
+        constexpr bool TAIL = decltype(tail)::value;
+        uint32_t sv8[2][NR]; // the scale bytes of each operand, in step order
 #pragma unroll
-        for (int i = 0; i < T::NB; ++i)
-            sa[i] = reinterpret_cast<const uint32_t *>(sl + buf * T::ROWS)[2 * (an + 32 * i) + h];
-#pragma unroll
-        for (int i = 0; i < T::MB; ++i)
-            sb[i] = reinterpret_cast<const uint32_t *>(sl + buf * T::ROWS)[2 * (bm + 32 * i) + h];
-        u32x4 a[2][T::NB], b[2][T::MB];
-        operands(buf, 0, a[0], b[0]);
-        uint2 sv[T::SR];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int c = s & 1;
-            if (s < 3)
-                operands(buf, s + 1, a[c ^ 1], b[c ^ 1]);
-#pragma unroll
-            for (int d = 0; d < T::ND; ++d)
-                if (d * 4 / T::ND == s)
-                    copy(d, buf ^ 1, k);
-            if (s == 3)
-                scales_in(next, sv);
-            if constexpr (decltype(tail)::value) { // blocks past the row: zero weights
-                const bool in = 4 * h + s < left;
+        for (int i = 0; i < NR; ++i) {
+            sv8[0][i] = __builtin_amdgcn_perm(sc.v[i][1], sc.v[i][0], pick);
+            sv8[1][i] = __builtin_amdgcn_perm(sc.v[i][3], sc.v[i][2], pick);
+        }
+        const int left = KB - 16 * (s_begin + u); // blocks of a partial span
+        auto step = [&](auto sel) __attribute__((always_inline)) {
+            constexpr int SEL = decltype(sel)::value, j = SEL & 1, p = SEL >> 1;
+            const int t = 4 * u + p;
+            Operands &now = op[j], &next = op[j ^ 1];
+            if constexpr (j == 1) {
+                // stage t + 1 has landed (and in the last stage the next span's
+                // scales, started in the first): the codes of stages t + 2 and
+                // t + 3 may be in flight, and the scales that were started among them
+                if constexpr (TAIL)
+                    wait_vmcnt<0>();
+                else
+                    wait_vmcnt<(NS - 2) * ND + (p == 1 || p == 2 ? NSC : 0)>();
+                __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0): this wave's reads of stage t
+                barrier_only();
+            }
+            if constexpr (TAIL) { // blocks past the row: zero weights
+                const bool in = 4 * p + 2 * h + j < left;
 #pragma unroll
                 for (int i = 0; i < T::NB; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        a[c][i][e] = in ? a[c][i][e] : 0u;
+                        now.a[i][e] = in ? now.a[i][e] : 0u;
             }
-            auto mul = [&](auto sel) __attribute__((always_inline)) {
-                constexpr int SEL = decltype(sel)::value;
-#pragma unroll
-                for (int i = 0; i < T::NB; ++i)
-#pragma unroll
-                    for (int j = 0; j < T::MB; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                            fp4_operand(a[c][i]), fp4_operand(b[c][j]), acc[i][j], FMT_FP4, FMT_FP4,
-                            SEL, (int)sa[i], SEL, (int)sb[j]);
-            };
-            if (s == 0)
-                mul(std::integral_constant<int, 0>{});
-            else if (s == 1)
-                mul(std::integral_constant<int, 1>{});
-            else if (s == 2)
-                mul(std::integral_constant<int, 2>{});
-            else
-                mul(std::integral_constant<int, 3>{});
-        }
-        scales_out(buf ^ 1, sv);
-        __builtin_amdgcn_s_waitcnt(0); // the copies and the scales of the next span are in LDS
-        barrier_only();
-    };
-    const int full = KB & 7 ? min(s_end, S - 1) : s_end; // spans before a row's partial last one
-    for (int span = s_begin; span < full; ++span)
-        run_span(span, std::false_type{});
-    if (full < s_end)
-        run_span(full, std::true_type{});
-
-    // acc[i][j][4 g + e] is n = 32 i + 8 g + 4 h + e of the wave's rows, m = 32 j + r
-#pragma unroll
-    for (int j = 0; j < T::MB; ++j) {
-        const int m = m0 + bm - T::TN + 32 * j;
-        if (m >= M)
-            continue;
-#pragma unroll
-        for (int i = 0; i < T::NB; ++i)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int n = n0 + 32 * (T::NB * wn + i) + 8 * g + 4 * h;
-                const float4_t v{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
-                                 acc[i][j][4 * g + 3]};
-                if (n >= N)
-                    continue;
-                if (splits > 1)
-                    *reinterpret_cast<float4_t *>(part + ((size_t)split * M + m) * N + n) = v;
+            // The step's other work, one piece at a time between the MFMAs: the
+            // next step's operands, (SEL 7) the next span's scales, then copies.
+            // In the partial last span only the rest of its own fourth stage is
+            // still to be copied.
+            constexpr bool LAST = TAIL && SEL != 0;
+            constexpr int C0 = j == 0 ? ND0 : 0, C1 = j == 0 ? ND : ND0;
+            constexpr int RS = SEL == 7 && !TAIL ? NR : 0, SCC = SEL == 1 && !TAIL ? NSC : 0;
+            constexpr int SIDE = NR + RS + SCC + (LAST ? 0 : C1 - C0), NM = T::NB * T::MB;
+            auto side = [&](int i) __attribute__((always_inline)) {
+                if (i < NR)
+                    read_operand(t + j, j ^ 1, i, next);
+                else if (i < NR + RS)
+                    read_scale(u + 1, i - NR, sc);
+                else if (i < NR + RS + SCC)
+                    scale_copy(u + 1, i - NR - RS);
                 else
-                    store4(y, ydt, (size_t)m * N + n, v);
+                    code_copy(j == 0 ? t + NS - 1 : t + NS, C0 + i - NR - RS - SCC);
+            };
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                const int i = m / T::MB, k = m % T::MB;
+                __builtin_amdgcn_sched_barrier(0);
+                acc[i][k] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    fp4_operand(now.a[i]), fp4_operand(now.b[k]), acc[i][k], FMT_FP4, FMT_FP4, SEL & 3,
+                    (int)sv8[SEL >> 2][i], SEL & 3, (int)sv8[SEL >> 2][T::NB + k]);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int q = 0; q < SIDE; ++q)
+                    if (q >= m * SIDE / NM && q < (m + 1) * SIDE / NM)
+                        side(q);
             }
-    }
+        };
+        step(std::integral_constant<int, 0>{});
+        step(std::integral_constant<int, 1>{});
+        if (TAIL && left <= 4)
+            return; // (the same for the whole workgroup)
+        step(std::integral_constant<int, 2>{});
+        step(std::integral_constant<int, 3>{});
+        if (TAIL && left <= 8)
+            return;
+        step(std::integral_constant<int, 4>{});
+        step(std::integral_constant<int, 5>{});
+        if (TAIL && left <= 12)
+            return;
+        step(std::integral_constant<int, 6>{});
+        step(std::integral_constant<int, 7>{});
+    };
+    const int full = (KB & 15 ? min(s_end, S - 1) : s_end) - s_begin;
+    for (int u = 0; u < full; ++u)
+        run_span(u, std::false_type{});
+    if (full < s_end - s_begin)
+        run_span(full, std::true_type{});
+    wait_vmcnt<0>(); // copies past the end: none is in flight when the workgroup ends
+
+    // Every wave has read its last operands (the barrier of the last stage came
+    // before them, so one more): the stage buffers become staging space.
+    barrier_only();
+    uint8_t *stage = smem + wave * T::WSTAGE;
+    if (splits > 1)
+        store_wave<T, DT_F32>(acc, part + (size_t)split * M * N, M, N, n0 + 32 * T::NB * wn,
+                              m0 + 32 * T::MB * wm, stage);
+    else if (ydt == DT_F32)
+        store_wave<T, DT_F32>(acc, y, M, N, n0 + 32 * T::NB * wn, m0 + 32 * T::MB * wm, stage);
+    else if (ydt == DT_F16)
+        store_wave<T, DT_F16>(acc, y, M, N, n0 + 32 * T::NB * wn, m0 + 32 * T::MB * wm, stage);
+    else
+        store_wave<T, DT_BF16>(acc, y, M, N, n0 + 32 * T::NB * wn, m0 + 32 * T::MB * wm, stage);
 }
 
 // y = the sum of the K parts, in part order.
@@ -437,14 +580,19 @@ __global__ __launch_bounds__(256) void mxfp4_sum_kernel(const float4_t *__restri
     store4(y, ydt, (size_t)i * 4, v);
 }
 
+size_t parts_bytes(int64_t M, int64_t N, int splits)
+{
+    return splits > 1 ? (size_t)splits * (size_t)M * (size_t)N * sizeof(float) : 0; // N % 8 == 0
+}
+
 template <class T>
 hipError_t launch_tile(const uint8_t *x, const uint8_t *xs, const uint8_t *w, const uint8_t *ws,
-                       void *y, int ydt, int M, int N, int K, int splits, void *workspace,
+                       void *y, int ydt, int M, int N, int K, int splits, bool packed, void *workspace,
                        hipStream_t stream)
 {
-    auto kern = mxfp4_tile_kernel<T>;
-    static std::atomic<uint64_t> lds_set{0};
-    if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), T::LDS, lds_set);
+    auto kern = packed ? mxfp4_tile_kernel<T, true> : mxfp4_tile_kernel<T, false>;
+    static std::atomic<uint64_t> lds_set[2];
+    if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), T::LDS, lds_set[packed]);
         e != hipSuccess)
         return e;
     const int tiles_m = (M + T::TM - 1) / T::TM;
@@ -454,6 +602,16 @@ hipError_t launch_tile(const uint8_t *x, const uint8_t *xs, const uint8_t *w, co
     if (grid > INT32_MAX / 256)
         return hipErrorInvalidValue;
     float *part = static_cast<float *>(workspace);
+    if (packed) {
+        uint8_t *scales = static_cast<uint8_t *>(workspace) + parts_bytes(M, N, splits);
+        const int spans = (K + MX_SPAN - 1) / MX_SPAN;
+        hipLaunchKernelGGL(mxfp4_pack_scales_kernel,
+                           dim3((unsigned)(((int64_t)(M + N) * spans + 255) / 256)), dim3(256), 0, stream,
+                           ws, xs, reinterpret_cast<u32x4 *>(scales), N, M, K >> 5, spans);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+        ws = scales;
+    }
     hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), (size_t)T::LDS, stream, x, xs, w, ws, y,
                        ydt, part, M, N, K, tiles_m, (int)tiles, splits, nxcd);
     hipError_t e = hipGetLastError();
@@ -465,35 +623,50 @@ hipError_t launch_tile(const uint8_t *x, const uint8_t *xs, const uint8_t *w, co
     return hipGetLastError();
 }
 
-using TileL = MxTile<2, 4, 4>; // 256 x 256
-using TileS = MxTile<2, 1, 2>; // 64 weight rows x 128 activation rows
+using TileL = MxTile<2, 4, 4, 4>; // 256 x 256
+using TileS = MxTile<2, 1, 2, 4>; // 64 weight rows x 128 activation rows
 
 bool few_rows(int64_t M, int64_t K) { return M <= 16 && (16 + M) * (K >> 5) <= 64 * 1024; }
 bool large_tile(int64_t M, int64_t N) { return ((M + 255) / 256) * ((N + 255) / 256) >= 128; }
 
-// K parts so that about two workgroups reach each CU, at least four spans each.
-int split_count(int64_t M, int64_t N, int64_t K)
+struct Plan {
+    bool few, large, packed;
+    int splits;
+};
+
+Plan plan(int64_t M, int64_t N, int64_t K)
 {
-    if (few_rows(M, K) || large_tile(M, N))
-        return 1;
-    const int64_t tiles = ((M + TileS::TM - 1) / TileS::TM) * ((N + TileS::TN - 1) / TileS::TN);
-    const int64_t spans = (K + MX_SPAN - 1) / MX_SPAN;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, spans / 4, 16}));
+    Plan p;
+    p.few = few_rows(M, K);
+    p.large = !p.few && large_tile(M, N);
+    p.packed = !p.few && (p.large || K % 128 != 0);
+    p.splits = 1;
+    if (!p.few && !p.large) {
+        // K parts so that about two workgroups reach each CU, at least two spans each
+        const int64_t tiles = ((M + TileS::TM - 1) / TileS::TM) * ((N + TileS::TN - 1) / TileS::TN);
+        const int64_t spans = (K + MX_SPAN - 1) / MX_SPAN;
+        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, spans / 2, 16}));
+    }
+    return p;
 }
 
 } // namespace
 
 size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
-    const int s = split_count(M, N, K);
-    return s > 1 ? (size_t)s * (size_t)M * (size_t)N * sizeof(float) : 0;
+    if (M == 0 || N == 0)
+        return 0;
+    const Plan p = plan(M, N, K);
+    const int64_t spans = (K + MX_SPAN - 1) / MX_SPAN;
+    return parts_bytes(M, N, p.splits) + (p.packed ? (size_t)(M + N) * (size_t)spans * 16 : 0);
 }
 
 hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t *w,
                              const uint8_t *ws, void *y, int ydt, int M, int N, int K,
                              void *workspace, hipStream_t stream)
 {
-    if (few_rows(M, K)) {
+    const Plan p = plan(M, N, K);
+    if (p.few) {
         // waves per workgroup: about 16 per CU in all, at least four steps each
         const int64_t groups = (N + FR_ROWS - 1) / FR_ROWS, steps = (K + 127) / 128;
         if (groups * 8 <= 4096 && steps >= 64)
@@ -502,9 +675,9 @@ hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t 
             return launch_few<1, 8>(x, xs, w, ws, y, ydt, M, N, K, stream);
         return launch_few<1, 4>(x, xs, w, ws, y, ydt, M, N, K, stream);
     }
-    if (large_tile(M, N))
-        return launch_tile<TileL>(x, xs, w, ws, y, ydt, M, N, K, 1, workspace, stream);
-    return launch_tile<TileS>(x, xs, w, ws, y, ydt, M, N, K, split_count(M, N, K), workspace, stream);
+    if (p.large)
+        return launch_tile<TileL>(x, xs, w, ws, y, ydt, M, N, K, 1, p.packed, workspace, stream);
+    return launch_tile<TileS>(x, xs, w, ws, y, ydt, M, N, K, p.splits, p.packed, workspace, stream);
 }
 
 } // namespace wob
