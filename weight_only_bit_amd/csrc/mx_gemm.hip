@@ -9,8 +9,8 @@
 // instruction is free as long as both operands agree.
 //
 // Two kernels:
-//  * few rows (M <= 16 MT): a workgroup owns 16 weight rows and its waves split
-//    K; codes go from memory straight into registers
+//  * few rows (M <= 16): waves own 16 weight rows each and may split K; the
+//    weights' codes go from memory straight into registers
 //    (v_mfma_scale_f32_16x16x128_f8f6f4); bound by the weights' bytes.
 //  * tiles: both operands through LDS (v_mfma_scale_f32_32x32x64_f8f6f4), K
 //    optionally split over workgroups with an fp32 sum in a second kernel.
@@ -49,94 +49,118 @@ __device__ __forceinline__ void store4(void *y, int ydt, size_t at, const float4
 
 // ---- Few rows --------------------------------------------------------------
 //
-// Workgroup: 16 weight rows; wave v of W takes the K steps j = v, v + W, ...
-// (128 k: lane (r, q) = (lane % 16, lane / 16) holds block 4 j + q of row r),
-// so the waves of a workgroup read neighbouring 64-byte pieces of the same
-// lines.  A lane's codes stream through a ring of FR_D slots.  The scale bytes
-// of the 16 weight rows are one contiguous stretch of memory (as are those of
-// the M activation rows): they are copied to LDS once, after the first loads
-// are under way.
+// M <= 16.  A wave owns 16 weight rows; W waves share them and split K, in pairs
+// of steps of 128 k (in a step lane (r, q) = (lane % 16, lane / 16) holds block
+// 4 j + q of row r, so a pair is one whole cache line of each row), and their
+// sums are joined in LDS.  A workgroup has G such groups of rows.  The weights'
+// codes go from memory into registers, FR_D loads of a lane ahead; only the x
+// operand and the scales pass through LDS: the activation rows (pitch 16 mod 128
+// bytes, which makes their reads conflict-free) and the scale bytes, each of them
+// one contiguous stretch of memory, copied once, with their loads ahead of the
+// codes' so that they land first.
+//
+// Bound by the weights' bytes.  Measured (graph replay over copies larger than
+// the caches, us; 1 x 16384 x 5376 / 1 x 43008 x 5376 / 1 x 5376 x 21504 / 16 x
+// 16384 x 5376 / 13 x 5760 x 2880 / 4 x 2048 x 2048):
+//   x straight from memory, W = 8, G = 1      14.9 / 28.2 / 21.0 / 20.6 / 6.6 / 3.5
+//   W = 8, G = 2, single steps, nontemporal   13.9 / 35.4 / 19.4 / 15.7 / 7.7 / 6.2
+//   W = 8, G = 2, pairs, ring of 8            11.1 / 26.3 / 16.8 / 13.2 / 4.7 / 5.7
+//   W = 8, G = 2, pairs, ring of 6            10.2 / 23.4 / 17.0 / 12.0 / 4.3 / 5.1
+//   W = 4, G = 1, pairs, ring of 4            10.5 / 24.1 / 20.1 / 20.8 / 5.0 / 2.9
+// (a plain read of the first shape's 47 MB takes 8.4).  Nontemporal loads gave up
+// the other half of a line; rings of 4 and 12 were no better than 6.
 constexpr int FR_ROWS = 16;
-constexpr int FR_D = 4;
+constexpr int FR_D = 6;  // loads ahead
+constexpr int FR_CH = 2; // neighbouring steps of a wave
 
-template <int MT>
-struct FewSlot {
-    u32x4 w, x[MT];
-};
-
-template <int MT, int W>
-__global__ __launch_bounds__(64 * W) void mxfp4_few_kernel(const uint8_t *__restrict__ x,
-                                                           const uint8_t *__restrict__ xs,
-                                                           const uint8_t *__restrict__ w,
-                                                           const uint8_t *__restrict__ ws,
-                                                           void *__restrict__ y, int ydt, int M,
-                                                           int N, int K)
+__host__ __device__ inline int few_pitch(int K) { return (K / 2 + 127 - 16) / 128 * 128 + 16; }
+__host__ __device__ inline size_t few_scales_at(int M, int K) { return (size_t)M * few_pitch(K); }
+inline size_t few_lds(int M, int K, int W, int G)
 {
+    const size_t staged = few_scales_at(M, K) + (((size_t)M * (K >> 5) + 15) & ~(size_t)15) +
+                          (size_t)G * FR_ROWS * (K >> 5);
+    const size_t sums = W > 1 ? (size_t)W * G * 1024 : 0;
+    return (std::max(staged, sums) + 15) & ~(size_t)15;
+}
+
+template <int W, int G>
+__global__ __launch_bounds__(64 * W * G) void mxfp4_few_kernel(const uint8_t *__restrict__ x,
+                                                               const uint8_t *__restrict__ xs,
+                                                               const uint8_t *__restrict__ w,
+                                                               const uint8_t *__restrict__ ws,
+                                                               void *__restrict__ y, int ydt, int M,
+                                                               int N, int K)
+{
+    constexpr int NT = 64 * W * G;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = blockIdx.x * FR_ROWS;
-    const int KB = K >> 5, steps = (KB + 3) >> 2;
-    const int rows = min(FR_ROWS, N - n0);
-    const u32x4 *wr = reinterpret_cast<const u32x4 *>(w) + (size_t)(n0 + min(r, rows - 1)) * KB;
-    const u32x4 *xr[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        xr[t] = reinterpret_cast<const u32x4 *>(x) + (size_t)min(16 * t + r, M - 1) * KB;
-    const int mine = (steps - wave + W - 1) / W; // steps of this wave
-    auto load = [&](int i, FewSlot<MT> &s) __attribute__((always_inline)) {
-        int b = min(4 * (wave + W * i) + q, KB - 1);
-        asm volatile("" : "+v"(b)); // one address per slot, not one pointer kept per slot
-        s.w = __builtin_nontemporal_load(wr + b);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-            s.x[t] = xr[t][b];
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), k = wave % W, g = wave / W;
+    const int KB = K >> 5, steps = (KB + 3) >> 2, pitch = few_pitch(K);
+    const int nw = blockIdx.x * FR_ROWS * G, n0 = nw + FR_ROWS * g;
+    const int rows = min(FR_ROWS * G, N - nw); // of the workgroup
+    uint8_t *const xsl = smem + few_scales_at(M, K);
+    uint8_t *const wsl = xsl + ((M * KB + 15) & ~15);
+
+    // Staging, 16 bytes a thread (8 for the weights' scales: N % 8 == 0; 4 and
+    // single bytes for x's), the first round's loads ahead of the codes'.
+    const int nx = M * KB, nws = rows * KB >> 3, nxs = nx >> 2;
+    const u32x4 *xg = reinterpret_cast<const u32x4 *>(x);
+    const uint64_t *wsg = reinterpret_cast<const uint64_t *>(ws + (size_t)nw * KB);
+    const uint32_t *xsg = reinterpret_cast<const uint32_t *>(xs);
+    const u32x4 x_first = xg[min(tid, nx - 1)];
+    const uint64_t ws_first = wsg[min(tid, nws - 1)];
+    const uint32_t xs_first = nxs ? xsg[min(tid, nxs - 1)] : 0u;
+
+    const u32x4 *wr = reinterpret_cast<const u32x4 *>(w) + (size_t)min(n0 + r, N - 1) * KB;
+    const int mine = FR_CH * (((steps + FR_CH - 1) / FR_CH - k + W - 1) / W); // steps of this wave
+    auto block = [&](int i) __attribute__((always_inline)) { // this lane's in step i
+        return 4 * (FR_CH * (k + W * (i / FR_CH)) + i % FR_CH) + q;
     };
-    FewSlot<MT> ring[FR_D];
+    u32x4 ring[FR_D];
+    auto load = [&](int i, u32x4 &s) __attribute__((always_inline)) {
+        int b = min(block(i), KB - 1);
+        asm volatile("" : "+v"(b)); // one address per load, not one pointer kept per slot
+        s = wr[b];
+    };
 #pragma unroll
     for (int d = 0; d < FR_D; ++d)
         load(min(d, max(mine - 1, 0)), ring[d]);
-    // scale bytes: 8-byte units (N % 8 == 0) of the weight rows, bytes of x
-    {
-        const uint64_t *src = reinterpret_cast<const uint64_t *>(ws + (size_t)n0 * KB);
-        uint64_t *dst = reinterpret_cast<uint64_t *>(smem);
-        for (int i = tid; i < rows * KB / 8; i += 64 * W)
-            dst[i] = src[i];
-        uint8_t *xd = smem + FR_ROWS * KB;
-        const int nb = M * KB, nd = nb >> 2;
-        for (int i = tid; i < nd; i += 64 * W)
-            reinterpret_cast<uint32_t *>(xd)[i] = reinterpret_cast<const uint32_t *>(xs)[i];
-        if (tid < (nb & 3))
-            xd[4 * nd + tid] = xs[4 * nd + tid];
-    }
+    __builtin_amdgcn_sched_barrier(0);
+
+    auto put_x = [&](int i, const u32x4 &v) __attribute__((always_inline)) {
+        const int m = M == 1 ? 0 : i / KB; // uniform
+        *reinterpret_cast<u32x4 *>(smem + (size_t)m * pitch + (size_t)(i - m * KB) * 16) = v;
+    };
+    if (tid < nx)
+        put_x(tid, x_first);
+    if (tid < nws)
+        reinterpret_cast<uint64_t *>(wsl)[tid] = ws_first;
+    if (tid < nxs)
+        reinterpret_cast<uint32_t *>(xsl)[tid] = xs_first;
+    for (int i = tid + NT; i < nx; i += NT)
+        put_x(i, xg[i]);
+    for (int i = tid + NT; i < nws; i += NT)
+        reinterpret_cast<uint64_t *>(wsl)[i] = wsg[i];
+    for (int i = tid + NT; i < nxs; i += NT)
+        reinterpret_cast<uint32_t *>(xsl)[i] = xsg[i];
+    if (tid < (nx & 3))
+        xsl[4 * nxs + tid] = xs[4 * nxs + tid];
     __syncthreads();
-    const uint8_t *wsl = smem + min(r, rows - 1) * KB;
-    const uint8_t *xsl[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        xsl[t] = smem + FR_ROWS * KB + min(16 * t + r, M - 1) * KB;
-    float4_t acc[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
-    auto multiply = [&](int i, const FewSlot<MT> &s) __attribute__((always_inline)) {
-        const int b = 4 * (wave + W * i) + q;
-        const bool in = b < KB; // the last step may leave some lanes without a block
+
+    const uint8_t *wrow = wsl + (min(n0 + r, N - 1) - nw) * KB;
+    const uint8_t *xrow = smem + (size_t)min(r, M - 1) * pitch, *xsrow = xsl + min(r, M - 1) * KB;
+    float4_t acc{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](int i, u32x4 wv) __attribute__((always_inline)) {
+        const int b = block(i);
+        const bool in = b < KB; // the last steps may leave some lanes without a block
         const int bc = in ? b : KB - 1;
-        u32x4 wv = s.w;
-        uint32_t sw = wsl[bc];
-        if (!in) {
-            wv = u32x4{0, 0, 0, 0};
-            sw = 127u;
-        }
+        const u32x4 xv = *reinterpret_cast<const u32x4 *>(xrow + 16 * bc);
+        const int sw = wrow[bc], sx = xsrow[bc]; // (the row's own: a NaN there is the result's)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            uint32_t sx = xsl[t][bc];
-            sx = in ? sx : 127u;
-            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                fp4_operand(wv), fp4_operand(s.x[t]), acc[t], FMT_FP4, FMT_FP4, 0, (int)sw, 0,
-                (int)sx);
-        }
+        for (int e = 0; e < 4; ++e)
+            wv[e] = in ? wv[e] : 0u;
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(wv), fp4_operand(xv), acc,
+                                                               FMT_FP4, FMT_FP4, 0, sw, 0, sx);
     };
     int i = 0;
     for (; i + FR_D < mine; i += FR_D) {
@@ -153,44 +177,35 @@ __global__ __launch_bounds__(64 * W) void mxfp4_few_kernel(const uint8_t *__rest
     for (int d = 0; d < FR_D; ++d)
         if (i + d < mine)
             multiply(i + d, ring[d]);
-    // Sum over the waves in wave order.  Lane (r, q) holds n = 4 q + e of
-    // output row 16 t + r in acc[t][e].
-    __syncthreads();
-    float4_t *part = reinterpret_cast<float4_t *>(smem);
+    // Lane (r, q) holds n = 4 q + e of output row r in acc[e]; the waves of a
+    // group are summed in order.
+    if constexpr (W > 1) {
+        __syncthreads();
+        float4_t *part = reinterpret_cast<float4_t *>(smem);
+        part[wave * 64 + lane] = acc;
+        __syncthreads();
+        if (k != 0)
+            return;
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-        part[(wave * MT + t) * 64 + lane] = acc[t];
-    __syncthreads();
-    for (int o = tid; o < 64 * MT; o += 64 * W) {
-        float4_t v = part[o];
-#pragma unroll
-        for (int k = 1; k < W; ++k)
-            v += part[k * MT * 64 + o];
-        const int m = 16 * (o >> 6) + (o & 15), n = 4 * ((o >> 4) & 3);
-        if (m < M && n < rows)
-            store4(y, ydt, (size_t)m * N + n0 + n, v);
+        for (int j = 1; j < W; ++j)
+            acc += part[(wave + j) * 64 + lane];
     }
+    const int n = n0 + 4 * q;
+    if (r < M && n < N)
+        store4(y, ydt, (size_t)r * N + n, acc);
 }
 
-template <int MT, int W>
-size_t few_lds(int M, int K)
-{
-    const size_t scales = (size_t)(FR_ROWS + M) * (K >> 5), sums = (size_t)W * MT * 1024;
-    return (std::max(scales, sums) + 15) & ~(size_t)15;
-}
-
-template <int MT, int W>
+template <int W, int G>
 hipError_t launch_few(const uint8_t *x, const uint8_t *xs, const uint8_t *w, const uint8_t *ws,
                       void *y, int ydt, int M, int N, int K, hipStream_t stream)
 {
-    auto kern = mxfp4_few_kernel<MT, W>;
+    auto kern = mxfp4_few_kernel<W, G>;
     static std::atomic<uint64_t> lds_set{0};
-    const size_t lds = few_lds<MT, W>(M, K);
     if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), 160 * 1024, lds_set);
         e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(kern, dim3((N + FR_ROWS - 1) / FR_ROWS), dim3(64 * W), lds, stream, x, xs, w,
-                       ws, y, ydt, M, N, K);
+    hipLaunchKernelGGL(kern, dim3((N + FR_ROWS * G - 1) / (FR_ROWS * G)), dim3(64 * W * G),
+                       few_lds(M, K, W, G), stream, x, xs, w, ws, y, ydt, M, N, K);
     return hipGetLastError();
 }
 
@@ -626,7 +641,8 @@ hipError_t launch_tile(const uint8_t *x, const uint8_t *xs, const uint8_t *w, co
 using TileL = MxTile<2, 4, 4, 4>; // 256 x 256
 using TileS = MxTile<2, 1, 2, 4>; // 64 weight rows x 128 activation rows
 
-bool few_rows(int64_t M, int64_t K) { return M <= 16 && (16 + M) * (K >> 5) <= 64 * 1024; }
+// Rows and scales of x must leave the LDS room for a second workgroup.
+bool few_rows(int64_t M, int64_t K) { return M <= 16 && K <= 65536 && few_lds((int)M, (int)K, 8, 2) <= 80 * 1024; }
 bool large_tile(int64_t M, int64_t N) { return ((M + 255) / 256) * ((N + 255) / 256) >= 128; }
 
 struct Plan {
@@ -667,13 +683,15 @@ hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t 
 {
     const Plan p = plan(M, N, K);
     if (p.few) {
-        // waves per workgroup: about 16 per CU in all, at least four steps each
-        const int64_t groups = (N + FR_ROWS - 1) / FR_ROWS, steps = (K + 127) / 128;
-        if (groups * 8 <= 4096 && steps >= 64)
-            return launch_few<1, 16>(x, xs, w, ws, y, ydt, M, N, K, stream);
-        if (groups * 4 <= 4096 && steps >= 32)
-            return launch_few<1, 8>(x, xs, w, ws, y, ydt, M, N, K, stream);
-        return launch_few<1, 4>(x, xs, w, ws, y, ydt, M, N, K, stream);
+        // Eight waves on a group of rows and two groups where that still makes 128
+        // workgroups; with fewer rows one group each (2048 x 2048: 5.1 us with two
+        // groups, 2.9 with one), four waves if K leaves them no more than a few steps.
+        const int groups = (N + FR_ROWS - 1) / FR_ROWS;
+        if (groups >= 256)
+            return launch_few<8, 2>(x, xs, w, ws, y, ydt, M, N, K, stream);
+        if (K >= 4096)
+            return launch_few<8, 1>(x, xs, w, ws, y, ydt, M, N, K, stream);
+        return launch_few<4, 1>(x, xs, w, ws, y, ydt, M, N, K, stream);
     }
     if (p.large)
         return launch_tile<TileL>(x, xs, w, ws, y, ydt, M, N, K, 1, p.packed, workspace, stream);
