@@ -7,37 +7,46 @@ namespace wob {
 
 namespace {
 
-constexpr int CH_WAVES = 4;
+constexpr int CH_THREADS = 256;
 
-template <int DT, int V>
-__global__ __launch_bounds__(64 * CH_WAVES) void moe_topk_kernel(
+template <int DT, int L, int V>
+__global__ __launch_bounds__(CH_THREADS) void moe_topk_kernel(
     const void *__restrict__ logits, const float *__restrict__ bias, int32_t *__restrict__ ids,
     float *__restrict__ weights, int T, int E, int topk, bool renormalize)
 {
-    const int t = blockIdx.x * CH_WAVES + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int t = blockIdx.x * (CH_THREADS / L) + threadIdx.x / L, g = threadIdx.x % L;
+    int id[CHOICE_MAX / L];
+    float w[CHOICE_MAX / L];
+    choose<DT, L, V>(logits, (int64_t)t * E, bias, t < T ? E : 0, topk, renormalize, g, id, w);
     if (t >= T)
         return;
-    int id;
-    float w;
-    choose_wave<DT, V>(logits, (int64_t)t * E, bias, E, topk, renormalize, id, w);
-    if (lane < topk) {
-        ids[(int64_t)t * topk + lane] = id;
-        weights[(int64_t)t * topk + lane] = w;
-    }
+#pragma unroll
+    for (int j = 0; j < CHOICE_MAX / L; ++j)
+        if (j * L + g < topk) {
+            ids[(int64_t)t * topk + j * L + g] = id[j];
+            weights[(int64_t)t * topk + j * L + g] = w[j];
+        }
 }
 
-template <int DT, int V>
+template <int DT, int L, int V>
 hipError_t launch_topk_v(const void *logits, const float *bias, int32_t *ids, float *weights, int T,
                          int E, int topk, bool renormalize, hipStream_t stream)
 {
-    if constexpr (V < 64) {
-        if (E > 64 * V)
-            return launch_topk_v<DT, 2 * V>(logits, bias, ids, weights, T, E, topk, renormalize,
+    // 16 lanes a token up to 256 experts, a whole wave beyond
+    if (E > L * V) {
+        if constexpr (L == 16 && V < 16)
+            return launch_topk_v<DT, 16, 2 * V>(logits, bias, ids, weights, T, E, topk, renormalize,
+                                                stream);
+        else if constexpr (L == 16)
+            return launch_topk_v<DT, 64, 8>(logits, bias, ids, weights, T, E, topk, renormalize,
                                             stream);
+        else if constexpr (V < 64)
+            return launch_topk_v<DT, 64, 2 * V>(logits, bias, ids, weights, T, E, topk, renormalize,
+                                                stream);
     }
-    hipLaunchKernelGGL((moe_topk_kernel<DT, V>), dim3((T + CH_WAVES - 1) / CH_WAVES),
-                       dim3(64 * CH_WAVES), 0, stream, logits, bias, ids, weights, T, E, topk,
-                       renormalize);
+    constexpr int PER = CH_THREADS / L; // tokens per workgroup
+    hipLaunchKernelGGL((moe_topk_kernel<DT, L, V>), dim3((T + PER - 1) / PER), dim3(CH_THREADS), 0,
+                       stream, logits, bias, ids, weights, T, E, topk, renormalize);
     return hipGetLastError();
 }
 
@@ -76,11 +85,11 @@ hipError_t launch_moe_topk(const void *logits, int dt, const float *bias, int32_
                            hipStream_t stream)
 {
     if (dt == DT_F16)
-        return launch_topk_v<DT_F16, 1>(logits, bias, ids, weights, T, E, topk, renormalize, stream);
+        return launch_topk_v<DT_F16, 16, 1>(logits, bias, ids, weights, T, E, topk, renormalize, stream);
     if (dt == DT_BF16)
-        return launch_topk_v<DT_BF16, 1>(logits, bias, ids, weights, T, E, topk, renormalize,
+        return launch_topk_v<DT_BF16, 16, 1>(logits, bias, ids, weights, T, E, topk, renormalize,
                                          stream);
-    return launch_topk_v<DT_F32, 1>(logits, bias, ids, weights, T, E, topk, renormalize, stream);
+    return launch_topk_v<DT_F32, 16, 1>(logits, bias, ids, weights, T, E, topk, renormalize, stream);
 }
 
 size_t moe_layer_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
