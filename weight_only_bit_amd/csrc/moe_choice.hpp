@@ -34,13 +34,11 @@ __device__ __forceinline__ float order_value(uint32_t k)
 }
 constexpr uint32_t KEY_NEG_INF = 0x007FFFFFu; // order_key(-inf); 0 is below every float
 
-template <int DT>
-__device__ __forceinline__ float logit_value(const void *p, int64_t at)
+__device__ __forceinline__ float logit_value(const void *p, int dt, int64_t at)
 {
-    if constexpr (DT == DT_F32)
+    if (dt == DT_F32)
         return static_cast<const float *>(p)[at];
-    else
-        return act_to_f32<DT>(static_cast<const uint16_t *>(p)[at]);
+    return act_to_f32(static_cast<const uint16_t *>(p)[at], dt);
 }
 
 __device__ __forceinline__ float exp_below(float l, float top)
@@ -65,13 +63,14 @@ __device__ __forceinline__ uint32_t group_reduce(uint32_t v, F f)
 
 constexpr int CHOICE_MAX = 64; // places of a token, at most
 
-// One group of L lanes (g: the lane's place in it) chooses for one token.  On
-// return lane g holds places g, g + L, ... in id[] and weight[].  Every lane of
-// the wave calls it with the same topk (a group without a token passes E = 0).
-template <int DT, int L, int V>
-__device__ __forceinline__ void choose(const void *logits, int64_t row, const float *bias, int E,
-                                       int topk, bool renormalize, int g, int (&id)[CHOICE_MAX / L],
-                                       float (&weight)[CHOICE_MAX / L])
+// One group of L lanes (g: the lane's place in it) chooses for one token, whose
+// scores begin at `row`.  On return lane g holds places g, g + L, ... in id[] and
+// weight[].  Every lane of the wave calls it with the same topk (a group without
+// a token passes E = 0).
+template <int L, int V>
+__device__ __forceinline__ void choose(const void *logits, int dt, int64_t row, const float *bias,
+                                       int E, int topk, bool renormalize, int g,
+                                       int (&id)[CHOICE_MAX / L], float (&weight)[CHOICE_MAX / L])
 {
     auto umax = [](uint32_t a, uint32_t b) { return max(a, b); };
     auto umin = [](uint32_t a, uint32_t b) { return min(a, b); };
@@ -84,7 +83,7 @@ __device__ __forceinline__ void choose(const void *logits, int64_t row, const fl
         const int e = v * L + g;
         float l = 0.f;
         if (e < E) {
-            l = logit_value<DT>(logits, row + e) + (bias ? bias[e] : 0.0f);
+            l = logit_value(logits, dt, row + e) + (bias ? bias[e] : 0.0f);
             l = l != l ? -__builtin_inff() : l;
         }
         key[v] = e < E ? order_key(l) : 0u;
