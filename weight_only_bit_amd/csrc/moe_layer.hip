@@ -56,78 +56,156 @@ hipError_t launch_topk_v(const void *logits, const float *bias, int32_t *ids, fl
 
 // ---- The layer for a few tokens --------------------------------------------
 //
-// Bound by the bytes of the chosen experts' weights, each read once, in two
-// kernels:
+// Bound by the bytes of the chosen experts' weights, each read once.  The pairs
+// p = (token, place) are grouped into units of up to 8 pairs of one expert;
 //
-//  up:   a workgroup takes one expert and MU_COLS columns of it.  It makes the
-//        choice of all tokens itself (its scores are a few KB in the cache;
-//        a kernel of its own would cost a launch), lists the expert's tokens,
-//        stages their rows of x in LDS, and streams the gate and up rows of its
-//        columns: a wave owns 16 gate rows and the 16 up rows beside them, W = 4
-//        waves share them and split K.  The activated and already weighted row
-//            a[p] = weight_p * silu(gate) * up          (rounded once to bf16)
-//        of each pair p = (token, place) goes to the workspace.
-//  down: a workgroup takes 16 rows of W2 in every chosen expert, so that a token's
-//        sum over its experts stays in one workgroup: no atomics, no third pass,
-//        and the order of the sum is fixed.  Its 16 waves are 4 parts of K x 4
-//        sets of experts.
+//  route: one workgroup makes the choice and writes the units (one token: the up
+//         kernel does it itself, since its pairs are its units);
+//  up:    a[p] = weight_p * silu(gate) * up, rounded once to bf16;
+//  down:  the rows pre[p] = W2 a[p] in fp32;
+//  join:  y[t] = the sum of its pairs' rows, in order of places.
 //
-// Both dequantise with v_cvt_scalef32_pk_bf16_fp4 into the A operand of
+// Up and down are one kernel: a workgroup takes one unit and FE_G groups of 16
+// weight rows (up: 16 gate rows and the 16 up rows beside them); FE_W waves share a
+// group and split K.  Every load that the workgroup needs is under way as soon as
+// the unit's entry is known; there is no loop around them for rows of up to
+// 128 FE_W FE_SPW elements.  Many short workgroups of few registers, two a CU
+// with 32 waves, measured faster than long ones that stream several units
+// through a ring (FEWFIGURES).
+//
+// Codes are dequantised with v_cvt_scalef32_pk_bf16_fp4 into the A operand of
 // v_mfma_f32_16x16x32_bf16 (lane (r, q) holds row r, block 4 j + q of the 128-k step
-// j: word s of its 16 code bytes feeds MFMA s of the step) with the tokens as B
-// columns: with one to a dozen tokens per expert the matrix unit does the work of
-// 16 for the same cost, and the vector unit only dequantises.
-constexpr int MU_W = 4, MU_G = 2; // up: waves of a group of rows, groups
-constexpr int MU_COLS = 16 * MU_G, MU_THREADS = 64 * MU_W * MU_G;
-constexpr int MU_D = 6;           // steps of a lane in flight
-constexpr int MD_W = 4, MD_S = 4; // down: parts of K, sets of experts
-constexpr int MD_WAVES = MD_W * MD_S, MD_THREADS = 64 * MD_WAVES;
-constexpr int MF_TOKENS = 32;     // tokens, at most (a 16-lane group each in the up kernel)
-constexpr int MF_PAIRS = 512;     // pairs, at most
-constexpr int MF_EXPERTS = 256;   // experts, at most (16 scores a lane)
-constexpr int MF_LDS = 64 * 1024;
+// j: word s of its 16 code bytes feeds MFMA s of the step) with the unit's pairs as
+// B columns, their rows staged in LDS.
+constexpr int FE_W = 8, FE_G = 2, FE_SPW = 3;
+constexpr int FE_THREADS = 64 * FE_W * FE_G;
+constexpr int FE_UNIT = 8;      // pairs of a unit, at most
+constexpr int MF_TOKENS = 32;   // tokens, at most: 16 lanes each in the choice
+constexpr int MF_PAIRS = 512;   // pairs, at most
+constexpr int MF_EXPERTS = 256; // experts, at most: 16 scores a lane
+constexpr int RT_THREADS = 512;
+static_assert(RT_THREADS / 16 >= MF_TOKENS, "every token has its lanes");
 
-// What the up kernel leaves for the down kernel: the pairs grouped by expert
-// and one unit per expert and 16 of its pairs.
+struct alignas(16) FewUnit {
+    int32_t expert, pairs, pad[2];
+    uint16_t pair[FE_UNIT];
+};
+
 struct FewWs {
     int32_t *units;  // their number
-    int4 *unit;      // {expert, first place in sorted, pairs, 0}
-    int32_t *sorted; // pairs by expert
+    int32_t *ids;    // [P] the chosen experts
+    float *weights;  // [P]
+    FewUnit *unit;   // [P]: every unit has a pair
     uint16_t *a;     // [P][I]
+    float *pre;      // [P][H]
 };
-size_t max_units(int64_t P) { return (size_t)P; } // every unit has a pair
 
-FewWs carve_few(void *ws, int64_t P)
+size_t few_a_at(int64_t P) { return round256(16 + (8 + sizeof(FewUnit)) * (size_t)P + 16); }
+size_t few_pre_at(int64_t P, int64_t I) { return few_a_at(P) + round256(2 * (size_t)P * (size_t)I); }
+size_t few_bytes(int64_t P, int64_t H, int64_t I) { return few_pre_at(P, I) + 4 * (size_t)P * (size_t)H; }
+
+FewWs carve_few(void *ws, int64_t P, int64_t I)
 {
     uint8_t *b = static_cast<uint8_t *>(ws);
     FewWs w;
     w.units = reinterpret_cast<int32_t *>(b);
-    w.unit = reinterpret_cast<int4 *>(b + 16);
-    w.sorted = reinterpret_cast<int32_t *>(b + 16 + 16 * max_units(P));
-    w.a = reinterpret_cast<uint16_t *>(b + round256(16 + 20 * max_units(P)));
+    w.unit = reinterpret_cast<FewUnit *>(b + 16);
+    w.ids = reinterpret_cast<int32_t *>(b + 16 + sizeof(FewUnit) * (size_t)P);
+    w.weights = reinterpret_cast<float *>(w.ids + P);
+    w.a = reinterpret_cast<uint16_t *>(b + few_a_at(P));
+    w.pre = reinterpret_cast<float *>(b + few_pre_at(P, I));
     return w;
-}
-size_t few_bytes(int64_t P, int64_t I) { return round256(16 + 20 * max_units(P)) + 2 * (size_t)P * (size_t)I; }
-
-// Bytes between staged rows of x: K rounded up to whole steps (zeros), 16 mod
-// 128, which makes the operand reads conflict-free.
-__host__ __device__ inline int up_pitch(int H) { return ((H + 127) & ~127) * 2 + 16; }
-// Staged rows: at most 8, and as many as leave the LDS room for two workgroups.
-inline size_t up_lds(int rows, int H, int P)
-{
-    const size_t staged = (size_t)rows * up_pitch(H) + (size_t)MU_G * 32 * (H >> 5);
-    const size_t sums = (size_t)MU_G * MU_W * 2 * 1024;
-    return ((std::max(staged, sums) + 15) & ~(size_t)15) + 12 * (size_t)P + 16;
-}
-inline int up_rows(int T, int H, int P)
-{
-    int rows = T > 4 ? 8 : T > 2 ? 4 : T;
-    while (rows > 0 && up_lds(rows, H, P) > (size_t)MF_LDS)
-        rows >>= 1;
-    return rows;
 }
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+struct FewArgs {
+    const uint16_t *x;
+    const void *logits;
+    const float *bias;
+    const uint8_t *w, *ws; // up: [E][2I][H/2] and scales; down: [E][H][I/2]
+    FewWs f;
+    uint16_t *y;
+    int dt, T, topk, E, H, I, renormalize;
+    int K, N, slices; // this kernel's row length, output columns and workgroups per unit
+};
+
+// The choice of all tokens and the units, in order of experts.  A wave lists an
+// expert's pairs by ballots over the pairs.
+template <int V>
+__global__ __launch_bounds__(RT_THREADS) void moe_few_route_kernel(const FewArgs p)
+{
+    __shared__ int32_t sid[MF_PAIRS], hits[MF_EXPERTS], first[MF_EXPERTS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, P = p.T * p.topk;
+    for (int e = tid; e < p.E; e += RT_THREADS)
+        hits[e] = 0;
+    __syncthreads();
+    const int t = tid >> 4, g = tid & 15;
+    int id[CHOICE_MAX / 16];
+    float wt[CHOICE_MAX / 16];
+    choose<16, V>(p.logits, p.dt, (int64_t)t * p.E, p.bias, t < p.T ? p.E : 0, p.topk,
+                  p.renormalize != 0, g, id, wt);
+    if (t < p.T) {
+#pragma unroll
+        for (int j = 0; j < CHOICE_MAX / 16; ++j)
+            if (16 * j + g < p.topk) {
+                const int i = t * p.topk + 16 * j + g;
+                sid[i] = id[j];
+                p.f.ids[i] = id[j];
+                p.f.weights[i] = wt[j];
+                if (id[j] >= 0)
+                    atomicAdd(&hits[id[j]], 1);
+            }
+    }
+    __syncthreads();
+    if (wave == 0) { // units before each expert's
+        int n = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 64) {
+            const int e = e0 + lane, mine = e < p.E ? (hits[e] + FE_UNIT - 1) / FE_UNIT : 0;
+            int upto = mine;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(upto, d);
+                upto += lane >= d ? o : 0;
+            }
+            if (e < p.E)
+                first[e] = n + upto - mine;
+            n += __shfl(upto, 63);
+        }
+        if (lane == 0)
+            *p.f.units = n;
+    }
+    __syncthreads();
+    for (int e = wave; e < p.E; e += RT_THREADS / 64) {
+        const int c = hits[e];
+        if (c == 0)
+            continue;
+        for (int u = lane; u * FE_UNIT < c; u += 64) {
+            p.f.unit[first[e] + u].expert = e;
+            p.f.unit[first[e] + u].pairs = min(FE_UNIT, c - u * FE_UNIT);
+        }
+        int rank = 0;
+        for (int i0 = 0; i0 < P; i0 += 64) {
+            const bool hit = i0 + lane < P && sid[i0 + lane] == e;
+            const uint64_t mask = __ballot(hit);
+            const int at = rank + __popcll(mask & (((uint64_t)1 << lane) - 1));
+            if (hit)
+                p.f.unit[first[e] + at / FE_UNIT].pair[at % FE_UNIT] = (uint16_t)(i0 + lane);
+            rank += __popcll(mask);
+        }
+    }
+}
+
+// Bytes between staged rows: K rounded up to whole steps (zeros), 16 mod 128,
+// which makes the operand reads conflict-free.
+__host__ __device__ inline int few_pitch(int K) { return ((K + 127) & ~127) * 2 + 16; }
+__host__ __device__ inline int few_rows(int T) { return T < FE_UNIT ? T : FE_UNIT; } // a unit's pairs have different tokens
+inline size_t few_lds(int T, int K, bool up)
+{
+    const size_t staged = (size_t)few_rows(T) * few_pitch(K) + (size_t)FE_G * (up ? 32 : 16) * (K >> 5);
+    const size_t sums = (size_t)FE_G * FE_W * (up ? 2 : 1) * 1024;
+    return (std::max(staged, sums) + 15) & ~(size_t)15;
+}
 
 // One 128-k step of 16 weight rows against the columns: word s of the lane's
 // codes times the column's k = 32 b + 8 s .. + 7.
@@ -139,394 +217,279 @@ __device__ __forceinline__ void step16(const u32x4 &codes, float scale, const u3
                                                       bitcast<bf168_t>(x[s]), acc, 0, 0, 0);
 }
 
-struct UpArgs {
-    const uint16_t *x;
-    const void *logits;
-    const float *bias;
-    const uint8_t *w, *ws;
-    FewWs out;
-    int dt, T, topk, E, H, I, renormalize, slices, rows;
-};
-
-template <int V>
-__global__ __launch_bounds__(MU_THREADS) void moe_up_kernel(const UpArgs p)
+// UP: gate and up rows, rows of x, activated rows of a; else rows of W2, rows of
+// a, fp32 rows of pre.  ONE: one token, and the choice made here (UP).
+template <bool UP, bool ONE, int V>
+__global__ __launch_bounds__(FE_THREADS, 8) void moe_few_kernel(const FewArgs p)
 {
+    constexpr int NR = UP ? 2 : 1; // 16-row operands of a group
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), k = wave % MU_W, g = wave / MU_W;
-    const int P = p.T * p.topk, KB = p.H >> 5, steps = (KB + 3) >> 2, pitch = up_pitch(p.H);
-    const size_t staged = (size_t)p.rows * pitch + (size_t)MU_G * 32 * KB;
-    const size_t sums = (size_t)MU_G * MU_W * 2 * 1024;
-    int32_t *const sid = reinterpret_cast<int32_t *>(smem + ((max(staged, sums) + 15) & ~(size_t)15));
-    float *const sw = reinterpret_cast<float *>(sid + P);
-    int32_t *const list = sid + 2 * P, *const count = sid + 3 * P;
-    const int slot = blockIdx.x / p.slices, slice = blockIdx.x - slot * p.slices;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), k = wave % FE_W, g = wave / FE_W;
+    const int KB = p.K >> 5, steps = (KB + 3) >> 2, pitch = few_pitch(p.K);
+    const int un = blockIdx.x / p.slices, slice = blockIdx.x - un * p.slices;
 
-    // The choice: 16 lanes a token.
-    {
-        const int t = tid >> 4, gl = tid & 15;
-        int id[CHOICE_MAX / 16];
-        float wt[CHOICE_MAX / 16];
-        choose<16, V>(p.logits, p.dt, (int64_t)t * p.E, p.bias, t < p.T ? p.E : 0, p.topk,
-                      p.renormalize != 0, gl, id, wt);
-        if (t < p.T) {
+    int e, pairs;
+    __shared__ int32_t pair_of[FE_UNIT];
+    __shared__ float weight_of[FE_UNIT];
+    if constexpr (ONE) {
+        // places with an expert come first, so place i is unit i
+        __shared__ int32_t id[CHOICE_MAX];
+        __shared__ float wt[CHOICE_MAX];
+        if (wave == 0) {
+            int cid[CHOICE_MAX / 16];
+            float cw[CHOICE_MAX / 16];
+            choose<16, V>(p.logits, p.dt, 0, p.bias, lane < 16 ? p.E : 0, p.topk, p.renormalize != 0,
+                          lane & 15, cid, cw);
+            if (lane < 16) {
 #pragma unroll
-            for (int j = 0; j < CHOICE_MAX / 16; ++j)
-                if (16 * j + gl < p.topk) {
-                    sid[t * p.topk + 16 * j + gl] = id[j];
-                    sw[t * p.topk + 16 * j + gl] = wt[j];
-                }
-        }
-        if (tid == 0)
-            *count = 0;
-    }
-    __syncthreads();
-
-    if (blockIdx.x == 0) {
-        // The pairs by expert (then by pair) and the units of up to 16 of them, each
-        // pair counting those before it; `list` holds a pair's rank in its expert.
-        for (int i = tid; i < P; i += MU_THREADS) {
-            int rank = 0;
-            for (int j = 0; j < i; ++j)
-                rank += sid[j] == sid[i];
-            list[i] = rank;
-        }
-        __syncthreads();
-        int units = 0;
-        for (int i = tid; i < P; i += MU_THREADS) {
-            const int e = sid[i], rank = list[i];
-            if (e < 0)
-                continue;
-            int lower = 0, all = 0, u = rank / 16;
-            for (int j = 0; j < P; ++j) {
-                const int o = sid[j];
-                const bool below = o >= 0 && o < e;
-                lower += below;
-                all += o == e;
-                u += below && list[j] % 16 == 0;
-            }
-            p.out.sorted[lower + rank] = i;
-            if (rank % 16 == 0) {
-                p.out.unit[u] = int4{e, lower + rank, min(16, all - rank), 0};
-                units = max(units, u + 1);
+                for (int j = 0; j < CHOICE_MAX / 16; ++j)
+                    if (16 * j + lane < p.topk) {
+                        id[16 * j + lane] = cid[j];
+                        wt[16 * j + lane] = cw[j];
+                    }
             }
         }
-        if (units)
-            atomicMax(count, units);
         __syncthreads();
+        if (blockIdx.x == 0) {
+            int n = 0;
+            for (int i = 0; i < p.topk; ++i)
+                n += id[i] >= 0;
+            if (tid == 0)
+                *p.f.units = n;
+            if (tid < p.topk) {
+                p.f.ids[tid] = id[tid];
+                FewUnit u;
+                u.expert = id[tid];
+                u.pairs = 1;
+                u.pair[0] = (uint16_t)tid;
+                p.f.unit[tid] = u;
+            }
+        }
+        e = __builtin_amdgcn_readfirstlane(id[un]);
+        if (e < 0)
+            return;
+        pairs = 1;
         if (tid == 0) {
-            *p.out.units = *count;
-            *count = 0;
+            pair_of[0] = un;
+            weight_of[0] = wt[un];
         }
-        __syncthreads();
+    } else {
+        if (un >= *p.f.units)
+            return;
+        const FewUnit *u = p.f.unit + un;
+        e = __builtin_amdgcn_readfirstlane(u->expert);
+        pairs = __builtin_amdgcn_readfirstlane(u->pairs);
+        if (tid < pairs) {
+            pair_of[tid] = u->pair[tid];
+            if constexpr (UP)
+                weight_of[tid] = p.f.weights[u->pair[tid]];
+        }
     }
 
-    // This workgroup's expert: with at most as many experts as pairs the slot is
-    // the expert, else the pair, and the first pair of an expert stands for it.
-    const int e = p.E <= P ? slot : sid[slot];
-    bool earlier = false;
-    for (int i = tid; i < P; i += MU_THREADS) {
-        if (e < 0 || sid[i] != e)
-            continue;
-        earlier |= i < slot;
-        list[atomicAdd(count, 1)] = i; // (in any order: each pair's row is computed on its own)
+    // Codes: scalar bases, 32-bit lane offsets.
+    const int c0 = (slice * FE_G + g) * 16;  // this group's columns (may lie past the last)
+    const int cc = min(c0, p.N - 16);
+    const size_t row = (size_t)e * NR * p.N + cc;
+    const uint8_t *const w0 = p.w + row * (size_t)KB * 16, *const w1 = w0 + (size_t)p.N * KB * 16;
+    const int rounds = (steps + FE_W * FE_SPW - 1) / (FE_W * FE_SPW);
+    auto block = [&](int round, int j) __attribute__((always_inline)) { // this lane's
+        return 4 * ((round * FE_W + k) * FE_SPW + j) + q;
+    };
+    u32x4 c[NR][FE_SPW];
+    auto load = [&](int round) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < FE_SPW; ++j) {
+            const uint32_t at = 16u * (uint32_t)(r * KB + min(block(round, j), KB - 1));
+            c[0][j] = *reinterpret_cast<const u32x4 *>(w0 + at);
+            if constexpr (UP)
+                c[1][j] = *reinterpret_cast<const u32x4 *>(w1 + at);
+        }
+    };
+    load(0);
+    // Scale bytes: the 16 rows of an operand are KB 16-byte units in a row.
+    uint8_t *const sl = smem + (size_t)few_rows(p.T) * pitch;
+    const int su = NR * FE_G * KB;
+    auto scale_unit = [&](int i) __attribute__((always_inline)) {
+        const int op = i / KB, at = i - op * KB, n = min((slice * FE_G + op / NR) * 16, p.N - 16);
+        return reinterpret_cast<const u32x4 *>(
+            p.ws + ((size_t)e * NR * p.N + (size_t)(op % NR) * p.N + n) * KB)[at];
+    };
+    const u32x4 sv = scale_unit(min(tid, su - 1));
+    __syncthreads(); // the pairs are listed
+    const int nv = pitch / 16, nx = p.K / 8; // 16-byte units of a staged row, of a row
+    const uint16_t *const rows = UP ? p.x : p.f.a;
+    auto x_unit = [&](int i) __attribute__((always_inline)) {
+        const int m = i / nv, at = i - m * nv;
+        const int src = UP ? pair_of[m] / p.topk : pair_of[m];
+        u32x4 v{0, 0, 0, 0};
+        if (at < nx)
+            v = reinterpret_cast<const u32x4 *>(rows + (size_t)src * p.K)[at];
+        return v;
+    };
+    constexpr int XB = 2; // units of a thread under way at a time
+    for (int i0 = tid; i0 < pairs * nv; i0 += XB * FE_THREADS) {
+        u32x4 v[XB];
+#pragma unroll
+        for (int i = 0; i < XB; ++i)
+            v[i] = x_unit(min(i0 + i * FE_THREADS, pairs * nv - 1));
+#pragma unroll
+        for (int i = 0; i < XB; ++i)
+            if (i0 + i * FE_THREADS < pairs * nv)
+                reinterpret_cast<u32x4 *>(smem)[i0 + i * FE_THREADS] = v[i];
     }
-    const int again = __syncthreads_or(p.E > P && earlier);
-    const int rows = *count;
-    if (rows == 0 || again)
+    if (tid < su)
+        reinterpret_cast<u32x4 *>(sl)[tid] = sv;
+    for (int i = tid + FE_THREADS; i < su; i += FE_THREADS)
+        reinterpret_cast<u32x4 *>(sl)[i] = scale_unit(i);
+    __syncthreads();
+
+    const uint8_t *const xr = smem + (size_t)min(r, pairs - 1) * pitch;
+    const uint8_t *const sr = sl + (size_t)(NR * 16 * g + r) * KB;
+    f32x4 acc[NR];
+#pragma unroll
+    for (int o = 0; o < NR; ++o)
+        acc[o] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int round = 0; round < rounds; ++round) {
+        if (round > 0)
+            load(round);
+#pragma unroll
+        for (int j = 0; j < FE_SPW; ++j) {
+            // (past the row: zero codes under one of the row's own scale bytes, so a NaN
+            // there is the row's result anyway, and the zeros behind the staged row)
+            const int b = block(round, j), bc = min(b, KB - 1), bx = min(b, 4 * steps - 1);
+            u32x4 x[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                x[s] = *reinterpret_cast<const u32x4 *>(xr + 64 * bx + 16 * s);
+#pragma unroll
+            for (int o = 0; o < NR; ++o) {
+                u32x4 v = c[o][j];
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    v[s] = b < KB ? v[s] : 0u;
+                step16(v, e8m0_to_f32(sr[o * 16 * KB + bc]), x, acc[o]);
+            }
+        }
+    }
+
+    // The waves' sums in order of K; lane (r, q) holds columns 4 q + i of pair r.
+    __syncthreads();
+    f32x4 *const part = reinterpret_cast<f32x4 *>(smem);
+#pragma unroll
+    for (int o = 0; o < NR; ++o)
+        part[(wave * NR + o) * 64 + lane] = acc[o];
+    __syncthreads();
+    if (k != 0 || r >= pairs || c0 >= p.N)
         return;
-
-    // Weight rows: this lane's gate row and the up row beside it (I % 32 == 0
-    // except for a last half slice: rows past it are clamped, not stored).
-    const int c0 = slice * MU_COLS + 16 * g;
-    const int gr = min(c0, p.I - 16) + r;
-    const size_t er = (size_t)e * 2 * (size_t)p.I;
-    const u32x4 *wg = reinterpret_cast<const u32x4 *>(p.w) + (er + gr) * (size_t)KB;
-    const u32x4 *wu = wg + (size_t)p.I * KB;
-    const int mine = 2 * (((steps + 1) / 2 - k + MU_W - 1) / MU_W); // neighbouring steps in pairs
-    auto block = [&](int i) __attribute__((always_inline)) {
-        return 4 * (2 * (k + MU_W * (i / 2)) + i % 2) + q;
-    };
-    u32x4 rg[MU_D], ru[MU_D];
-    auto load = [&](int i, int d) __attribute__((always_inline)) {
-        int b = min(block(i), KB - 1);
-        asm volatile("" : "+v"(b));
-        rg[d] = wg[b];
-        ru[d] = wu[b];
-    };
-    uint8_t *const sl = smem + (size_t)p.rows * pitch; // scales: per group 16 gate, 16 up rows
-    const int nv = pitch / 16, nx = p.H / 8;           // 16-byte units of a staged row, of x's
-
-    for (int m0 = 0; m0 < rows; m0 += p.rows) {
-        const int mr = min(p.rows, rows - m0);
-        if (m0 > 0)
-            __syncthreads(); // the previous pass's sums have been read
-        auto x_unit = [&](int i) __attribute__((always_inline)) {
-            const int m = i / nv, c = i - m * nv;
-            u32x4 v{0, 0, 0, 0};
-            if (c < nx)
-                v = reinterpret_cast<const u32x4 *>(p.x + (size_t)(list[m0 + m] / p.topk) * p.H)[c];
-            return v;
-        };
-        // rows of x and the scales are requested ahead of the codes and land first
-        constexpr int XB = 2;
-        u32x4 xv[XB];
 #pragma unroll
-        for (int b = 0; b < XB; ++b)
-            xv[b] = x_unit(min(tid + b * MU_THREADS, mr * nv - 1));
-        // 16 rows of scales are 16 KB bytes in a row, 16-byte aligned
-        const int su = 2 * MU_G * KB; // 16-byte units
-        auto s_unit = [&](int i) __attribute__((always_inline)) {
-            const int part = i / KB, c = i - part * KB; // group, gate / up
-            const size_t row = er + (size_t)(part & 1) * p.I + min(slice * MU_COLS + 16 * (part >> 1), p.I - 16);
-            return reinterpret_cast<const u32x4 *>(p.ws + row * KB)[c];
-        };
-        const u32x4 sv = s_unit(min(tid, su - 1));
+    for (int o = 0; o < NR; ++o)
+        for (int j = 1; j < FE_W; ++j)
+            acc[o] += part[((wave + j) * NR + o) * 64 + lane];
+    const int pair = pair_of[r];
+    const size_t to = (size_t)pair * p.N + c0 + 4 * q;
+    if constexpr (UP) {
+        const float wt = weight_of[r];
+        float a[4];
 #pragma unroll
-        for (int d = 0; d < MU_D; ++d)
-            load(min(d, max(mine - 1, 0)), d);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int b = 0; b < XB; ++b)
-            if (tid + b * MU_THREADS < mr * nv)
-                reinterpret_cast<u32x4 *>(smem)[tid + b * MU_THREADS] = xv[b];
-        if (tid < su)
-            reinterpret_cast<u32x4 *>(sl)[tid] = sv;
-        for (int i = tid + XB * MU_THREADS; i < mr * nv; i += MU_THREADS)
-            reinterpret_cast<u32x4 *>(smem)[i] = x_unit(i);
-        for (int i = tid + MU_THREADS; i < su; i += MU_THREADS)
-            reinterpret_cast<u32x4 *>(sl)[i] = s_unit(i);
-        __syncthreads();
-
-        const uint8_t *xr = smem + (size_t)min(r, mr - 1) * pitch;
-        const uint8_t *sg = sl + (size_t)(32 * g + r) * KB, *sup = sg + (size_t)16 * KB;
-        f32x4 ag{0.f, 0.f, 0.f, 0.f}, au{0.f, 0.f, 0.f, 0.f};
-        auto multiply = [&](int i, int d) __attribute__((always_inline)) {
-            const int b = block(i);
-            const bool in = b < KB;
-            const int bc = in ? b : KB - 1;
-            // (past the row: zero codes under the row's own scale; x is zero there)
-            u32x4 cg = rg[d], cu = ru[d], xo[4];
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                cg[s] = in ? cg[s] : 0u;
-                cu[s] = in ? cu[s] : 0u;
-                xo[s] = *reinterpret_cast<const u32x4 *>(xr + 64 * min(b, 4 * steps - 1) + 16 * s);
-            }
-            step16(cg, e8m0_to_f32(sg[bc]), xo, ag);
-            step16(cu, e8m0_to_f32(sup[bc]), xo, au);
-        };
-        int i = 0;
-        for (; i + MU_D < mine; i += MU_D) {
-#pragma unroll
-            for (int d = 0; d < MU_D; ++d) {
-                if (i + d < mine)
-                    multiply(i + d, d);
-                __builtin_amdgcn_sched_barrier(0);
-                load(min(i + d + MU_D, mine - 1), d);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-#pragma unroll
-        for (int d = 0; d < MU_D; ++d)
-            if (i + d < mine)
-                multiply(i + d, d);
-
-        // Sums over the parts of K in order; lane (r, q) holds columns 4 q + e of
-        // row r of the pass.
-        __syncthreads();
-        f32x4 *part = reinterpret_cast<f32x4 *>(smem);
-        part[(2 * wave + 0) * 64 + lane] = ag;
-        part[(2 * wave + 1) * 64 + lane] = au;
-        __syncthreads();
-        if (k == 0) {
-#pragma unroll
-            for (int j = 1; j < MU_W; ++j) {
-                ag += part[(2 * (wave + j) + 0) * 64 + lane];
-                au += part[(2 * (wave + j) + 1) * 64 + lane];
-            }
-            const int n = c0 + 4 * q;
-            if (r < mr && n < p.I) {
-                const int pair = list[m0 + r];
-                const float wt = sw[pair];
-                float a[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    a[j] = wt * (ag[j] / (1.0f + expf(-ag[j])) * au[j]);
-                *reinterpret_cast<uint2 *>(p.out.a + (size_t)pair * p.I + n) =
-                    uint2{f32x2_to_act2<DT_BF16>(a[0], a[1]), f32x2_to_act2<DT_BF16>(a[2], a[3])};
-            }
-        }
+        for (int j = 0; j < 4; ++j)
+            a[j] = wt * (acc[0][j] / (1.0f + expf(-acc[0][j])) * acc[NR - 1][j]);
+        *reinterpret_cast<uint2 *>(p.f.a + to) =
+            uint2{f32x2_to_act2<DT_BF16>(a[0], a[1]), f32x2_to_act2<DT_BF16>(a[2], a[3])};
+    } else {
+        *reinterpret_cast<f32x4 *>(p.f.pre + to) = acc[0];
     }
 }
 
-struct DownArgs {
-    const uint8_t *w, *ws;
-    FewWs in;
-    uint16_t *y;
-    int T, topk, H, I, P;
-};
-
-// The down kernel's ring holds pairs of steps: two code loads, the eight scale
-// bytes of the pair and the B operands of both steps.
-struct DownSlot {
-    u32x4 w[2], x[2][4];
-    uint64_t s;
-};
-constexpr int MD_D = 2; // pairs of steps in flight
-
-__global__ __launch_bounds__(MD_THREADS) void moe_down_kernel(const DownArgs p)
+// y[t][h .. h + 3] = the sum of token t's rows of pre, in order of places.
+__global__ __launch_bounds__(256) void moe_few_join_kernel(const float *__restrict__ pre,
+                                                           const int32_t *__restrict__ ids,
+                                                           uint16_t *__restrict__ y, int topk, int H)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
-    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), k = wave % MD_W, set = wave / MD_W;
-    const int KB = p.I >> 5, h0 = blockIdx.x * 16;
-    const int per = ((KB + 7) / 8 - k + MD_W - 1) / MD_W; // pairs of steps of this wave and unit
-    float *const sums = reinterpret_cast<float *>(smem);  // [wave][T][16]
-    float *const ys = sums + wave * p.T * 16;
-    for (int i = lane; i < p.T * 16; i += 64)
-        ys[i] = 0.f;
-    const int units = *p.in.units;
-    int4 *const table = reinterpret_cast<int4 *>(sums + MD_WAVES * p.T * 16);
-    int32_t *const sorted = reinterpret_cast<int32_t *>(table + p.P);
-    for (int i = tid; i < units; i += MD_THREADS)
-        table[i] = p.in.unit[i];
-    for (int i = tid; i < p.P; i += MD_THREADS)
-        sorted[i] = p.in.sorted[i]; // (places behind the last pair with an expert are not used)
-    __syncthreads();
-    const int mine = set < units ? (units - set + MD_S - 1) / MD_S : 0;
-    const int items = mine * per; // unit by unit
-    const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc(
-        p.in.a, 0, (int)((uint32_t)p.P * (uint32_t)p.I * 2u), 0x00020000);
-
-    // The unit that loads are issued for, and the unit whose products are summed.
-    struct Unit {
-        int n, expert, pairs, pair; // number, its expert, pairs, this lane's pair
-    };
-    auto unit = [&](int n) __attribute__((always_inline)) {
-        const int4 u = table[set + MD_S * min(n, mine - 1)];
-        return Unit{n, u.x, u.z, sorted[u.y + min(r, u.z - 1)]};
-    };
-    DownSlot ring[MD_D];
-    Unit lu, cu;
-    int lc = 0, cc = 0; // pair of steps within the unit
-    auto load = [&](DownSlot &s) __attribute__((always_inline)) {
-        const size_t row = (size_t)lu.expert * p.H + h0 + r;
-        const int b = 8 * (k + MD_W * lc);
-        const u32x4 *w = reinterpret_cast<const u32x4 *>(p.w) + row * KB;
-        const uint8_t *sc = p.ws + row * KB;
-        __builtin_memcpy(&s.s, sc + min(b, KB - 8), 8); // the row's last eight where b + 8 > KB
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int bj = b + 4 * j + q;
-            s.w[j] = w[min(bj, KB - 1)];
-            // columns without a pair and blocks past the row read as zero
-            const uint32_t at = r < lu.pairs && bj < KB
-                                    ? ((uint32_t)lu.pair * (uint32_t)p.I + 32u * (uint32_t)bj) * 2u
-                                    : 0xFFFFFF00u;
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                s.x[j][t] = __builtin_amdgcn_raw_buffer_load_b128(rows, at + 16u * (uint32_t)t, 0, 0);
-        }
-        if (++lc == per) {
-            lc = 0;
-            lu = unit(lu.n + 1);
-        }
-    };
-    f32x4 acc{0.f, 0.f, 0.f, 0.f};
-    auto multiply = [&](const DownSlot &s) __attribute__((always_inline)) {
-        const int b = 8 * (k + MD_W * cc);
-        const uint64_t v = s.s >> (8 * max(b - (KB - 8), 0));
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            step16(s.w[j], e8m0_to_f32((uint32_t)(v >> (32 * j + 8 * q)) & 0xFFu), s.x[j], acc);
-        if (++cc == per) {
-            if (r < cu.pairs) { // this lane's token: rows 4 q .. + 3 of its outputs
-                f32x4 *to = reinterpret_cast<f32x4 *>(ys + (cu.pair / p.topk) * 16) + q;
-                *to += acc;
-            }
-            acc = f32x4{0.f, 0.f, 0.f, 0.f};
-            cc = 0;
-            cu = unit(cu.n + 1);
-        }
-    };
-    if (items > 0) {
-        lu = cu = unit(0);
-#pragma unroll
-        for (int d = 0; d < MD_D; ++d)
-            load(ring[d]);
-        int i = 0;
-        for (; i + MD_D <= items; i += MD_D) {
-#pragma unroll
-            for (int d = 0; d < MD_D; ++d) {
-                multiply(ring[d]);
-                __builtin_amdgcn_sched_barrier(0);
-                load(ring[d]); // past the last item: the last unit's again
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-#pragma unroll
-        for (int d = 0; d < MD_D; ++d)
-            if (i + d < items)
-                multiply(ring[d]);
+    const int t = blockIdx.y, h = (blockIdx.x * 256 + threadIdx.x) * 4;
+    if (h >= H)
+        return;
+    f32x4 v{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < topk; ++s) {
+        const int p = t * topk + s;
+        if (ids[p] >= 0)
+            v += *reinterpret_cast<const f32x4 *>(pre + (size_t)p * H + h);
     }
-    __syncthreads();
-    for (int i = tid; i < p.T * 16; i += MD_THREADS) {
-        float v = 0.f;
-#pragma unroll
-        for (int j = 0; j < MD_WAVES; ++j)
-            v += sums[j * p.T * 16 + i];
-        p.y[(size_t)(i >> 4) * p.H + h0 + (i & 15)] = f32_to_act<DT_BF16>(v);
-    }
+    *reinterpret_cast<uint2 *>(y + (size_t)t * H + h) =
+        uint2{f32x2_to_act2<DT_BF16>(v[0], v[1]), f32x2_to_act2<DT_BF16>(v[2], v[3])};
 }
 
-// Whether the two kernels above take the layer: their scores, tables and staged
-// rows fit, and a row of W2 has the eight scale bytes that one load takes.
+// Whether the kernels above take the layer: their lists and the staged rows fit.
 bool layer_few(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
 {
-    return T <= MF_TOKENS && T * topk <= MF_PAIRS && E <= MF_EXPERTS && I >= 256 && H <= 32768 &&
-           up_rows((int)T, (int)H, (int)(T * topk)) > 0;
+    constexpr size_t most = 150 * 1024;
+    return T <= MF_TOKENS && T * topk <= MF_PAIRS && E <= MF_EXPERTS && H <= 32768 && I <= 32768 &&
+           few_lds((int)T, (int)H, true) <= most && few_lds((int)T, (int)I, false) <= most;
 }
 
-hipError_t launch_layer_few(const MoeLayerArgs &a, void *workspace, hipStream_t stream)
+template <bool UP, bool ONE, int V>
+hipError_t launch_few(const FewArgs &a, hipStream_t stream)
 {
-    const int P = a.T * a.topk;
-    UpArgs u;
-    u.x = static_cast<const uint16_t *>(a.x);
-    u.logits = a.logits;
-    u.bias = a.bias;
-    u.w = a.w1;
-    u.ws = a.w1s;
-    u.out = carve_few(workspace, P);
-    u.dt = a.logits_dt;
-    u.T = a.T;
-    u.topk = a.topk;
-    u.E = a.E;
-    u.H = a.H;
-    u.I = a.I;
-    u.renormalize = a.renormalize;
-    u.slices = (a.I + MU_COLS - 1) / MU_COLS;
-    u.rows = up_rows(a.T, a.H, P);
-    const size_t lds = up_lds(u.rows, a.H, P);
-    const unsigned grid = (unsigned)(std::min(a.E, P) * u.slices);
-    if (a.E <= 32)
-        hipLaunchKernelGGL(moe_up_kernel<2>, dim3(grid), dim3(MU_THREADS), lds, stream, u);
-    else
-        hipLaunchKernelGGL(moe_up_kernel<16>, dim3(grid), dim3(MU_THREADS), lds, stream, u);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess)
+    auto kern = moe_few_kernel<UP, ONE, V>;
+    static std::atomic<uint64_t> lds_set{0};
+    if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), 156 * 1024, lds_set);
+        e != hipSuccess)
         return e;
-    DownArgs d;
-    d.w = a.w2;
-    d.ws = a.w2s;
-    d.in = u.out;
-    d.y = static_cast<uint16_t *>(a.y);
-    d.T = a.T;
-    d.topk = a.topk;
-    d.H = a.H;
-    d.I = a.I;
-    d.P = P;
-    hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(a.H / 16)), dim3(MD_THREADS),
-                       (size_t)MD_WAVES * a.T * 64 + (size_t)P * 20, stream, d);
+    // units: at most one for every pair, one for every expert and FE_UNIT of its pairs
+    const int P = a.T * a.topk, units = std::min(P, a.E * ((a.T + FE_UNIT - 1) / FE_UNIT));
+    hipLaunchKernelGGL(kern, dim3((unsigned)(units * a.slices)), dim3(FE_THREADS), few_lds(a.T, a.K, UP),
+                       stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_layer_few(const MoeLayerArgs &m, void *workspace, hipStream_t stream)
+{
+    FewArgs a;
+    a.x = static_cast<const uint16_t *>(m.x);
+    a.logits = m.logits;
+    a.bias = m.bias;
+    a.f = carve_few(workspace, m.T * m.topk, m.I);
+    a.y = static_cast<uint16_t *>(m.y);
+    a.dt = m.logits_dt;
+    a.T = m.T;
+    a.topk = m.topk;
+    a.E = m.E;
+    a.H = m.H;
+    a.I = m.I;
+    a.renormalize = m.renormalize;
+    hipError_t e = hipSuccess;
+    if (m.T > 1) {
+        if (m.E <= 32)
+            hipLaunchKernelGGL(moe_few_route_kernel<2>, dim3(1), dim3(RT_THREADS), 0, stream, a);
+        else
+            hipLaunchKernelGGL(moe_few_route_kernel<16>, dim3(1), dim3(RT_THREADS), 0, stream, a);
+        e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    a.w = m.w1;
+    a.ws = m.w1s;
+    a.K = m.H;
+    a.N = m.I;
+    a.slices = (m.I + 16 * FE_G - 1) / (16 * FE_G);
+    if (m.T > 1)
+        e = launch_few<true, false, 1>(a, stream);
+    else if (m.E <= 32)
+        e = launch_few<true, true, 2>(a, stream);
+    else
+        e = launch_few<true, true, 16>(a, stream);
+    if (e != hipSuccess)
+        return e;
+    a.w = m.w2;
+    a.ws = m.w2s;
+    a.K = m.I;
+    a.N = m.H;
+    a.slices = (m.H + 16 * FE_G - 1) / (16 * FE_G);
+    e = launch_few<false, false, 1>(a, stream);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(moe_few_join_kernel, dim3((unsigned)((m.H + 1023) / 1024), (unsigned)m.T), dim3(256), 0,
+                       stream, a.f.pre, a.f.ids, a.y, m.topk, m.H);
     return hipGetLastError();
 }
 
@@ -575,7 +538,7 @@ hipError_t launch_moe_topk(const void *logits, int dt, const float *bias, int32_
 size_t moe_layer_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
 {
     if (layer_few(T, topk, E, H, I))
-        return few_bytes(T * topk, I);
+        return few_bytes(T * topk, H, I);
     return layer_stage_at(T * topk, I) + moe_stage2_workspace_bytes(T, topk, E, H);
 }
 
