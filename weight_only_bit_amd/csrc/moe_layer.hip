@@ -65,20 +65,29 @@ hipError_t launch_topk_v(const void *logits, const float *bias, int32_t *ids, fl
 //  down:  the rows pre[p] = W2 a[p] in fp32;
 //  join:  y[t] = the sum of its pairs' rows, in order of places.
 //
-// Up and down are one kernel: a workgroup takes one unit and FE_G groups of 16
-// weight rows (up: 16 gate rows and the 16 up rows beside them); FE_W waves share a
-// group and split K.  Every load that the workgroup needs is under way as soon as
-// the unit's entry is known; there is no loop around them for rows of up to
-// 128 FE_W FE_SPW elements.  Many short workgroups of few registers, two a CU
-// with 32 waves, measured faster than long ones that stream several units
-// through a ring (FEWFIGURES).
+// Up and down are one kernel: a workgroup takes one unit and G groups of 16
+// weight rows (up: 16 gate rows and the 16 up rows beside them); W waves share a
+// group and split K.  Every load that the workgroup needs for its first 128 W FE_SPW
+// elements of K is under way as soon as the unit's entry is known.  Many short
+// workgroups with few registers (64: 32 waves a CU) took 105 us for 32 tokens where
+// long ones that stream several units through a ring of registers took 145 to 160
+// (each unit then waits for a whole memory round trip: too few waves to hide it).
+// 32 experts, top 4, H = I = 2880, graph replay over three copies, us for 1 / 4 / 8 /
+// 16 / 32 tokens:
+//   W = 8, G = 1, FE_SPW = 3    20.1 / 47.5 / 69.9 / 92.9 / 121
+//   W = 4, G = 2, FE_SPW = 3    21.7 / 50.7 / 71.2 / 90.8 / 105
+//   W = 8, G = 2, FE_SPW = 3    23.1 / 55.7 / 77.7 / 97.6 / 115
+//   W = 12, G = 1, FE_SPW = 2   24.8 / 60.3 / - / - / 145
+// (plain reads of the weights alone: 9 / 26 / 42 / 55 / 61).  The narrow form has
+// twice the workgroups, each with its own copy of the rows: better until the rows
+// weigh.
 //
 // Codes are dequantised with v_cvt_scalef32_pk_bf16_fp4 into the A operand of
 // v_mfma_f32_16x16x32_bf16 (lane (r, q) holds row r, block 4 j + q of the 128-k step
 // j: word s of its 16 code bytes feeds MFMA s of the step) with the unit's pairs as
 // B columns, their rows staged in LDS.
-constexpr int FE_W = 8, FE_G = 2, FE_SPW = 3;
-constexpr int FE_THREADS = 64 * FE_W * FE_G;
+constexpr int FE_NARROW = 8;    // tokens with W = 8, G = 1, at most; more: W = 4, G = 2
+constexpr int FE_SPW = 3;       // steps of a wave at a time
 constexpr int FE_UNIT = 8;      // pairs of a unit, at most
 constexpr int MF_TOKENS = 32;   // tokens, at most: 16 lanes each in the choice
 constexpr int MF_PAIRS = 512;   // pairs, at most
@@ -89,18 +98,18 @@ static_assert(RT_THREADS / 16 >= MF_TOKENS, "every token has its lanes");
 struct alignas(16) FewUnit {
     int32_t expert, pairs, pad[2];
     uint16_t pair[FE_UNIT];
+    float weight[FE_UNIT];
 };
 
 struct FewWs {
     int32_t *units;  // their number
     int32_t *ids;    // [P] the chosen experts
-    float *weights;  // [P]
     FewUnit *unit;   // [P]: every unit has a pair
     uint16_t *a;     // [P][I]
     float *pre;      // [P][H]
 };
 
-size_t few_a_at(int64_t P) { return round256(16 + (8 + sizeof(FewUnit)) * (size_t)P + 16); }
+size_t few_a_at(int64_t P) { return round256(16 + (4 + sizeof(FewUnit)) * (size_t)P); }
 size_t few_pre_at(int64_t P, int64_t I) { return few_a_at(P) + round256(2 * (size_t)P * (size_t)I); }
 size_t few_bytes(int64_t P, int64_t H, int64_t I) { return few_pre_at(P, I) + 4 * (size_t)P * (size_t)H; }
 
@@ -111,7 +120,6 @@ FewWs carve_few(void *ws, int64_t P, int64_t I)
     w.units = reinterpret_cast<int32_t *>(b);
     w.unit = reinterpret_cast<FewUnit *>(b + 16);
     w.ids = reinterpret_cast<int32_t *>(b + 16 + sizeof(FewUnit) * (size_t)P);
-    w.weights = reinterpret_cast<float *>(w.ids + P);
     w.a = reinterpret_cast<uint16_t *>(b + few_a_at(P));
     w.pre = reinterpret_cast<float *>(b + few_pre_at(P, I));
     return w;
@@ -136,6 +144,7 @@ template <int V>
 __global__ __launch_bounds__(RT_THREADS) void moe_few_route_kernel(const FewArgs p)
 {
     __shared__ int32_t sid[MF_PAIRS], hits[MF_EXPERTS], first[MF_EXPERTS];
+    __shared__ float sw[MF_PAIRS];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, P = p.T * p.topk;
     for (int e = tid; e < p.E; e += RT_THREADS)
         hits[e] = 0;
@@ -151,8 +160,8 @@ __global__ __launch_bounds__(RT_THREADS) void moe_few_route_kernel(const FewArgs
             if (16 * j + g < p.topk) {
                 const int i = t * p.topk + 16 * j + g;
                 sid[i] = id[j];
+                sw[i] = wt[j];
                 p.f.ids[i] = id[j];
-                p.f.weights[i] = wt[j];
                 if (id[j] >= 0)
                     atomicAdd(&hits[id[j]], 1);
             }
@@ -189,8 +198,11 @@ __global__ __launch_bounds__(RT_THREADS) void moe_few_route_kernel(const FewArgs
             const bool hit = i0 + lane < P && sid[i0 + lane] == e;
             const uint64_t mask = __ballot(hit);
             const int at = rank + __popcll(mask & (((uint64_t)1 << lane) - 1));
-            if (hit)
-                p.f.unit[first[e] + at / FE_UNIT].pair[at % FE_UNIT] = (uint16_t)(i0 + lane);
+            if (hit) {
+                FewUnit &u = p.f.unit[first[e] + at / FE_UNIT];
+                u.pair[at % FE_UNIT] = (uint16_t)(i0 + lane);
+                u.weight[at % FE_UNIT] = sw[i0 + lane];
+            }
             rank += __popcll(mask);
         }
     }
@@ -200,10 +212,11 @@ __global__ __launch_bounds__(RT_THREADS) void moe_few_route_kernel(const FewArgs
 // which makes the operand reads conflict-free.
 __host__ __device__ inline int few_pitch(int K) { return ((K + 127) & ~127) * 2 + 16; }
 __host__ __device__ inline int few_rows(int T) { return T < FE_UNIT ? T : FE_UNIT; } // a unit's pairs have different tokens
-inline size_t few_lds(int T, int K, bool up)
+template <bool UP, int W, int G>
+size_t few_lds(int T, int K)
 {
-    const size_t staged = (size_t)few_rows(T) * few_pitch(K) + (size_t)FE_G * (up ? 32 : 16) * (K >> 5);
-    const size_t sums = (size_t)FE_G * FE_W * (up ? 2 : 1) * 1024;
+    const size_t staged = (size_t)few_rows(T) * few_pitch(K) + (size_t)G * (UP ? 32 : 16) * (K >> 5);
+    const size_t sums = (size_t)G * W * (UP ? 2 : 1) * 1024;
     return (std::max(staged, sums) + 15) & ~(size_t)15;
 }
 
@@ -219,18 +232,19 @@ __device__ __forceinline__ void step16(const u32x4 &codes, float scale, const u3
 
 // UP: gate and up rows, rows of x, activated rows of a; else rows of W2, rows of
 // a, fp32 rows of pre.  ONE: one token, and the choice made here (UP).
-template <bool UP, bool ONE, int V>
-__global__ __launch_bounds__(FE_THREADS, 8) void moe_few_kernel(const FewArgs p)
+template <bool UP, bool ONE, int V, int W, int G>
+__global__ __launch_bounds__(64 * W * G, 8) void moe_few_kernel(const FewArgs p)
 {
+    constexpr int NT = 64 * W * G;
     constexpr int NR = UP ? 2 : 1; // 16-row operands of a group
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), k = wave % FE_W, g = wave / FE_W;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), k = wave % W, g = wave / W;
     const int KB = p.K >> 5, steps = (KB + 3) >> 2, pitch = few_pitch(p.K);
     const int un = blockIdx.x / p.slices, slice = blockIdx.x - un * p.slices;
 
     int e, pairs;
-    __shared__ int32_t pair_of[FE_UNIT];
+    __shared__ int32_t pair_of[FE_UNIT], row_of[FE_UNIT]; // pairs, their rows of the input
     __shared__ float weight_of[FE_UNIT];
     if constexpr (ONE) {
         // places with an expert come first, so place i is unit i
@@ -272,29 +286,35 @@ __global__ __launch_bounds__(FE_THREADS, 8) void moe_few_kernel(const FewArgs p)
         pairs = 1;
         if (tid == 0) {
             pair_of[0] = un;
+            row_of[0] = 0;
             weight_of[0] = wt[un];
         }
     } else {
-        if (un >= *p.f.units)
-            return;
+        // the unit's entry is requested with the number of units, not after it (it is
+        // in the table, but holds nothing past the last unit)
         const FewUnit *u = p.f.unit + un;
-        e = __builtin_amdgcn_readfirstlane(u->expert);
-        pairs = __builtin_amdgcn_readfirstlane(u->pairs);
+        const int units = *p.f.units, expert = u->expert, n = u->pairs;
+        const int pair = u->pair[tid & (FE_UNIT - 1)];
+        const float weight = u->weight[tid & (FE_UNIT - 1)];
+        if (un >= units)
+            return;
+        e = __builtin_amdgcn_readfirstlane(expert);
+        pairs = __builtin_amdgcn_readfirstlane(n);
         if (tid < pairs) {
-            pair_of[tid] = u->pair[tid];
-            if constexpr (UP)
-                weight_of[tid] = p.f.weights[u->pair[tid]];
+            pair_of[tid] = pair;
+            row_of[tid] = UP ? pair / p.topk : pair;
+            weight_of[tid] = weight;
         }
     }
 
     // Codes: scalar bases, 32-bit lane offsets.
-    const int c0 = (slice * FE_G + g) * 16;  // this group's columns (may lie past the last)
+    const int c0 = (slice * G + g) * 16;  // this group's columns (may lie past the last)
     const int cc = min(c0, p.N - 16);
     const size_t row = (size_t)e * NR * p.N + cc;
     const uint8_t *const w0 = p.w + row * (size_t)KB * 16, *const w1 = w0 + (size_t)p.N * KB * 16;
-    const int rounds = (steps + FE_W * FE_SPW - 1) / (FE_W * FE_SPW);
+    const int rounds = (steps + W * FE_SPW - 1) / (W * FE_SPW);
     auto block = [&](int round, int j) __attribute__((always_inline)) { // this lane's
-        return 4 * ((round * FE_W + k) * FE_SPW + j) + q;
+        return 4 * ((round * W + k) * FE_SPW + j) + q;
     };
     u32x4 c[NR][FE_SPW];
     auto load = [&](int round) __attribute__((always_inline)) {
@@ -309,9 +329,9 @@ __global__ __launch_bounds__(FE_THREADS, 8) void moe_few_kernel(const FewArgs p)
     load(0);
     // Scale bytes: the 16 rows of an operand are KB 16-byte units in a row.
     uint8_t *const sl = smem + (size_t)few_rows(p.T) * pitch;
-    const int su = NR * FE_G * KB;
+    const int su = NR * G * KB;
     auto scale_unit = [&](int i) __attribute__((always_inline)) {
-        const int op = i / KB, at = i - op * KB, n = min((slice * FE_G + op / NR) * 16, p.N - 16);
+        const int op = i / KB, at = i - op * KB, n = min((slice * G + op / NR) * 16, p.N - 16);
         return reinterpret_cast<const u32x4 *>(
             p.ws + ((size_t)e * NR * p.N + (size_t)(op % NR) * p.N + n) * KB)[at];
     };
@@ -321,26 +341,25 @@ __global__ __launch_bounds__(FE_THREADS, 8) void moe_few_kernel(const FewArgs p)
     const uint16_t *const rows = UP ? p.x : p.f.a;
     auto x_unit = [&](int i) __attribute__((always_inline)) {
         const int m = i / nv, at = i - m * nv;
-        const int src = UP ? pair_of[m] / p.topk : pair_of[m];
         u32x4 v{0, 0, 0, 0};
         if (at < nx)
-            v = reinterpret_cast<const u32x4 *>(rows + (size_t)src * p.K)[at];
+            v = reinterpret_cast<const u32x4 *>(rows + (size_t)row_of[m] * p.K)[at];
         return v;
     };
     constexpr int XB = 2; // units of a thread under way at a time
-    for (int i0 = tid; i0 < pairs * nv; i0 += XB * FE_THREADS) {
+    for (int i0 = tid; i0 < pairs * nv; i0 += XB * NT) {
         u32x4 v[XB];
 #pragma unroll
         for (int i = 0; i < XB; ++i)
-            v[i] = x_unit(min(i0 + i * FE_THREADS, pairs * nv - 1));
+            v[i] = x_unit(min(i0 + i * NT, pairs * nv - 1));
 #pragma unroll
         for (int i = 0; i < XB; ++i)
-            if (i0 + i * FE_THREADS < pairs * nv)
-                reinterpret_cast<u32x4 *>(smem)[i0 + i * FE_THREADS] = v[i];
+            if (i0 + i * NT < pairs * nv)
+                reinterpret_cast<u32x4 *>(smem)[i0 + i * NT] = v[i];
     }
     if (tid < su)
         reinterpret_cast<u32x4 *>(sl)[tid] = sv;
-    for (int i = tid + FE_THREADS; i < su; i += FE_THREADS)
+    for (int i = tid + NT; i < su; i += NT)
         reinterpret_cast<u32x4 *>(sl)[i] = scale_unit(i);
     __syncthreads();
 
@@ -384,7 +403,7 @@ __global__ __launch_bounds__(FE_THREADS, 8) void moe_few_kernel(const FewArgs p)
         return;
 #pragma unroll
     for (int o = 0; o < NR; ++o)
-        for (int j = 1; j < FE_W; ++j)
+        for (int j = 1; j < W; ++j)
             acc[o] += part[((wave + j) * NR + o) * 64 + lane];
     const int pair = pair_of[r];
     const size_t to = (size_t)pair * p.N + c0 + 4 * q;
@@ -410,10 +429,22 @@ __global__ __launch_bounds__(256) void moe_few_join_kernel(const float *__restri
     if (h >= H)
         return;
     f32x4 v{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < topk; ++s) {
-        const int p = t * topk + s;
-        if (ids[p] >= 0)
-            v += *reinterpret_cast<const f32x4 *>(pre + (size_t)p * H + h);
+    const int32_t *const id = ids + t * topk;
+    const float *const row = pre + (size_t)t * topk * H + h;
+    constexpr int B = 8; // places under way at a time (a place without an expert has no row: not added)
+    for (int s0 = 0; s0 < topk; s0 += B) {
+        f32x4 a[B];
+        bool on[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int s = min(s0 + i, topk - 1);
+            a[i] = *reinterpret_cast<const f32x4 *>(row + (size_t)s * H);
+            on[i] = s0 + i < topk && id[s] >= 0;
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            if (on[i])
+                v += a[i];
     }
     *reinterpret_cast<uint2 *>(y + (size_t)t * H + h) =
         uint2{f32x2_to_act2<DT_BF16>(v[0], v[1]), f32x2_to_act2<DT_BF16>(v[2], v[3])};
@@ -424,22 +455,31 @@ bool layer_few(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
 {
     constexpr size_t most = 150 * 1024;
     return T <= MF_TOKENS && T * topk <= MF_PAIRS && E <= MF_EXPERTS && H <= 32768 && I <= 32768 &&
-           few_lds((int)T, (int)H, true) <= most && few_lds((int)T, (int)I, false) <= most;
+           few_lds<true, 4, 2>((int)T, (int)H) <= most && few_lds<false, 4, 2>((int)T, (int)I) <= most;
 }
 
-template <bool UP, bool ONE, int V>
-hipError_t launch_few(const FewArgs &a, hipStream_t stream)
+template <bool UP, bool ONE, int V, int W, int G>
+hipError_t launch_few_as(FewArgs a, hipStream_t stream)
 {
-    auto kern = moe_few_kernel<UP, ONE, V>;
+    auto kern = moe_few_kernel<UP, ONE, V, W, G>;
     static std::atomic<uint64_t> lds_set{0};
     if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), 156 * 1024, lds_set);
         e != hipSuccess)
         return e;
     // units: at most one for every pair, one for every expert and FE_UNIT of its pairs
     const int P = a.T * a.topk, units = std::min(P, a.E * ((a.T + FE_UNIT - 1) / FE_UNIT));
-    hipLaunchKernelGGL(kern, dim3((unsigned)(units * a.slices)), dim3(FE_THREADS), few_lds(a.T, a.K, UP),
-                       stream, a);
+    a.slices = (a.N + 16 * G - 1) / (16 * G);
+    const size_t lds = few_lds<UP, W, G>(a.T, a.K);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(units * a.slices)), dim3(64 * W * G), lds, stream, a);
     return hipGetLastError();
+}
+
+template <bool UP, bool ONE, int V>
+hipError_t launch_few(const FewArgs &a, hipStream_t stream)
+{
+    if (ONE || a.T <= FE_NARROW)
+        return launch_few_as<UP, ONE, V, 8, 1>(a, stream);
+    return launch_few_as<UP, false, V, 4, 2>(a, stream);
 }
 
 hipError_t launch_layer_few(const MoeLayerArgs &m, void *workspace, hipStream_t stream)
@@ -471,7 +511,6 @@ hipError_t launch_layer_few(const MoeLayerArgs &m, void *workspace, hipStream_t 
     a.ws = m.w1s;
     a.K = m.H;
     a.N = m.I;
-    a.slices = (m.I + 16 * FE_G - 1) / (16 * FE_G);
     if (m.T > 1)
         e = launch_few<true, false, 1>(a, stream);
     else if (m.E <= 32)
@@ -484,7 +523,6 @@ hipError_t launch_layer_few(const MoeLayerArgs &m, void *workspace, hipStream_t 
     a.ws = m.w2s;
     a.K = m.I;
     a.N = m.H;
-    a.slices = (m.H + 16 * FE_G - 1) / (16 * FE_G);
     e = launch_few<false, false, 1>(a, stream);
     if (e != hipSuccess)
         return e;
