@@ -89,10 +89,12 @@ hipError_t launch_topk_v(const void *logits, const float *bias, int32_t *ids, fl
 constexpr int FE_NARROW = 8;    // tokens with W = 8, G = 1, at most; more: W = 4, G = 2
 constexpr int FE_SPW = 3;       // steps of a wave at a time
 constexpr int FE_UNIT = 8;      // pairs of a unit, at most
-constexpr int MF_TOKENS = 32;   // tokens, at most: 16 lanes each in the choice
+// Tokens, at most: 16 lanes each in the choice.  64 take 144 us here and 164 through
+// the tile kernels of the two stages, which 33 take as well (here 105).
+constexpr int MF_TOKENS = 64;
 constexpr int MF_PAIRS = 512;   // pairs, at most
 constexpr int MF_EXPERTS = 256; // experts, at most: 16 scores a lane
-constexpr int RT_THREADS = 512;
+constexpr int RT_THREADS = 1024;
 static_assert(RT_THREADS / 16 >= MF_TOKENS, "every token has its lanes");
 
 struct alignas(16) FewUnit {
