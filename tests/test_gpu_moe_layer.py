@@ -97,6 +97,34 @@ def test_choice_masks(wob, dtype, E, topk):
     _choice(wob, l, topk, torch.full((E,), -inf))
 
 
+@pytest.mark.parametrize("E,topk", [(3, 2), (32, 4), (33, 8), (128, 3), (256, 8), (260, 8)])
+def test_choice_zeros_of_both_signs_are_equal_scores(wob, E, topk):
+    """-0 + -0 is -0 and 0 + -0 is 0: the same score, so the lowest expert comes first."""
+    torch = torch_mod()
+    g = torch.Generator().manual_seed(E)
+    l = torch.where(torch.rand((50, E), generator=g) < 0.5, 0.0, -0.0)
+    _choice(wob, l, topk, torch.full((E,), -0.0))
+    _choice(wob, l, topk, torch.zeros(E), False)
+    _choice(wob, l, topk)
+
+
+@pytest.mark.parametrize("E", [64, 100, 128, 200, 256, 512])
+@pytest.mark.parametrize("topk", [8, 16, 17])
+def test_choice_ties_in_some_rows(wob, E, topk):
+    """Rows with equal scores at, above and below the last place, beside rows without."""
+    torch = torch_mod()
+    g = torch.Generator().manual_seed(E + topk)
+    l = torch.randn((96, E), generator=g)
+    top = l.sort(-1, descending=True).values
+    l[3, 0] = l[3, E - 1] = top[3, topk - 1]      # a second one at the last place
+    l[9, 5], l[9, 50] = top[9, 0] + 1, top[9, 0] + 1
+    l[17, 7] = l[17, 8] = top[17, -1] - 1          # far below it
+    l[33] = 0.25
+    l[34, :-3] = -float("inf")
+    _choice(wob, l, topk)
+    _choice(wob, l, topk, None, False)
+
+
 def test_choice_empty_batch(wob):
     torch = torch_mod()
     ids, w = wob.moe_topk(torch.empty((0, 8), device="cuda"), 2)

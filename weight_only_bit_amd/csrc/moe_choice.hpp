@@ -1,5 +1,5 @@
 // The choice of a token's experts, shared by the stand-alone kernel and the
-// mixture-of-experts layer (both give the same bits).
+// mixture-of-experts layer.
 //
 // With l_e = logit_e + bias_e in binary32 (NaN counts as -inf):
 //     ids     = the topk largest l_e > -inf, largest first, ties to the lowest e
@@ -9,12 +9,20 @@
 // Where the maximum is +inf, exp(l - max) is read as its limit: 1 for the
 // experts at +inf and 0 for the others.
 //
-// L lanes share a token, lane g of them holding experts v L + g in V registers
-// as unsigned keys of the same order.  A place costs one maximum of the keys,
-// then the lowest index that has it; both are reduced over the lanes with
-// cross-lane operands of the vector ALU (no LDS round trip) for L = 16, so four
-// tokens of a wave are chosen at once: E = 256, topk = 8, 16384 tokens take
-// 16 us (14.4 in a kernel trace), where one token a wave with shuffles took 25.
+// L lanes share a token, lane g of them holding experts v L + g (QUAD: 4 (v / 4) L +
+// 4 g + v % 4, loaded four at a time) in V registers as unsigned keys of the same
+// order; reductions over the lanes use cross-lane
+// operands of the vector ALU (no LDS round trip) for L = 16, so four tokens of a
+// wave are chosen at once.  Two ways to the same result:
+//  * one place after the other: the largest key, the lowest expert that has it,
+//    and that expert's key cleared (5 V operations a place);
+//  * for many registers: the topk largest different keys first, without clearing
+//    (the next one below k is the largest key - k in wrapping arithmetic: 1.5 V
+//    operations a place), then every lane finds which of its experts reach the last
+//    of them and their places by counting.  Equal keys show as a count above
+//    the number of places; that wave then goes the first way.
+// 16384 tokens, 256 experts, top 8: 9.6 us; the first way alone 14.2, one token a
+// wave with shuffles through LDS 25.
 #pragma once
 
 #include "wob_device.hpp"
@@ -41,6 +49,16 @@ __device__ __forceinline__ float logit_value(const void *p, int dt, int64_t at)
     return act_to_f32(static_cast<const uint16_t *>(p)[at], dt);
 }
 
+__device__ __forceinline__ float4_t logit_value4(const void *p, int dt, int64_t at) // at % 4 == 0
+{
+    if (dt == DT_F32)
+        return *reinterpret_cast<const float4_t *>(static_cast<const float *>(p) + at);
+    const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + at);
+    return float4_t{act_to_f32((uint16_t)(v.x & 0xFFFFu), dt), act_to_f32((uint16_t)(v.x >> 16), dt),
+                    act_to_f32((uint16_t)(v.y & 0xFFFFu), dt), act_to_f32((uint16_t)(v.y >> 16), dt)};
+}
+
+// exp(l - top) for l <= top; 1 where both are +inf, 0 for l = -inf below any top.
 __device__ __forceinline__ float exp_below(float l, float top)
 {
     return l == top ? 1.0f : __expf(l - top);
@@ -64,29 +82,50 @@ __device__ __forceinline__ uint32_t group_reduce(uint32_t v, F f)
 constexpr int CHOICE_MAX = 64; // places of a token, at most
 
 // One group of L lanes (g: the lane's place in it) chooses for one token, whose
-// scores begin at `row`.  On return lane g holds places g, g + L, ... in id[] and
-// weight[].  Every lane of the wave calls it with the same topk (a group without
-// a token passes E = 0).
-template <int L, int V>
+// scores begin at `row`: put(place, expert, weight) is called once for every place
+// below topk, by some lane of the group.  Every lane of the wave calls with the
+// same topk (a group without a token passes E = 0 and ignores what it is told).
+template <int L, int V, bool QUAD, class Put>
 __device__ __forceinline__ void choose(const void *logits, int dt, int64_t row, const float *bias,
-                                       int E, int topk, bool renormalize, int g,
-                                       int (&id)[CHOICE_MAX / L], float (&weight)[CHOICE_MAX / L])
+                                       int E, int topk, bool renormalize, int g, Put put)
 {
     auto umax = [](uint32_t a, uint32_t b) { return max(a, b); };
     auto umin = [](uint32_t a, uint32_t b) { return min(a, b); };
+    auto uadd = [](uint32_t a, uint32_t b) { return a + b; };
     auto fadd = [](uint32_t a, uint32_t b) {
         return bitcast<uint32_t>(bitcast<float>(a) + bitcast<float>(b));
     };
+    static_assert(!QUAD || V % 4 == 0, "whole loads");
+    auto expert = [&](int v) { return QUAD ? 4 * (v / 4) * L + 4 * g + v % 4 : v * L + g; };
+    float l[V];
     uint32_t key[V];
+    if constexpr (QUAD) { // E % 4 == 0
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            const int e = expert(v);
+            float4_t f = {0.f, 0.f, 0.f, 0.f};
+            if (e < E) {
+                f = logit_value4(logits, dt, row + e);
+                if (bias)
+                    f += *reinterpret_cast<const float4_t *>(bias + e);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                l[v + i] = f[i];
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = expert(v);
+            l[v] = e < E ? logit_value(logits, dt, row + e) + (bias ? bias[e] : 0.0f) : 0.f;
+        }
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = v * L + g;
-        float l = 0.f;
-        if (e < E) {
-            l = logit_value(logits, dt, row + e) + (bias ? bias[e] : 0.0f);
-            l = l != l ? -__builtin_inff() : l;
-        }
-        key[v] = e < E ? order_key(l) : 0u;
+        const bool in = expert(v) < E;
+        l[v] += 0.0f; // -0 becomes +0: the two are equal scores
+        l[v] = in && l[v] == l[v] ? l[v] : -__builtin_inff();
+        key[v] = in ? order_key(l[v]) : 0u;
     }
     auto best_key = [&]() {
         uint32_t k = key[0];
@@ -101,14 +140,82 @@ __device__ __forceinline__ void choose(const void *logits, int dt, int64_t row, 
     if (!renormalize) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (key[v] > KEY_NEG_INF)
-                total += exp_below(order_value(key[v]), top);
+            total += exp_below(l[v], top);
         total = bitcast<float>(group_reduce<L>(bitcast<uint32_t>(total), fadd));
     }
+
+    constexpr int NK = 16; // places of the second way, at most
+    if constexpr (V >= 8 && V <= 32) {
+        if (topk <= NK) {
+            uint32_t kept[NK]; // the largest different keys above -inf, zeros behind them
+            uint32_t last = k;
+            int n = 0;
+#pragma unroll
+            for (int s = 0; s < NK; ++s) {
+                kept[s] = 0u;
+                if (s < topk) {
+                    uint32_t c = k;
+                    if (s > 0) {
+                        uint32_t d = key[0] - last;
+#pragma unroll
+                        for (int v = 1; v < V; ++v)
+                            d = max(d, key[v] - last);
+                        c = group_reduce<L>(d, umax) + last; // not below `last` if nothing is
+                    }
+                    const bool on = n == s && c > KEY_NEG_INF && (s == 0 || c < last);
+                    kept[s] = on ? c : 0u;
+                    last = on ? c : last;
+                    n += on;
+                }
+            }
+            uint32_t mine = 0; // bit v: the expert of register v is chosen
+#pragma unroll
+            for (int v = V - 1; v >= 0; --v)
+                mine = mine << 1 | (uint32_t)(key[v] >= last);
+            mine = n ? mine : 0u;
+            const int found = (int)group_reduce<L>((uint32_t)__popc(mine), uadd);
+            if (!__any(found != n)) {
+                if (renormalize) {
+                    total = 0.f;
+#pragma unroll
+                    for (int s = 0; s < NK; ++s)
+                        if (s < topk)
+                            total += kept[s] ? exp_below(order_value(kept[s]), top) : 0.f;
+                }
+                while (__any(mine != 0u)) {
+                    if (mine != 0u) {
+                        const int v = __ffs(mine) - 1;
+                        mine &= mine - 1;
+                        float f = l[0];
+#pragma unroll
+                        for (int i = 1; i < V; ++i)
+                            f = v == i ? l[i] : f;
+                        const uint32_t own = order_key(f);
+                        int place = 0;
+#pragma unroll
+                        for (int s = 0; s < NK; ++s)
+                            place += kept[s] > own;
+                        put(place, expert(v), exp_below(f, top) / total);
+                    }
+                }
+                for (int s = n + g; s < topk; s += L)
+                    put(s, -1, 0.f);
+                return;
+            }
+        }
+    }
+
+    int id[CHOICE_MAX / L];
+    float weight[CHOICE_MAX / L];
 #pragma unroll
     for (int j = 0; j < CHOICE_MAX / L; ++j) {
         id[j] = -1;
         weight[j] = 0.f;
+    }
+    if (renormalize)
+        total = 0.f;
+#pragma unroll
+    for (int j = 0; j < CHOICE_MAX / L; ++j) {
         for (int s = 0; s < L; ++s) {
             if (j * L + s >= topk)
                 break;
@@ -118,7 +225,7 @@ __device__ __forceinline__ void choose(const void *logits, int dt, int64_t row, 
             uint32_t e = ~0u;
 #pragma unroll
             for (int v = V - 1; v >= 0; --v)
-                e = key[v] == k ? (uint32_t)(v * L + g) : e;
+                e = key[v] == k ? (uint32_t)expert(v) : e;
             e = group_reduce<L>(e, umin);
             const bool some = k > KEY_NEG_INF; // an expert above -inf is left
             const float p = some ? exp_below(order_value(k), top) : 0.f;
@@ -130,12 +237,13 @@ __device__ __forceinline__ void choose(const void *logits, int dt, int64_t row, 
             }
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                key[v] = some && e == (uint32_t)(v * L + g) ? 0u : key[v];
+                key[v] = some && e == (uint32_t)expert(v) ? 0u : key[v];
         }
     }
 #pragma unroll
     for (int j = 0; j < CHOICE_MAX / L; ++j)
-        weight[j] = id[j] < 0 ? 0.f : weight[j] / total;
+        if (j * L + g < topk)
+            put(j * L + g, id[j], id[j] < 0 ? 0.f : weight[j] / total);
 }
 
 } // namespace wob

@@ -13,23 +13,19 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 constexpr int CH_THREADS = 256;
 
-template <int DT, int L, int V>
+template <int DT, int L, int V, bool QUAD>
 __global__ __launch_bounds__(CH_THREADS) void moe_topk_kernel(
     const void *__restrict__ logits, const float *__restrict__ bias, int32_t *__restrict__ ids,
     float *__restrict__ weights, int T, int E, int topk, bool renormalize)
 {
     const int t = blockIdx.x * (CH_THREADS / L) + threadIdx.x / L, g = threadIdx.x % L;
-    int id[CHOICE_MAX / L];
-    float w[CHOICE_MAX / L];
-    choose<L, V>(logits, DT, (int64_t)t * E, bias, t < T ? E : 0, topk, renormalize, g, id, w);
-    if (t >= T)
-        return;
-#pragma unroll
-    for (int j = 0; j < CHOICE_MAX / L; ++j)
-        if (j * L + g < topk) {
-            ids[(int64_t)t * topk + j * L + g] = id[j];
-            weights[(int64_t)t * topk + j * L + g] = w[j];
-        }
+    choose<L, V, QUAD>(logits, DT, (int64_t)t * E, bias, t < T ? E : 0, topk, renormalize, g,
+                 [&](int place, int id, float w) {
+                     if (t < T) {
+                         ids[(int64_t)t * topk + place] = id;
+                         weights[(int64_t)t * topk + place] = w;
+                     }
+                 });
 }
 
 template <int DT, int L, int V>
@@ -49,8 +45,16 @@ hipError_t launch_topk_v(const void *logits, const float *bias, int32_t *ids, fl
                                                 stream);
     }
     constexpr int PER = CH_THREADS / L; // tokens per workgroup
-    hipLaunchKernelGGL((moe_topk_kernel<DT, L, V>), dim3((T + PER - 1) / PER), dim3(CH_THREADS), 0,
-                       stream, logits, bias, ids, weights, T, E, topk, renormalize);
+    const dim3 grid((unsigned)((T + PER - 1) / PER));
+    if constexpr (V % 4 == 0) {
+        if (E % 4 == 0) {
+            hipLaunchKernelGGL((moe_topk_kernel<DT, L, V, true>), grid, dim3(CH_THREADS), 0, stream, logits,
+                               bias, ids, weights, T, E, topk, renormalize);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((moe_topk_kernel<DT, L, V, false>), grid, dim3(CH_THREADS), 0, stream, logits, bias,
+                       ids, weights, T, E, topk, renormalize);
     return hipGetLastError();
 }
 
@@ -152,22 +156,17 @@ __global__ __launch_bounds__(RT_THREADS) void moe_few_route_kernel(const FewArgs
         hits[e] = 0;
     __syncthreads();
     const int t = tid >> 4, g = tid & 15;
-    int id[CHOICE_MAX / 16];
-    float wt[CHOICE_MAX / 16];
-    choose<16, V>(p.logits, p.dt, (int64_t)t * p.E, p.bias, t < p.T ? p.E : 0, p.topk,
-                  p.renormalize != 0, g, id, wt);
-    if (t < p.T) {
-#pragma unroll
-        for (int j = 0; j < CHOICE_MAX / 16; ++j)
-            if (16 * j + g < p.topk) {
-                const int i = t * p.topk + 16 * j + g;
-                sid[i] = id[j];
-                sw[i] = wt[j];
-                p.f.ids[i] = id[j];
-                if (id[j] >= 0)
-                    atomicAdd(&hits[id[j]], 1);
-            }
-    }
+    choose<16, V, false>(p.logits, p.dt, (int64_t)t * p.E, p.bias, t < p.T ? p.E : 0, p.topk,
+                  p.renormalize != 0, g, [&](int place, int id, float w) {
+                      if (t < p.T) {
+                          const int i = t * p.topk + place;
+                          sid[i] = id;
+                          sw[i] = w;
+                          p.f.ids[i] = id;
+                          if (id >= 0)
+                              atomicAdd(&hits[id], 1);
+                      }
+                  });
     __syncthreads();
     if (wave == 0) { // units before each expert's
         int n = 0;
@@ -252,20 +251,14 @@ __global__ __launch_bounds__(64 * W * G, 8) void moe_few_kernel(const FewArgs p)
         // places with an expert come first, so place i is unit i
         __shared__ int32_t id[CHOICE_MAX];
         __shared__ float wt[CHOICE_MAX];
-        if (wave == 0) {
-            int cid[CHOICE_MAX / 16];
-            float cw[CHOICE_MAX / 16];
-            choose<16, V>(p.logits, p.dt, 0, p.bias, lane < 16 ? p.E : 0, p.topk, p.renormalize != 0,
-                          lane & 15, cid, cw);
-            if (lane < 16) {
-#pragma unroll
-                for (int j = 0; j < CHOICE_MAX / 16; ++j)
-                    if (16 * j + lane < p.topk) {
-                        id[16 * j + lane] = cid[j];
-                        wt[16 * j + lane] = cw[j];
-                    }
-            }
-        }
+        if (wave == 0)
+            choose<16, V, false>(p.logits, p.dt, 0, p.bias, lane < 16 ? p.E : 0, p.topk, p.renormalize != 0,
+                          lane & 15, [&](int place, int c, float w) {
+                              if (lane < 16) {
+                                  id[place] = c;
+                                  wt[place] = w;
+                              }
+                          });
         __syncthreads();
         if (blockIdx.x == 0) {
             int n = 0;
