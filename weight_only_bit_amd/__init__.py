@@ -18,6 +18,8 @@ Layouts are those of ``include/weight_only_bit.h``.
 """
 from __future__ import annotations
 
+import functools
+
 from . import _lib
 from ._lib import (ACT_NONE, ACT_SILU_MUL, BF16, DTYPE, F16, F32, INVALID_ARG, OK, PATH_AUTO,
                    PATH_SKINNY, PATH_TILED, U4X8_I32, UNSUPPORTED, WobArgError, WobDtypeError,
@@ -34,20 +36,22 @@ __all__ = [
 
 _torch_mod = None
 _tags = None
-_raw_stream = None
+_raw_stream = _get_device = _values = _bytes = None
 
 
 def _torch():
-    """torch, imported on first use; the dtype tags and the stream query with it."""
-    global _torch_mod, _tags, _raw_stream
+    """torch, imported on first use; the dtype tags and the device and stream queries with it."""
+    global _torch_mod, _tags, _values, _bytes, _raw_stream, _get_device
     if _torch_mod is None:
         import torch
         _tags = {torch.float16: F16, torch.bfloat16: BF16, torch.int32: U4X8_I32,
                  torch.float32: F32}
+        _values, _bytes = (torch.float16, torch.bfloat16, torch.float32), (torch.uint8,)
         # the current stream's handle without building a Stream object: 0.1
         # against 1.9 us, in calls whose launch takes 3
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _torch_mod = torch
     return _torch_mod
 
@@ -61,28 +65,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(device):
-    _torch()
-    return _raw_stream(device.index)
-
-
-class _Here:
-    """The context of a device that is current already."""
-
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_HERE = _Here()
-
-
-def _on(device):
-    """torch.cuda.device(device), which costs 1.3 us, only where it changes the device."""
-    cuda = _torch().cuda
-    return _HERE if cuda.current_device() == device.index else cuda.device(device)
+def _run(fn, device, *args):
+    """fn(*args, stream) with `device` current, on its current stream.  (Entering
+    torch.cuda.device costs 1.3 us, so it is done only where it changes the device.)"""
+    index = device.index
+    if _get_device() == index:
+        return fn(*args, _raw_stream(index))
+    with _torch_mod.cuda.device(index):
+        return fn(*args, _raw_stream(index))
 
 
 def _check_device(*tensors):
@@ -107,6 +97,8 @@ def _check_device(*tensors):
 
 def _want(t, name, shape, dtypes):
     """t must exist, have exactly `shape`, and one of `dtypes`."""
+    if t is not None and t.shape == shape and t.dtype in dtypes:
+        return
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype not in dtypes:
@@ -164,11 +156,9 @@ def gemm(x, qweight, scales, qzeros, group_size: int, out=None, path: int = PATH
         out = torch.empty((M, N), dtype=x.dtype, device=x.device)
     _want(out, "out", (M, N), (x.dtype,))
     dev = _check_device(x, qweight, scales, qzeros, out)
-    with _on(dev):
-        st = _lib.lib().w4a16_gemm_ex(
-            _ptr(x), _tag(x), _ptr(qweight), _ptr(scales), _tag(scales), _ptr(qzeros),
-            _tag(qzeros) if qzeros is not None else U4X8_I32, _ptr(out), M, N, K, group_size,
-            path, _stream(dev))
+    st = _run(_lib.lib().w4a16_gemm_ex, dev, _ptr(x), _tag(x), _ptr(qweight), _ptr(scales),
+               _tag(scales), _ptr(qzeros), _tag(qzeros) if qzeros is not None else U4X8_I32,
+               _ptr(out), M, N, K, group_size, path)
     _lib.check(st, "w4a16_gemm")
     return out
 
@@ -189,11 +179,9 @@ def gemm_grouped(x, m_offsets, qweight, scales, qzeros, group_size: int, out=Non
         out = torch.empty((total_m, N), dtype=x.dtype, device=x.device)
     _want(out, "out", (total_m, N), (x.dtype,))
     dev = _check_device(x, m_offsets, qweight, scales, qzeros, out)
-    with _on(dev):
-        st = _lib.lib().w4a16_gemm_grouped(
-            _ptr(x), _tag(x), _ptr(m_offsets), E, total_m, _ptr(qweight), _ptr(scales),
-            _tag(scales), _ptr(qzeros), _tag(qzeros) if qzeros is not None else U4X8_I32,
-            _ptr(out), N, K, group_size, _stream(dev))
+    st = _run(_lib.lib().w4a16_gemm_grouped, dev, _ptr(x), _tag(x), _ptr(m_offsets), E, total_m,
+               _ptr(qweight), _ptr(scales), _tag(scales), _ptr(qzeros), _tag(qzeros) if qzeros is
+               not None else U4X8_I32, _ptr(out), N, K, group_size)
     _lib.check(st, "w4a16_gemm_grouped")
     return out
 
@@ -238,15 +226,11 @@ def mxfp4_moe_gemm(x, topk_ids, w_fp4, w_scale, out=None, workspace=None, act: i
     if ws_bytes < need:
         raise ValueError(f"workspace holds {ws_bytes} bytes; {need} are needed")
     dev = _check_device(x, topk_ids, w_fp4, w_scale, out, workspace)
-    with _on(dev):
-        if tile_m == 32:
-            st = _lib.lib().mxfp4_moe_gemm(
-                _ptr(x), _ptr(topk_ids), _ptr(w_fp4), _ptr(w_scale), _ptr(out), T, topk, E, N, K,
-                act, _ptr(workspace), ws_bytes, _stream(dev))
-        else:
-            st = _lib.lib().mxfp4_moe_gemm_tile_m(
-                _ptr(x), _ptr(topk_ids), _ptr(w_fp4), _ptr(w_scale), _ptr(out), T, topk, E, N, K,
-                act, tile_m, _ptr(workspace), ws_bytes, _stream(dev))
+    args = (_ptr(x), _ptr(topk_ids), _ptr(w_fp4), _ptr(w_scale), _ptr(out), T, topk, E, N, K, act)
+    if tile_m == 32:
+        st = _run(_lib.lib().mxfp4_moe_gemm, dev, *args, _ptr(workspace), ws_bytes)
+    else:
+        st = _run(_lib.lib().mxfp4_moe_gemm_tile_m, dev, *args, tile_m, _ptr(workspace), ws_bytes)
     _lib.check(st, "mxfp4_moe_gemm")
     return out
 
@@ -283,17 +267,15 @@ def mxfp4_moe_stage2(a, topk_ids, topk_weights, w2_fp4, w2_scale, out=None, work
     if ws_bytes < need:
         raise ValueError(f"workspace holds {ws_bytes} bytes; {need} are needed")
     dev = _check_device(a, topk_ids, topk_weights, w2_fp4, w2_scale, out, workspace)
-    with _on(dev):
-        st = _lib.lib().mxfp4_moe_stage2(
-            _ptr(a), _ptr(topk_ids), _ptr(topk_weights), _ptr(w2_fp4), _ptr(w2_scale), _ptr(out),
-            T, topk, E, H, I, _ptr(workspace), ws_bytes, _stream(dev))
+    st = _run(_lib.lib().mxfp4_moe_stage2, dev, _ptr(a), _ptr(topk_ids), _ptr(topk_weights),
+               _ptr(w2_fp4), _ptr(w2_scale), _ptr(out), T, topk, E, H, I, _ptr(workspace), ws_bytes)
     _lib.check(st, "mxfp4_moe_stage2")
     return out
 
 
 def _value_dtypes():
-    torch = _torch()
-    return (torch.float16, torch.bfloat16, torch.float32)
+    _torch()
+    return _values
 
 
 def _workspace(workspace, need, device):
@@ -335,18 +317,18 @@ def mxfp4_quantize(x, out=None, out_scale=None):
         out = torch.empty((*lead, K // 2), dtype=torch.uint8, device=x.device)
     if out_scale is None:
         out_scale = torch.empty((*lead, K // 32), dtype=torch.uint8, device=x.device)
-    _want(out, "out", (*lead, K // 2), (torch.uint8,))
-    _want(out_scale, "out_scale", (*lead, K // 32), (torch.uint8,))
+    _want(out, "out", (*lead, K // 2), _bytes)
+    _want(out_scale, "out_scale", (*lead, K // 32), _bytes)
     dev = _check_device(out, out_scale)
     if x.device != dev:
         raise ValueError("operands live on different devices")
-    with _on(dev):
-        st = _lib.lib().mxfp4_quantize(_ptr(x), _tag(x), ldx, _ptr(out), _ptr(out_scale), R, K,
-                                       _stream(dev))
+    st = _run(_lib.lib().mxfp4_quantize, dev, _ptr(x), _tag(x), ldx, _ptr(out), _ptr(out_scale), R,
+               K)
     _lib.check(st, "mxfp4_quantize")
     return out, out_scale
 
 
+@functools.lru_cache(maxsize=256)
 def mxfp4_gemm_workspace_size(M: int, N: int, K: int) -> int:
     """Bytes of workspace mxfp4_gemm needs (0 also for arguments it refuses)."""
     return int(_lib.lib().mxfp4_gemm_workspace_size(M, N, K))
@@ -363,10 +345,10 @@ def mxfp4_gemm(x_fp4, x_scale, w_fp4, w_scale, out=None, out_dtype=None, workspa
     N = w_fp4.shape[0]
     if K < 32 or K % 32 != 0:
         raise ValueError(f"K={K} must be a multiple of 32 (one E8M0 scale per 32)")
-    _want(x_fp4, "x_fp4", (M, K // 2), (torch.uint8,))
-    _want(x_scale, "x_scale", (M, K // 32), (torch.uint8,))
-    _want(w_fp4, "w_fp4", (N, K // 2), (torch.uint8,))
-    _want(w_scale, "w_scale", (N, K // 32), (torch.uint8,))
+    _want(x_fp4, "x_fp4", (M, K // 2), _bytes)
+    _want(x_scale, "x_scale", (M, K // 32), _bytes)
+    _want(w_fp4, "w_fp4", (N, K // 2), _bytes)
+    _want(w_scale, "w_scale", (N, K // 32), _bytes)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
     if out_dtype not in _value_dtypes():
@@ -376,9 +358,8 @@ def mxfp4_gemm(x_fp4, x_scale, w_fp4, w_scale, out=None, out_dtype=None, workspa
     _want(out, "out", (M, N), (out_dtype,))
     workspace, ws_bytes = _workspace(workspace, mxfp4_gemm_workspace_size(M, N, K), x_fp4.device)
     dev = _check_device(x_fp4, x_scale, w_fp4, w_scale, out, workspace)
-    with _on(dev):
-        st = _lib.lib().mxfp4_gemm(_ptr(x_fp4), _ptr(x_scale), _ptr(w_fp4), _ptr(w_scale), _ptr(out),
-                                   _tag(out), M, N, K, _ptr(workspace), ws_bytes, _stream(dev))
+    st = _run(_lib.lib().mxfp4_gemm, dev, _ptr(x_fp4), _ptr(x_scale), _ptr(w_fp4), _ptr(w_scale),
+               _ptr(out), _tag(out), M, N, K, _ptr(workspace), ws_bytes)
     _lib.check(st, "mxfp4_gemm")
     return out
 
@@ -411,13 +392,13 @@ def moe_topk(logits, topk: int, bias=None, renormalize: bool = True, ids=None, w
     _want(ids, "ids", (T, topk), (torch.int32,))
     _want(weights, "weights", (T, topk), (torch.float32,))
     dev = _check_device(logits, bias, ids, weights)
-    with _on(dev):
-        st = _lib.lib().moe_topk(_ptr(logits), _tag(logits), _ptr(bias), _ptr(ids), _ptr(weights),
-                                 T, E, topk, int(bool(renormalize)), _stream(dev))
+    st = _run(_lib.lib().moe_topk, dev, _ptr(logits), _tag(logits), _ptr(bias), _ptr(ids),
+               _ptr(weights), T, E, topk, int(bool(renormalize)))
     _lib.check(st, "moe_topk")
     return ids, weights
 
 
+@functools.lru_cache(maxsize=256)
 def moe_layer_workspace_size(T: int, topk: int, E: int, H: int, I: int) -> int:
     """Bytes of workspace mxfp4_moe_layer needs (0 for arguments it refuses)."""
     return int(_lib.lib().mxfp4_moe_layer_workspace_size(T, topk, E, H, I))
@@ -437,20 +418,18 @@ def mxfp4_moe_layer(x, logits, topk: int, w1_fp4, w1_scale, w2_fp4, w2_scale, bi
     if H < 64 or I < 64 or H % 64 != 0 or I % 64 != 0:
         raise ValueError(f"H={H} and I={I} must be multiples of 64")
     _want(x, "x", (T, H), (torch.bfloat16,))
-    _want(w1_fp4, "w1_fp4", (E, 2 * I, H // 2), (torch.uint8,))
-    _want(w1_scale, "w1_scale", (E, 2 * I, H // 32), (torch.uint8,))
-    _want(w2_fp4, "w2_fp4", (E, H, I // 2), (torch.uint8,))
-    _want(w2_scale, "w2_scale", (E, H, I // 32), (torch.uint8,))
+    _want(w1_fp4, "w1_fp4", (E, 2 * I, H // 2), _bytes)
+    _want(w1_scale, "w1_scale", (E, 2 * I, H // 32), _bytes)
+    _want(w2_fp4, "w2_fp4", (E, H, I // 2), _bytes)
+    _want(w2_scale, "w2_scale", (E, H, I // 32), _bytes)
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _want(out, "out", (T, H), (torch.bfloat16,))
     workspace, ws_bytes = _workspace(workspace, moe_layer_workspace_size(T, topk, E, H, I), x.device)
     dev = _check_device(x, logits, bias, w1_fp4, w1_scale, w2_fp4, w2_scale, out, workspace)
-    with _on(dev):
-        st = _lib.lib().mxfp4_moe_layer(
-            _ptr(x), _ptr(logits), _tag(logits), _ptr(bias), _ptr(w1_fp4), _ptr(w1_scale),
-            _ptr(w2_fp4), _ptr(w2_scale), _ptr(out), T, topk, E, H, I, int(bool(renormalize)),
-            _ptr(workspace), ws_bytes, _stream(dev))
+    st = _run(_lib.lib().mxfp4_moe_layer, dev, _ptr(x), _ptr(logits), _tag(logits), _ptr(bias),
+               _ptr(w1_fp4), _ptr(w1_scale), _ptr(w2_fp4), _ptr(w2_scale), _ptr(out), T, topk, E, H,
+               I, int(bool(renormalize)), _ptr(workspace), ws_bytes)
     _lib.check(st, "mxfp4_moe_layer")
     return out
 
@@ -470,11 +449,9 @@ def w4a16_dequant(qweight, scales, qzeros, group_size: int, out_dtype=None):
         raise TypeError("out_dtype must be float32 or the scales' dtype")
     out = torch.empty((N, K), dtype=out_dtype, device=qweight.device)
     dev = _check_device(qweight, scales, qzeros, out)
-    with _on(dev):
-        st = _lib.lib().w4a16_dequant(
-            _ptr(qweight), _ptr(scales), _tag(scales), _ptr(qzeros),
-            _tag(qzeros) if qzeros is not None else U4X8_I32, _ptr(out), _tag(out), N, K,
-            group_size, _stream(dev))
+    st = _run(_lib.lib().w4a16_dequant, dev, _ptr(qweight), _ptr(scales), _tag(scales),
+               _ptr(qzeros), _tag(qzeros) if qzeros is not None else U4X8_I32, _ptr(out), _tag(out),
+               N, K, group_size)
     _lib.check(st, "w4a16_dequant")
     return out
 
@@ -487,12 +464,11 @@ def mxfp4_dequant(w_fp4, w_scale):
     N, K = w_fp4.shape[0], w_fp4.shape[1] * 2
     if K % 32 != 0:
         raise ValueError(f"K={K} must be a multiple of 32")
-    _want(w_fp4, "w_fp4", (N, K // 2), (torch.uint8,))
-    _want(w_scale, "w_scale", (N, K // 32), (torch.uint8,))
+    _want(w_fp4, "w_fp4", (N, K // 2), _bytes)
+    _want(w_scale, "w_scale", (N, K // 32), _bytes)
     out = torch.empty((N, K), dtype=torch.bfloat16, device=w_fp4.device)
     dev = _check_device(w_fp4, w_scale, out)
-    with _on(dev):
-        st = _lib.lib().mxfp4_dequant(_ptr(w_fp4), _ptr(w_scale), _ptr(out), N, K, _stream(dev))
+    st = _run(_lib.lib().mxfp4_dequant, dev, _ptr(w_fp4), _ptr(w_scale), _ptr(out), N, K)
     _lib.check(st, "mxfp4_dequant")
     return out
 
@@ -504,6 +480,5 @@ def stream_read(buf, nbytes: int, sink) -> None:
     if nbytes > buf.numel() * buf.element_size() or sink.numel() * sink.element_size() < 1024:
         raise ValueError("buffer smaller than nbytes or sink under 1024 bytes")
     dev = _check_device(buf, sink)
-    with _on(dev):
-        st = _lib.lib().wob_stream_read(_ptr(buf), nbytes, _ptr(sink), _stream(dev))
+    st = _run(_lib.lib().wob_stream_read, dev, _ptr(buf), nbytes, _ptr(sink))
     _lib.check(st, "wob_stream_read")
