@@ -193,6 +193,13 @@ def test_product_long_rows(wob, M, N, K):
     _check(wob, _operands(M, N, K, 3, 120, 123), "fp32")
 
 
+@pytest.mark.parametrize("M,N,K", [(1000, 1096, 6144), (1000, 1096, 6240), (1000, 1032, 6560),
+                                   (1100, 2040, 6176), (70, 9224, 6336), (127, 5000, 12288)])
+def test_product_many_rows_long(wob, M, N, K):
+    """Too few tiles for the largest one and rows too long for the smallest."""
+    _check(wob, _operands(M, N, K, 5, 117, 121), "fp32")
+
+
 @pytest.mark.parametrize("M", [1, 5, 40, 140, 300])
 def test_product_extreme_scales(wob, M):
     """Scale bytes at both ends whose products are ordinary numbers, and a NaN scale: it

@@ -222,7 +222,7 @@ hipError_t launch_few(const uint8_t *x, const uint8_t *xs, const uint8_t *w, con
 // by span, the 16 bytes of successive rows side by side, so that one copy takes
 // 64 rows.  2048 x 16384 x 5376: scales 8 bytes a row at a time 118 us, 16 bytes
 // 114, packed 110 with the packing; 100 x 5376 x 21504, where the scales are
-// a larger share, 29.7 us straight and 32.1 packed.  Rows that are not
+// a larger share, 2.4 us less straight than packed.  Rows that are not
 // 4-byte aligned (K % 128 != 0) are always packed.
 //
 // A stage is two MFMA steps of 64 k: in step j the lane half h = lane / 32
@@ -590,8 +590,17 @@ __global__ __launch_bounds__(256) void mxfp4_sum_kernel(const float4_t *__restri
     if (i >= n4)
         return;
     float4_t v = part[i];
-    for (int s = 1; s < splits; ++s)
-        v += part[(size_t)s * n4 + i];
+    constexpr int B = 4; // parts under way at a time
+    for (int s0 = 1; s0 < splits; s0 += B) {
+        float4_t a[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            a[j] = part[(size_t)min(s0 + j, splits - 1) * n4 + i];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            if (s0 + j < splits)
+                v += a[j];
+    }
     store4(y, ydt, (size_t)i * 4, v);
 }
 
@@ -639,31 +648,55 @@ hipError_t launch_tile(const uint8_t *x, const uint8_t *xs, const uint8_t *w, co
 }
 
 using TileL = MxTile<2, 4, 4, 4>; // 256 x 256
+using TileM = MxTile<2, 2, 2, 4>; // 128 x 128
 using TileS = MxTile<2, 1, 2, 4>; // 64 weight rows x 128 activation rows
 
 // Rows and scales of x must leave the LDS room for a second workgroup.
 bool few_rows(int64_t M, int64_t K) { return M <= 16 && K <= 65536 && few_lds((int)M, (int)K, 8, 2) <= 80 * 1024; }
 bool large_tile(int64_t M, int64_t N) { return ((M + 255) / 256) * ((N + 255) / 256) >= 128; }
 
+enum class Path { Few, Large, Medium, Small };
+
 struct Plan {
-    bool few, large, packed;
+    Path path;
+    bool packed;
     int splits;
 };
 
+// K parts for `tiles` tiles so that up to one workgroup reaches each CU, at least
+// two spans each.  A part costs its sums' way through memory and the launch that
+// adds them, about 4.5 us, so there is one only where it takes five spans off the
+// longest workgroup: 100 x 5760 x 2880 11.9 us whole and 13.9 in two parts,
+// 100 x 4096 x 3584 8.6 and 9.9 in three, 100 x 2048 x 4096 9.3 and 8.7 in four,
+// 100 x 512 x 5376 11.7 and 8.0 in five.  Two workgroups on each CU bring nothing:
+// 100 x 16384 x 5376 19.1 us with 256 and 26.3 with 512.
+int k_parts(int64_t tiles, int64_t K)
+{
+    const int64_t spans = (K + MX_SPAN - 1) / MX_SPAN;
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({256 / tiles, spans / 2, 16}));
+    return spans - (spans + parts - 1) / parts >= 5 ? (int)parts : 1;
+}
+
+template <class T>
+int64_t tile_count(int64_t M, int64_t N) { return ((M + T::TM - 1) / T::TM) * ((N + T::TN - 1) / T::TN); }
+
 Plan plan(int64_t M, int64_t N, int64_t K)
 {
-    Plan p;
-    p.few = few_rows(M, K);
-    p.large = !p.few && large_tile(M, N);
-    p.packed = !p.few && (p.large || K % 128 != 0);
-    p.splits = 1;
-    if (!p.few && !p.large) {
-        // K parts so that about two workgroups reach each CU, at least two spans each
-        const int64_t tiles = ((M + TileS::TM - 1) / TileS::TM) * ((N + TileS::TN - 1) / TileS::TN);
-        const int64_t spans = (K + MX_SPAN - 1) / MX_SPAN;
-        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, spans / 2, 16}));
-    }
-    return p;
+    if (few_rows(M, K))
+        return {Path::Few, false, 1};
+    if (large_tile(M, N))
+        return {Path::Large, true, 1};
+    const bool packed = K % 128 != 0;
+    const int64_t spans = (K + MX_SPAN - 1) / MX_SPAN;
+    const int small = k_parts(tile_count<TileS>(M, N), K);
+    // Where the small tile's parts are still long, a tile of twice the weight rows
+    // in more parts: 100 x 5376 x 21504 (14 spans a part) 24.9 us and 27.9 with the
+    // small one, 200 x 5376 x 21504 (42) 34 and 60; 100 x 5376 x 10752 (7 spans) 18.4
+    // and 17.8, 100 x 16384 x 5376 (11) 21.6 and 19.1.  Up to 64 rows, where half of
+    // it is idle, it brings little: 64 x 5376 x 21504 22.2 and 22.8.
+    if (M > 64 && spans > 11 * (int64_t)small)
+        return {Path::Medium, packed, k_parts(tile_count<TileM>(M, N), K)};
+    return {Path::Small, packed, small};
 }
 
 } // namespace
@@ -682,7 +715,7 @@ hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t 
                              void *workspace, hipStream_t stream)
 {
     const Plan p = plan(M, N, K);
-    if (p.few) {
+    if (p.path == Path::Few) {
         // Eight waves on a group of rows and two groups where that still makes 128
         // workgroups; with fewer rows one group each (2048 x 2048: 5.1 us with two
         // groups, 2.9 with one), four waves if K leaves them no more than a few steps.
@@ -693,8 +726,10 @@ hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t 
             return launch_few<8, 1>(x, xs, w, ws, y, ydt, M, N, K, stream);
         return launch_few<4, 1>(x, xs, w, ws, y, ydt, M, N, K, stream);
     }
-    if (p.large)
+    if (p.path == Path::Large)
         return launch_tile<TileL>(x, xs, w, ws, y, ydt, M, N, K, 1, p.packed, workspace, stream);
+    if (p.path == Path::Medium)
+        return launch_tile<TileM>(x, xs, w, ws, y, ydt, M, N, K, p.splits, p.packed, workspace, stream);
     return launch_tile<TileS>(x, xs, w, ws, y, ydt, M, N, K, p.splits, p.packed, workspace, stream);
 }
 
