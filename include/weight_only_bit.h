@@ -287,7 +287,7 @@ size_t mxfp4_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
  *  A scale byte of 255 (NaN) makes every output of its row (of x) or column
  *  (of w) NaN.
  *  K % 32 == 0, K >= 32, N % 8 == 0, M >= 0, N >= 0, M*K/2 and N*K/2 below
- *  2^32 (else WOB_INVALID_ARG).  M == 0 or N == 0 is a no-op returning WOB_OK.
+ *  2^32, M + N below 2^27 (else WOB_INVALID_ARG).  M == 0 or N == 0 is a no-op returning WOB_OK.
  *  workspace: device memory of at least mxfp4_gemm_workspace_size(M, N, K)
  *  bytes, 16-byte aligned (may be NULL when that is 0, else WOB_INVALID_ARG);
  *  its contents on entry do not matter.  Calls that share one workspace must
@@ -311,7 +311,7 @@ int mxfp4_gemm(const uint8_t *x_fp4, const uint8_t *x_scale, const uint8_t *w_fp
  *
  *  logits [T][E] of logits_dtype WOB_F16, WOB_BF16 or WOB_F32 (else
  *  WOB_DTYPE), bias [E] fp32 or NULL.
- *  T >= 0, 1 <= E <= 4096, 1 <= topk <= 64, topk <= E, T*topk below 2^31
+ *  T >= 0, 1 <= E <= 4096, 1 <= topk <= 64, topk <= E, T below 2^25
  *  (else WOB_INVALID_ARG).  T == 0 is a no-op returning WOB_OK.
  */
 int moe_topk(const void *logits, int logits_dtype, const float *bias, int32_t *ids, float *weights,
@@ -327,16 +327,18 @@ size_t mxfp4_moe_layer_workspace_size(int64_t T, int64_t topk, int64_t E, int64_
 /*
  * A whole mixture-of-experts layer, BF16 x MXFP4, from the router's scores:
  *   (id_s, p_s) = moe_topk(logits[t], bias, topk, renormalize)
- *   a_s = silu(W1g_e x[t]) * (W1u_e x[t]),  e = id_s, rounded to bf16
+ *   a_s = silu(W1g_e x[t]) * (W1u_e x[t]),  e = id_s
  *   y[t] = sum over s with id_s >= 0 of p_s * (W2_e a_s)
+ *  a_s is rounded once to bf16, the matrix instructions' operand type: by
+ *  itself, or for few tokens as p_s * a_s.
  *  x [T][H] bf16; logits, bias as for moe_topk; w1_fp4 [E][2I][H/2],
  *  w1_scale [E][2I][H/32] (gate rows 0 .. I-1, up rows I .. 2I-1); w2_fp4
  *  [E][H][I/2], w2_scale [E][H][I/32]; y [T][H] bf16.
  *  The function of moe_topk, mxfp4_moe_gemm (WOB_ACT_SILU_MUL) and
  *  mxfp4_moe_stage2 in turn; the sums are fp32 and their order may differ.
  *  H % 64 == 0, H >= 64, I % 64 == 0, I >= 64, T >= 0, 1 <= topk <= 64,
- *  topk <= E, 1 <= E <= 4096, T*H*2, T*topk*I*2, I*H and H*I/2 below 2^32
- *  (else WOB_INVALID_ARG).  T == 0 is a no-op returning WOB_OK.
+ *  topk <= E, 1 <= E <= 4096, T below 2^25, T*H*2, T*topk*I*2 and I*H below
+ *  2^32, E*I*H at most 2^40 (else WOB_INVALID_ARG).  T == 0 is a no-op returning WOB_OK.
  *  workspace: device memory of at least mxfp4_moe_layer_workspace_size(T,
  *  topk, E, H, I) bytes, 16-byte aligned; contents on entry do not matter.
  *  Calls that share one workspace must be ordered on one stream.

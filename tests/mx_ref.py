@@ -100,9 +100,9 @@ def layer(x, ids, weights, w1, w1s, w2, w2s):
 
     The kernel's pre-activations are off by at most H 2^-23 sum |x w1| (fp32
     sums), silu has slope below 1.1, exp and the quotient cost 2^-21, the
-    activated row is rounded to bf16 (2^-8), the I products and topk slots are
-    summed in fp32, and the weights are off by 2^-18 (choice_bound for scores
-    within 32 of the maximum and E <= 256)."""
+    activated row, by itself or weighted, is rounded to bf16 (2^-8), the I
+    products and topk slots are summed in fp32, and the weights are off by 2^-18
+    (choice_bound for scores within 32 of the maximum and E <= 256)."""
     T, H = x.shape
     I = w2.shape[2] * 2
     y, bound = np.zeros((T, H)), np.zeros((T, H))

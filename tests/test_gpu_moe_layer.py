@@ -304,3 +304,92 @@ def test_layer_captured_and_replayed(wob, T):
     ref, bound = R.layer(x.double().cpu().numpy(), ids, p, *ref_in)
     off = np.abs(y.double().cpu().numpy() - ref)
     assert (off <= R.rounded(ref, bound, "bf16")).all()
+
+
+@pytest.mark.parametrize("T,E,topk,H,I", [
+    (64, 16, 8, 128, 64), (65, 16, 8, 128, 64), (64, 16, 9, 128, 64),    # tokens, pairs at their limits
+    (8, 70, 64, 64, 64), (9, 70, 64, 64, 64), (57, 33, 9, 192, 64),
+    (5, 256, 6, 64, 128), (5, 257, 6, 64, 128), (1, 256, 64, 64, 64),    # experts
+    (1, 3, 2, 4160, 64), (3, 3, 2, 8192, 64), (9, 2, 1, 6208, 192),      # rows of several rounds
+    (1, 3, 2, 64, 4160), (3, 3, 2, 64, 8192), (9, 2, 1, 192, 6208),
+    (8, 2, 2, 8512, 64), (8, 2, 2, 8576, 64), (8, 2, 2, 64, 8576),       # the staged rows' limit
+    (1, 2, 2, 32768, 64), (1, 2, 2, 32832, 64), (1, 2, 1, 64, 32768), (1, 2, 1, 64, 32832)])
+def test_layer_at_the_limits_of_its_kernels(wob, T, E, topk, H, I):
+    """On both sides of every limit of the kernels for few tokens."""
+    x, logits, w = _layer_inputs(T, E, H, I, T + E + topk)
+    _check_layer(wob, x, logits, topk, w)
+
+
+@pytest.mark.parametrize("T", [1, 12])
+def test_layer_on_two_streams_at_once(wob, T):
+    """Calls without a common workspace do not disturb each other."""
+    torch = torch_mod()
+    E, topk, H, I = 16, 4, 1024, 768
+    sets = []
+    for seed in (1, 2):
+        x, logits, w = _layer_inputs(T, E, H, I, seed)
+        sets.append((x.cuda(), logits.cuda(), topk, *(dev(a) for a in w)))
+    want = [wob.mxfp4_moe_layer(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(20):
+        for i, (st, s) in enumerate(zip(streams, sets)):
+            with torch.cuda.stream(st):
+                got[i].append(wob.mxfp4_moe_layer(*s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(want[i], y) for y in got[i])
+
+
+@pytest.mark.parametrize("T", [1, 20, 70])
+def test_layer_captured_with_its_own_workspace(wob, T):
+    """Captured without a workspace of the caller's: the graph's memory pool holds it."""
+    torch = torch_mod()
+    E, topk, H, I = 8, 2, 256, 128
+    x, logits, w = _layer_inputs(T, E, H, I, 77)
+    x, logits, wd = x.cuda(), logits.cuda(), [dev(a) for a in w]
+    want = wob.mxfp4_moe_layer(x, logits, topk, *wd)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = wob.mxfp4_moe_layer(x, logits, topk, *wd)
+    for _ in range(3):
+        y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        assert torch.equal(wob.mxfp4_moe_layer(x, logits, topk, *wd), want)
+
+
+def test_choice_offsets_past_32_bits(wob):
+    """More than 2^31 scores: the last rows, and one in the middle."""
+    torch = torch_mod()
+    T, E, topk = 530000, 4096, 3
+    l = torch.zeros((T, E), dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, 1, T // 2, 524288, 524289, T - 1], device="cuda")
+    l[rows, torch.tensor([5, 4095, 17, 3, 2048, 4094], device="cuda")] = 2.0
+    l[rows, torch.tensor([6, 0, 4000, 4, 1, 9], device="cuda")] = 1.0
+    ids, w = wob.moe_topk(l, topk)
+    got, rest = ids[rows].cpu().tolist(), ids[1000].cpu().tolist()
+    assert got == [[5, 6, 0], [4095, 0, 1], [17, 4000, 0], [3, 4, 0], [2048, 1, 0], [4094, 9, 0]]
+    assert rest == [0, 1, 2]
+    # exp of -1 and -2 to 2^-21 (argument, exponential), sum and quotient to 2^-22
+    want = torch.softmax(torch.tensor([2.0, 1.0, 0.0], dtype=torch.float64), 0)
+    assert (w[rows].cpu().double() - want).abs().max() <= 2.0 ** -20
+
+
+def test_choice_on_two_streams_at_once(wob):
+    torch = torch_mod()
+    g = torch.Generator().manual_seed(4)
+    ls = [torch.randn((4000, 128), generator=g).cuda() for _ in range(2)]
+    want = [wob.moe_topk(l, 8) for l in ls]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in ls], [[], []]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(wob.moe_topk(ls[i], 8))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, want[i][0]) and torch.equal(b, want[i][1]) for a, b in got[i])

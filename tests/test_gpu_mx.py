@@ -327,3 +327,54 @@ def test_captured_and_replayed(wob, M):
         torch.cuda.synchronize()
         want = wob.mxfp4_gemm(*wob.mxfp4_quantize(x), wc, ws)
         assert torch.equal(y, want), k
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (16, 72, 8608), (16, 72, 8640), (17, 72, 8608), (15, 40, 9152), (8, 40, 16384),   # rows staged whole
+    (1, 40, 53248), (1, 40, 53600), (1, 24, 65536), (2, 24, 65568), (1, 8, 131072),
+    (1, 4088, 4064), (1, 4096, 64), (2, 4104, 4128), (1, 200, 4096)])                # workgroup shapes
+def test_product_at_the_limits_of_its_kernels(wob, M, N, K):
+    """On both sides of the limits of the kernel for few rows."""
+    _check(wob, _operands(M, N, K, K + N, 120, 123), "fp32")
+
+
+@pytest.mark.parametrize("M", [1, 40, 100, 600])
+def test_product_on_two_streams_at_once(wob, M):
+    """Calls without a common workspace do not disturb each other."""
+    torch = torch_mod()
+    sets = [[dev(o) for o in _operands(M, 2056, 6240, seed, 117, 121)] for seed in (1, 2)]
+    want = [wob.mxfp4_gemm(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], [[], []]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(wob.mxfp4_gemm(*sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(want[i], y) for y in got[i])
+
+
+def test_quantise_offsets_past_32_bits(wob):
+    """More than 2^31 elements, and rows whose distances pass 2^32 bytes."""
+    torch = torch_mod()
+    K = 16384
+    n = (1 << 31) // K + 40
+    x = torch.zeros((n, K), dtype=torch.bfloat16, device="cuda")
+    rows = [0, 1, n // 2, (1 << 31) // K - 1, (1 << 31) // K, n - 1]
+    g = torch.Generator().manual_seed(8)
+    v = torch.randn((len(rows), K), generator=g).to(torch.bfloat16)
+    x[rows] = v.cuda()
+    codes, scale = wob.mxfp4_quantize(x)
+    rc, rs = _quant_ref(v)
+    assert np.array_equal(codes[rows].cpu().numpy(), rc) and np.array_equal(scale[rows].cpu().numpy(), rs)
+    assert not codes[2].any() and not scale[n - 2].any()
+    wide = x.view(-1)[:n // 2 * 2 * K].view(-1, 2 * K)[:, 64:64 + 96]   # rows 2 K apart
+    codes, scale = wob.mxfp4_quantize(wide)
+    wc, wsc = _quant_ref(wide[[0, n // 4, wide.shape[0] - 1]].cpu())
+    at = [0, n // 4, wide.shape[0] - 1]
+    assert np.array_equal(codes[at].cpu().numpy(), wc) and np.array_equal(scale[at].cpu().numpy(), wsc)
+
+
+def _quant_ref(v):
+    return R.quantize(v.double().numpy())

@@ -54,6 +54,9 @@ def test_gemm_refusals(L):
                 dict(ws=F.odd), dict(y=F.odd), dict(M=1 << 20, K=1 << 14), dict(N=1 << 20, K=1 << 14),
                 dict(M=1 << 40)):
         assert g(**bad) == L.INVALID_ARG, bad
+    for bad in (dict(M=17, N=(1 << 27) - 16, K=32), dict(M=1 << 26, N=1 << 26, K=32),
+                dict(M=1, N=1 << 27, K=32), dict(M=1 << 27, N=8, K=32), dict(M=0, N=1 << 27)):
+        assert g(**bad) == L.INVALID_ARG, bad   # M + N below 2^27
     assert g(M=0) == L.OK and g(N=0) == L.OK
     size = L.lib().mxfp4_gemm_workspace_size
     assert size(-1, 8, 64) == 0 and size(4, 8, 0) == 0 and size(1 << 40, 8, 64) == 0
@@ -70,7 +73,7 @@ def test_topk_refusals(L):
         return L.lib().moe_topk(l, dt, b, i, w, T, E, topk, 1, None)
     assert k(dt=2) == L.DTYPE
     for bad in (dict(T=-1), dict(E=0), dict(E=4097), dict(topk=0), dict(topk=9), dict(E=128, topk=65),
-                dict(T=1 << 40), dict(l=None), dict(i=None), dict(w=None), dict(l=F.odd),
+                dict(T=1 << 40), dict(T=1 << 25, topk=1), dict(l=None), dict(i=None), dict(w=None), dict(l=F.odd),
                 dict(b=F.odd), dict(i=F.odd), dict(w=F.odd)):
         assert k(**bad) == L.INVALID_ARG, bad
     assert k(T=0) == L.OK

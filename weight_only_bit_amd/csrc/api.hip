@@ -442,9 +442,15 @@ int mxfp4_quantize(const void *x, int x_dtype, int64_t ldx, uint8_t *codes, uint
                     "mxfp4 quantize");
 }
 
+namespace {
+
+constexpr int64_t GEMM_ROWS = (int64_t)1 << 27; // of both operands of the MXFP4 product together: below
+
+} // namespace
+
 size_t mxfp4_gemm_workspace_size(int64_t M, int64_t N, int64_t K)
 {
-    if (M < 0 || N < 0 || K < 32 || M > INT_MAX / 2 || N > INT_MAX / 2 || K > INT_MAX / 2)
+    if (M < 0 || N < 0 || K < 32 || M >= GEMM_ROWS || N >= GEMM_ROWS || K > INT_MAX / 2)
         return 0;
     return wob::mxfp4_gemm_workspace_bytes(M, N, K);
 }
@@ -461,9 +467,10 @@ int mxfp4_gemm(const uint8_t *x_fp4, const uint8_t *x_scale, const uint8_t *w_fp
     if (K % 32 != 0 || N % 8 != 0)
         return fail(WOB_INVALID_ARG, "need K %% 32 == 0 and N %% 8 == 0 (K=%lld N=%lld)",
                     (long long)K, (long long)N);
-    // 32-bit in-kernel offsets into each operand's codes
-    if (M > INT_MAX / 2 || N > INT_MAX / 2 || K > INT_MAX / 2 || M * (K / 2) > (int64_t)UINT32_MAX ||
-        N * (K / 2) > (int64_t)UINT32_MAX)
+    // 32-bit in-kernel offsets into each operand's codes and into a span's packed
+    // scales (16 bytes a row of either operand); 32 threads a row of w in one launch
+    if (M >= GEMM_ROWS || N >= GEMM_ROWS || M + N >= GEMM_ROWS || K > INT_MAX / 2 ||
+        M * (K / 2) > (int64_t)UINT32_MAX || N * (K / 2) > (int64_t)UINT32_MAX)
         return fail(WOB_INVALID_ARG, "shape too large");
     if (M == 0 || N == 0)
         return ok();
