@@ -313,11 +313,22 @@ def test_layer_captured_and_replayed(wob, T):
     (1, 3, 2, 4160, 64), (3, 3, 2, 8192, 64), (9, 2, 1, 6208, 192),      # rows of several rounds
     (1, 3, 2, 64, 4160), (3, 3, 2, 64, 8192), (9, 2, 1, 192, 6208),
     (8, 2, 2, 8512, 64), (8, 2, 2, 8576, 64), (8, 2, 2, 64, 8576),       # the staged rows' limit
+    (1, 4, 4, 64, 4096), (1, 70, 34, 128, 1792), (1, 70, 35, 128, 1792), (1, 2, 2, 64, 32768),
     (1, 2, 2, 32768, 64), (1, 2, 2, 32832, 64), (1, 2, 1, 64, 32768), (1, 2, 1, 64, 32832)])
 def test_layer_at_the_limits_of_its_kernels(wob, T, E, topk, H, I):
     """On both sides of every limit of the kernels for few tokens."""
     x, logits, w = _layer_inputs(T, E, H, I, T + E + topk)
     _check_layer(wob, x, logits, topk, w)
+
+
+@pytest.mark.parametrize("left", [0, 1, 2, 4, 5])
+@pytest.mark.parametrize("E,H,I", [(9, 128, 64), (40, 64, 1408)])
+def test_layer_one_token_with_experts_left(wob, E, H, I, left):
+    """One token for which fewer experts than places are left, down to none."""
+    x, logits, w = _layer_inputs(1, E, H, I, left)
+    logits[:, left:] = -float("inf")
+    for renormalize in (True, False):
+        _check_layer(wob, x, logits, 5, w, None, renormalize)
 
 
 @pytest.mark.parametrize("T", [1, 12])

@@ -69,6 +69,8 @@ hipError_t launch_topk_v(const void *logits, const float *bias, int32_t *ids, fl
 //  down:  the rows pre[p] = W2 a[p] in fp32;
 //  join:  y[t] = the sum of its pairs' rows, in order of places.
 //
+// (One token: down and join are one kernel, see moe_one_down_kernel.)
+//
 // Up and down are one kernel: a workgroup takes one unit and G groups of 16
 // weight rows (up: 16 gate rows and the 16 up rows beside them); W waves share a
 // group and split K.  Every load that the workgroup needs for its first 128 W FE_SPW
@@ -99,6 +101,7 @@ constexpr int MF_TOKENS = 64;
 constexpr int MF_PAIRS = 512;   // pairs, at most
 constexpr int MF_EXPERTS = 256; // experts, at most: 16 scores a lane
 constexpr int RT_THREADS = 1024;
+constexpr size_t FEW_LDS = 150 * 1024; // of a workgroup, at most, besides its lists
 static_assert(RT_THREADS / 16 >= MF_TOKENS, "every token has its lanes");
 
 struct alignas(16) FewUnit {
@@ -415,6 +418,115 @@ __global__ __launch_bounds__(64 * W * G, 8) void moe_few_kernel(const FewArgs p)
     }
 }
 
+// One token, in place of down and join: y[c .. c + 15] = the sum of W2_e a[place] over its
+// places, by one workgroup of W waves; the places' rows laid end to end are one long K.
+// 32 experts, top 4, H = I = 2880: the layer 17.6 us and 19.8 with the kernels above;
+// 64, top 8, H = 2048, I = 1408: 19.6 and 22.7; 8, top 2, H = 4096, I = 1792: 13.7 and
+// 16.3; 16, top 1, 2880: 10.0 and 11.5.  Eight waves instead 18.8 / 21.0 / 13.9 / 9.4,
+// six steps of a wave at a time instead of two 18.3 / 20.3 / 15.3 / 10.9.
+constexpr int OD_W = 16;
+constexpr int OD_SPW = 2; // steps of a wave at a time
+
+size_t one_down_lds(int topk, int K) { return (size_t)topk * (few_pitch(K) + (K >> 5) * 16); }
+
+__global__ __launch_bounds__(64 * OD_W) void moe_one_down_kernel(const FewArgs p)
+{
+    constexpr int W = OD_W, SPW = OD_SPW, NT = 64 * W;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float part[W * 16];
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+    const int k = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int KB = p.K >> 5, steps = (KB + 3) >> 2, pitch = few_pitch(p.K), c0 = blockIdx.x * 16;
+
+    // Staged: all places' rows (those without an expert hold anything and are not used).
+    const int nv = pitch / 16, nx = p.K / 8, rows16 = p.topk * nv, su = p.topk * KB;
+    auto a_unit = [&](int i) __attribute__((always_inline)) {
+        const int m = i / nv, at = i - m * nv;
+        u32x4 v{0, 0, 0, 0};
+        if (at < nx)
+            v = reinterpret_cast<const u32x4 *>(p.f.a + (size_t)m * p.K)[at];
+        return v;
+    };
+    auto scale_unit = [&](int i) __attribute__((always_inline)) {
+        const int m = i / KB, e = max(p.f.ids[m], 0);
+        return reinterpret_cast<const u32x4 *>(p.ws + ((size_t)e * p.N + c0) * KB)[i - m * KB];
+    };
+    constexpr int XB = 2; // units of a thread under way at a time
+    u32x4 av[XB];
+#pragma unroll
+    for (int i = 0; i < XB; ++i)
+        av[i] = a_unit(min(tid + i * NT, rows16 - 1));
+    const u32x4 sv = scale_unit(min(tid, su - 1));
+    const int n = *p.f.units, total = n * steps; // places with an expert: the first ones
+
+    u32x4 c[SPW];
+    auto load = [&](int round) __attribute__((always_inline)) {
+        const int i0 = (round * W + k) * SPW;
+        int place = i0 / steps, at = i0 - place * steps;
+#pragma unroll
+        for (int j = 0; j < SPW; ++j) {
+            const int e = max(p.f.ids[min(place, p.topk - 1)], 0);
+            const uint8_t *base = p.w + ((size_t)e * p.N + c0) * KB * 16;
+            c[j] = *reinterpret_cast<const u32x4 *>(base + 16u * (uint32_t)(r * KB + min(4 * at + q, KB - 1)));
+            if (++at == steps) {
+                at = 0;
+                ++place;
+            }
+        }
+    };
+    load(0);
+
+#pragma unroll
+    for (int i = 0; i < XB; ++i)
+        if (tid + i * NT < rows16)
+            reinterpret_cast<u32x4 *>(smem)[tid + i * NT] = av[i];
+    for (int i = tid + XB * NT; i < rows16; i += NT)
+        reinterpret_cast<u32x4 *>(smem)[i] = a_unit(i);
+    uint8_t *const sl = smem + (size_t)p.topk * pitch;
+    if (tid < su)
+        reinterpret_cast<u32x4 *>(sl)[tid] = sv;
+    for (int i = tid + NT; i < su; i += NT)
+        reinterpret_cast<u32x4 *>(sl)[i] = scale_unit(i);
+    __syncthreads();
+
+    f32x4 acc{0.f, 0.f, 0.f, 0.f};
+    for (int round = 0; round * W * SPW < total; ++round) {
+        if (round > 0)
+            load(round);
+        const int i0 = (round * W + k) * SPW;
+        int place = i0 / steps, at = i0 - place * steps;
+#pragma unroll
+        for (int j = 0; j < SPW; ++j) {
+            if (i0 + j < total) {
+                const int b = 4 * at + q;
+                const uint8_t *const xr = smem + (size_t)place * pitch + 64 * b;
+                u32x4 x[4], v = c[j];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    x[s] = *reinterpret_cast<const u32x4 *>(xr + 16 * s);
+                    v[s] = b < KB ? v[s] : 0u;
+                }
+                step16(v, e8m0_to_f32(sl[(size_t)(place * 16 + r) * KB + min(b, KB - 1)]), x, acc);
+            }
+            if (++at == steps) {
+                at = 0;
+                ++place;
+            }
+        }
+    }
+    // the waves' sums in order of K; every column of the instruction is the token's
+    if (r == 0)
+        *reinterpret_cast<f32x4 *>(part + k * 16 + 4 * q) = acc;
+    __syncthreads();
+    if (tid < 16) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            v += part[w * 16 + tid];
+        p.y[c0 + tid] = (uint16_t)f32x2_to_act2<DT_BF16>(v, v);
+    }
+}
+
 // y[t][h .. h + 3] = the sum of token t's rows of pre, in order of places.
 __global__ __launch_bounds__(256) void moe_few_join_kernel(const float *__restrict__ pre,
                                                            const int32_t *__restrict__ ids,
@@ -448,9 +560,8 @@ __global__ __launch_bounds__(256) void moe_few_join_kernel(const float *__restri
 // Whether the kernels above take the layer: their lists and the staged rows fit.
 bool layer_few(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
 {
-    constexpr size_t most = 150 * 1024;
     return T <= MF_TOKENS && T * topk <= MF_PAIRS && E <= MF_EXPERTS && H <= 32768 && I <= 32768 &&
-           few_lds<true, 4, 2>((int)T, (int)H) <= most && few_lds<false, 4, 2>((int)T, (int)I) <= most;
+           few_lds<true, 4, 2>((int)T, (int)H) <= FEW_LDS && few_lds<false, 4, 2>((int)T, (int)I) <= FEW_LDS;
 }
 
 template <bool UP, bool ONE, int V, int W, int G>
@@ -458,7 +569,7 @@ hipError_t launch_few_as(FewArgs a, hipStream_t stream)
 {
     auto kern = moe_few_kernel<UP, ONE, V, W, G>;
     static std::atomic<uint64_t> lds_set{0};
-    if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), 156 * 1024, lds_set);
+    if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), FEW_LDS, lds_set);
         e != hipSuccess)
         return e;
     // units: at most one for every pair, one for every expert and FE_UNIT of its pairs
@@ -518,6 +629,16 @@ hipError_t launch_layer_few(const MoeLayerArgs &m, void *workspace, hipStream_t 
     a.ws = m.w2s;
     a.K = m.I;
     a.N = m.H;
+    if (m.T == 1 && one_down_lds(m.topk, m.I) <= FEW_LDS) {
+        auto kern = moe_one_down_kernel;
+        static std::atomic<uint64_t> lds_set{0};
+        e = lds_optin(reinterpret_cast<const void *>(kern), FEW_LDS, lds_set);
+        if (e != hipSuccess)
+            return e;
+        hipLaunchKernelGGL(kern, dim3((unsigned)(m.H / 16)), dim3(64 * OD_W),
+                           one_down_lds(m.topk, m.I), stream, a);
+        return hipGetLastError();
+    }
     e = launch_few<false, false, 1>(a, stream);
     if (e != hipSuccess)
         return e;
