@@ -80,13 +80,14 @@ def _check_device(*tensors):
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
+        at = t.get_device()
+        if at < 0:  # a host tensor
             raise ValueError("all operands must be device tensors")
         if not t.is_contiguous():
             raise ValueError("all operands must be contiguous")
         if first is None:
-            first, index = t, t.get_device()
-        elif t.get_device() != index:
+            first, index = t, at
+        elif at != index:
             raise ValueError("operands live on different devices")
     return None if first is None else first.device
 
@@ -273,9 +274,14 @@ def mxfp4_moe_stage2(a, topk_ids, topk_weights, w2_fp4, w2_scale, out=None, work
     return out
 
 
-def _value_dtypes():
-    _torch()
-    return _values
+def _output(t, name, shape, dtype, device):
+    """A caller's output on `device`, checked, or a new one, which needs no check."""
+    if t is None:
+        return _torch_mod.empty(shape, dtype=dtype, device=device)
+    _want(t, name, shape, (dtype,))
+    if _check_device(t) != device:
+        raise ValueError("operands live on different devices")
+    return t
 
 
 def _workspace(workspace, need, device):
@@ -299,7 +305,7 @@ def mxfp4_quantize(x, out=None, out_scale=None):
     torch = _torch()
     if x.dim() < 1:
         raise ValueError("x must be [..., K]")
-    _want(x, "x", tuple(x.shape), _value_dtypes())
+    _want(x, "x", x.shape, _values)
     K = x.shape[-1]
     if K < 32 or K % 32 != 0:
         raise ValueError(f"K={K} must be a multiple of 32 (one E8M0 scale per 32)")
@@ -313,17 +319,13 @@ def mxfp4_quantize(x, out=None, out_scale=None):
         ldx = x.stride(0)
     else:
         raise ValueError("x must be contiguous, or a 2-D column slice of a contiguous tensor")
-    if out is None:
-        out = torch.empty((*lead, K // 2), dtype=torch.uint8, device=x.device)
-    if out_scale is None:
-        out_scale = torch.empty((*lead, K // 32), dtype=torch.uint8, device=x.device)
-    _want(out, "out", (*lead, K // 2), _bytes)
-    _want(out_scale, "out_scale", (*lead, K // 32), _bytes)
-    dev = _check_device(out, out_scale)
-    if x.device != dev:
-        raise ValueError("operands live on different devices")
-    st = _run(_lib.lib().mxfp4_quantize, dev, _ptr(x), _tag(x), ldx, _ptr(out), _ptr(out_scale), R,
-               K)
+    dev = x.device
+    out = _output(out, "out", (*lead, K // 2), torch.uint8, dev)
+    out_scale = _output(out_scale, "out_scale", (*lead, K // 32), torch.uint8, dev)
+    if x.get_device() < 0:
+        raise ValueError("all operands must be device tensors")
+    st = _run(_lib.lib().mxfp4_quantize, dev, x.data_ptr(), _tags[x.dtype], ldx, out.data_ptr(),
+               out_scale.data_ptr(), R, K)
     _lib.check(st, "mxfp4_quantize")
     return out, out_scale
 
@@ -351,15 +353,14 @@ def mxfp4_gemm(x_fp4, x_scale, w_fp4, w_scale, out=None, out_dtype=None, workspa
     _want(w_scale, "w_scale", (N, K // 32), _bytes)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
-    if out_dtype not in _value_dtypes():
+    if out_dtype not in _values:
         raise TypeError(f"out_dtype {out_dtype} must be float16, bfloat16 or float32")
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x_fp4.device)
-    _want(out, "out", (M, N), (out_dtype,))
-    workspace, ws_bytes = _workspace(workspace, mxfp4_gemm_workspace_size(M, N, K), x_fp4.device)
-    dev = _check_device(x_fp4, x_scale, w_fp4, w_scale, out, workspace)
-    st = _run(_lib.lib().mxfp4_gemm, dev, _ptr(x_fp4), _ptr(x_scale), _ptr(w_fp4), _ptr(w_scale),
-               _ptr(out), _tag(out), M, N, K, _ptr(workspace), ws_bytes)
+    dev = x_fp4.device
+    out = _output(out, "out", (M, N), out_dtype, dev)
+    workspace, ws_bytes = _workspace(workspace, mxfp4_gemm_workspace_size(M, N, K), dev)
+    _check_device(x_fp4, x_scale, w_fp4, w_scale, workspace)
+    st = _run(_lib.lib().mxfp4_gemm, dev, x_fp4.data_ptr(), x_scale.data_ptr(), w_fp4.data_ptr(),
+               w_scale.data_ptr(), out.data_ptr(), _tags[out_dtype], M, N, K, _ptr(workspace), ws_bytes)
     _lib.check(st, "mxfp4_gemm")
     return out
 
@@ -369,7 +370,7 @@ def _check_choice(logits, topk, bias):
     torch = _torch()
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
-    _want(logits, "logits", tuple(logits.shape), _value_dtypes())
+    _want(logits, "logits", logits.shape, _values)
     T, E = logits.shape
     if not 1 <= topk <= min(E, 64):
         raise ValueError(f"topk={topk} must be between 1 and min(E={E}, 64)")
@@ -385,15 +386,12 @@ def moe_topk(logits, topk: int, bias=None, renormalize: bool = True, ids=None, w
     experts.  Places without an expert above -inf hold id -1 and weight 0."""
     torch = _torch()
     T, E = _check_choice(logits, topk, bias)
-    if ids is None:
-        ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
-    if weights is None:
-        weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
-    _want(ids, "ids", (T, topk), (torch.int32,))
-    _want(weights, "weights", (T, topk), (torch.float32,))
-    dev = _check_device(logits, bias, ids, weights)
-    st = _run(_lib.lib().moe_topk, dev, _ptr(logits), _tag(logits), _ptr(bias), _ptr(ids),
-               _ptr(weights), T, E, topk, int(bool(renormalize)))
+    dev = logits.device
+    ids = _output(ids, "ids", (T, topk), torch.int32, dev)
+    weights = _output(weights, "weights", (T, topk), torch.float32, dev)
+    _check_device(logits, bias)
+    st = _run(_lib.lib().moe_topk, dev, logits.data_ptr(), _tags[logits.dtype], _ptr(bias),
+               ids.data_ptr(), weights.data_ptr(), T, E, topk, 1 if renormalize else 0)
     _lib.check(st, "moe_topk")
     return ids, weights
 
@@ -422,14 +420,14 @@ def mxfp4_moe_layer(x, logits, topk: int, w1_fp4, w1_scale, w2_fp4, w2_scale, bi
     _want(w1_scale, "w1_scale", (E, 2 * I, H // 32), _bytes)
     _want(w2_fp4, "w2_fp4", (E, H, I // 2), _bytes)
     _want(w2_scale, "w2_scale", (E, H, I // 32), _bytes)
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    _want(out, "out", (T, H), (torch.bfloat16,))
-    workspace, ws_bytes = _workspace(workspace, moe_layer_workspace_size(T, topk, E, H, I), x.device)
-    dev = _check_device(x, logits, bias, w1_fp4, w1_scale, w2_fp4, w2_scale, out, workspace)
-    st = _run(_lib.lib().mxfp4_moe_layer, dev, _ptr(x), _ptr(logits), _tag(logits), _ptr(bias),
-               _ptr(w1_fp4), _ptr(w1_scale), _ptr(w2_fp4), _ptr(w2_scale), _ptr(out), T, topk, E, H,
-               I, int(bool(renormalize)), _ptr(workspace), ws_bytes)
+    dev = x.device
+    out = _output(out, "out", (T, H), torch.bfloat16, dev)
+    workspace, ws_bytes = _workspace(workspace, moe_layer_workspace_size(T, topk, E, H, I), dev)
+    _check_device(x, logits, bias, w1_fp4, w1_scale, w2_fp4, w2_scale, workspace)
+    st = _run(_lib.lib().mxfp4_moe_layer, dev, x.data_ptr(), logits.data_ptr(), _tags[logits.dtype],
+               _ptr(bias), w1_fp4.data_ptr(), w1_scale.data_ptr(), w2_fp4.data_ptr(),
+               w2_scale.data_ptr(), out.data_ptr(), T, topk, E, H, I, 1 if renormalize else 0,
+               _ptr(workspace), ws_bytes)
     _lib.check(st, "mxfp4_moe_layer")
     return out
 
