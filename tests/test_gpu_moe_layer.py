@@ -314,6 +314,8 @@ def test_layer_captured_and_replayed(wob, T):
     (1, 3, 2, 64, 4160), (3, 3, 2, 64, 8192), (9, 2, 1, 192, 6208),
     (8, 2, 2, 8512, 64), (8, 2, 2, 8576, 64), (8, 2, 2, 64, 8576),       # the staged rows' limit
     (1, 4, 4, 64, 4096), (1, 70, 34, 128, 1792), (1, 70, 35, 128, 1792), (1, 2, 2, 64, 32768),
+    (4, 9, 3, 128, 2112), (5, 9, 3, 128, 2112), (8, 9, 3, 128, 2048), (9, 9, 3, 128, 2048),
+    (4, 40, 34, 128, 1792), (4, 40, 35, 128, 1792), (3, 5, 2, 2048, 2112), (12, 5, 2, 1024, 1088),
     (1, 2, 2, 32768, 64), (1, 2, 2, 32832, 64), (1, 2, 1, 64, 32768), (1, 2, 1, 64, 32832)])
 def test_layer_at_the_limits_of_its_kernels(wob, T, E, topk, H, I):
     """On both sides of every limit of the kernels for few tokens."""
@@ -321,12 +323,14 @@ def test_layer_at_the_limits_of_its_kernels(wob, T, E, topk, H, I):
     _check_layer(wob, x, logits, topk, w)
 
 
+@pytest.mark.parametrize("T", [1, 3, 8])
 @pytest.mark.parametrize("left", [0, 1, 2, 4, 5])
 @pytest.mark.parametrize("E,H,I", [(9, 128, 64), (40, 64, 1408)])
-def test_layer_one_token_with_experts_left(wob, E, H, I, left):
-    """One token for which fewer experts than places are left, down to none."""
-    x, logits, w = _layer_inputs(1, E, H, I, left)
+def test_layer_with_experts_left(wob, T, E, H, I, left):
+    """Tokens for which fewer experts than places are left, down to none."""
+    x, logits, w = _layer_inputs(T, E, H, I, left)
     logits[:, left:] = -float("inf")
+    logits[T // 2:, 3] = -float("inf")
     for renormalize in (True, False):
         _check_layer(wob, x, logits, 5, w, None, renormalize)
 

@@ -69,21 +69,21 @@ hipError_t launch_topk_v(const void *logits, const float *bias, int32_t *ids, fl
 //  down:  the rows pre[p] = W2 a[p] in fp32;
 //  join:  y[t] = the sum of its pairs' rows, in order of places.
 //
-// (One token: down and join are one kernel, see moe_one_down_kernel.)
+// (For the fewest tokens down and join are one kernel, see moe_token_down_kernel.)
 //
 // Up and down are one kernel: a workgroup takes one unit and G groups of 16
 // weight rows (up: 16 gate rows and the 16 up rows beside them); W waves share a
-// group and split K.  Every load that the workgroup needs for its first 128 W FE_SPW
+// group and split K.  Every load that the workgroup needs for its first 128 W SPW
 // elements of K is under way as soon as the unit's entry is known.  Many short
 // workgroups with few registers (64: 32 waves a CU) took 105 us for 32 tokens where
 // long ones that stream several units through a ring of registers took 145 to 160
 // (each unit then waits for a whole memory round trip: too few waves to hide it).
 // 32 experts, top 4, H = I = 2880, graph replay over three copies, us for 1 / 4 / 8 /
-// 16 / 32 tokens:
-//   W = 8, G = 1, FE_SPW = 3    20.1 / 47.5 / 69.9 / 92.9 / 121
-//   W = 4, G = 2, FE_SPW = 3    21.7 / 50.7 / 71.2 / 90.8 / 105
-//   W = 8, G = 2, FE_SPW = 3    23.1 / 55.7 / 77.7 / 97.6 / 115
-//   W = 12, G = 1, FE_SPW = 2   24.8 / 60.3 / - / - / 145
+// 16 / 32 tokens, with down by units and join throughout:
+//   W = 8, G = 1, SPW = 3    20.1 / 47.5 / 69.9 / 92.9 / 121
+//   W = 4, G = 2, SPW = 3    21.7 / 50.7 / 71.2 / 90.8 / 105
+//   W = 8, G = 2, SPW = 3    23.1 / 55.7 / 77.7 / 97.6 / 115
+//   W = 12, G = 1, SPW = 2   24.8 / 60.3 / - / - / 145
 // (plain reads of the weights alone: 9 / 26 / 42 / 55 / 61).  The narrow form has
 // twice the workgroups, each with its own copy of the rows: better until the rows
 // weigh.
@@ -93,10 +93,9 @@ hipError_t launch_topk_v(const void *logits, const float *bias, int32_t *ids, fl
 // j: word s of its 16 code bytes feeds MFMA s of the step) with the unit's pairs as
 // B columns, their rows staged in LDS.
 constexpr int FE_NARROW = 8;    // tokens with W = 8, G = 1, at most; more: W = 4, G = 2
-constexpr int FE_SPW = 3;       // steps of a wave at a time
 constexpr int FE_UNIT = 8;      // pairs of a unit, at most
-// Tokens, at most: 16 lanes each in the choice.  64 take 144 us here and 164 through
-// the tile kernels of the two stages, which 33 take as well (here 105).
+// Tokens, at most: 16 lanes each in the choice.  64 take 136 us here and 164 through
+// the tile kernels of the two stages, which 33 take as well (here 104).
 constexpr int MF_TOKENS = 64;
 constexpr int MF_PAIRS = 512;   // pairs, at most
 constexpr int MF_EXPERTS = 256; // experts, at most: 16 scores a lane
@@ -236,7 +235,7 @@ __device__ __forceinline__ void step16(const u32x4 &codes, float scale, const u3
 
 // UP: gate and up rows, rows of x, activated rows of a; else rows of W2, rows of
 // a, fp32 rows of pre.  ONE: one token, and the choice made here (UP).
-template <bool UP, bool ONE, int V, int W, int G>
+template <bool UP, bool ONE, int V, int W, int G, int SPW>
 __global__ __launch_bounds__(64 * W * G, 8) void moe_few_kernel(const FewArgs p)
 {
     constexpr int NT = 64 * W * G;
@@ -310,14 +309,14 @@ __global__ __launch_bounds__(64 * W * G, 8) void moe_few_kernel(const FewArgs p)
     const int cc = min(c0, p.N - 16);
     const size_t row = (size_t)e * NR * p.N + cc;
     const uint8_t *const w0 = p.w + row * (size_t)KB * 16, *const w1 = w0 + (size_t)p.N * KB * 16;
-    const int rounds = (steps + W * FE_SPW - 1) / (W * FE_SPW);
+    const int rounds = (steps + W * SPW - 1) / (W * SPW);
     auto block = [&](int round, int j) __attribute__((always_inline)) { // this lane's
-        return 4 * ((round * W + k) * FE_SPW + j) + q;
+        return 4 * ((round * W + k) * SPW + j) + q;
     };
-    u32x4 c[NR][FE_SPW];
+    u32x4 c[NR][SPW];
     auto load = [&](int round) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < FE_SPW; ++j) {
+        for (int j = 0; j < SPW; ++j) {
             const uint32_t at = 16u * (uint32_t)(r * KB + min(block(round, j), KB - 1));
             c[0][j] = *reinterpret_cast<const u32x4 *>(w0 + at);
             if constexpr (UP)
@@ -371,7 +370,7 @@ __global__ __launch_bounds__(64 * W * G, 8) void moe_few_kernel(const FewArgs p)
         if (round > 0)
             load(round);
 #pragma unroll
-        for (int j = 0; j < FE_SPW; ++j) {
+        for (int j = 0; j < SPW; ++j) {
             // (past the row: zero codes under one of the row's own scale bytes, so a NaN
             // there is the row's result anyway, and the zeros behind the staged row)
             const int b = block(round, j), bc = min(b, KB - 1), bx = min(b, 4 * steps - 1);
@@ -418,25 +417,32 @@ __global__ __launch_bounds__(64 * W * G, 8) void moe_few_kernel(const FewArgs p)
     }
 }
 
-// One token, in place of down and join: y[c .. c + 15] = the sum of W2_e a[place] over its
-// places, by one workgroup of W waves; the places' rows laid end to end are one long K.
-// 32 experts, top 4, H = I = 2880: the layer 17.6 us and 19.8 with the kernels above;
-// 64, top 8, H = 2048, I = 1408: 19.6 and 22.7; 8, top 2, H = 4096, I = 1792: 13.7 and
-// 16.3; 16, top 1, 2880: 10.0 and 11.5.  Eight waves instead 18.8 / 21.0 / 13.9 / 9.4,
-// six steps of a wave at a time instead of two 18.3 / 20.3 / 15.3 / 10.9.
-constexpr int OD_W = 16;
-constexpr int OD_SPW = 2; // steps of a wave at a time
+// Up to 4 tokens, and up to 8 with rows of up to 2048, in place of down and join: y[t][c .. c + 15] =
+// the sum of W2_e a[p] over the token's places, by one workgroup of W waves; the places'
+// rows laid end to end are one long K.  An expert of two tokens is read twice, most of it
+// from caches; the fp32 rows and a launch go.  The layer in us, this and the other way:
+//   32 experts, top 4, H = I = 2880            T = 1 17.5 / 19.8, 4 45.4 / 47.3, 6 62.2 / 60.4, 8 71.0 / 69.2
+//   64 experts, top 8, H = 2048, I = 1408      T = 1 19.9 / 22.7, 4 41.3 / 48.8, 8 57.9 / 65.8, 12 73.2 / 68.8
+//   8 experts, top 2, H = 4096, I = 1792       T = 1 13.7 / 16.3, 4 24.4 / 27.3, 8 36.7 / 36.7
+//   128 experts, top 8, H = 4096, I = 1536     T = 4 77.6 / 93.0, 8 142 / 164, 16 196 / 183
+//   4 experts, top 4 (all of them), 2880       T = 4 27.2 / 24.2
+// One token has 16 waves (eight: 18.8 for the first), more have eight (T = 4 of the
+// third: 16 waves 27.0); six steps of a wave at a time instead of two 18.3 for the first.
+constexpr int TD_SPW = 2; // steps of a wave at a time
 
-size_t one_down_lds(int topk, int K) { return (size_t)topk * (few_pitch(K) + (K >> 5) * 16); }
+size_t token_down_lds(int topk, int K) { return (size_t)topk * (few_pitch(K) + (K >> 5) * 16); }
 
-__global__ __launch_bounds__(64 * OD_W) void moe_one_down_kernel(const FewArgs p)
+template <bool ONE, int W>
+__global__ __launch_bounds__(64 * W) void moe_token_down_kernel(const FewArgs p)
 {
-    constexpr int W = OD_W, SPW = OD_SPW, NT = 64 * W;
+    constexpr int SPW = TD_SPW, NT = 64 * W;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float part[W * 16];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
     const int k = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int KB = p.K >> 5, steps = (KB + 3) >> 2, pitch = few_pitch(p.K), c0 = blockIdx.x * 16;
+    const int32_t *const ids = p.f.ids + blockIdx.y * p.topk; // this token's
+    const uint16_t *const rows = p.f.a + (size_t)blockIdx.y * p.topk * p.K;
 
     // Staged: all places' rows (those without an expert hold anything and are not used).
     const int nv = pitch / 16, nx = p.K / 8, rows16 = p.topk * nv, su = p.topk * KB;
@@ -444,11 +450,11 @@ __global__ __launch_bounds__(64 * OD_W) void moe_one_down_kernel(const FewArgs p
         const int m = i / nv, at = i - m * nv;
         u32x4 v{0, 0, 0, 0};
         if (at < nx)
-            v = reinterpret_cast<const u32x4 *>(p.f.a + (size_t)m * p.K)[at];
+            v = reinterpret_cast<const u32x4 *>(rows + (size_t)m * p.K)[at];
         return v;
     };
     auto scale_unit = [&](int i) __attribute__((always_inline)) {
-        const int m = i / KB, e = max(p.f.ids[m], 0);
+        const int m = i / KB, e = max(ids[m], 0);
         return reinterpret_cast<const u32x4 *>(p.ws + ((size_t)e * p.N + c0) * KB)[i - m * KB];
     };
     constexpr int XB = 2; // units of a thread under way at a time
@@ -457,7 +463,10 @@ __global__ __launch_bounds__(64 * OD_W) void moe_one_down_kernel(const FewArgs p
     for (int i = 0; i < XB; ++i)
         av[i] = a_unit(min(tid + i * NT, rows16 - 1));
     const u32x4 sv = scale_unit(min(tid, su - 1));
-    const int n = *p.f.units, total = n * steps; // places with an expert: the first ones
+    // places with an expert: the first ones (of one token: its units, a scalar load)
+    const int total =
+        steps * (ONE ? *p.f.units
+                     : __popcll(__ballot(lane < p.topk && ids[min(lane, p.topk - 1)] >= 0)));
 
     u32x4 c[SPW];
     auto load = [&](int round) __attribute__((always_inline)) {
@@ -465,7 +474,7 @@ __global__ __launch_bounds__(64 * OD_W) void moe_one_down_kernel(const FewArgs p
         int place = i0 / steps, at = i0 - place * steps;
 #pragma unroll
         for (int j = 0; j < SPW; ++j) {
-            const int e = max(p.f.ids[min(place, p.topk - 1)], 0);
+            const int e = max(ids[min(place, p.topk - 1)], 0);
             const uint8_t *base = p.w + ((size_t)e * p.N + c0) * KB * 16;
             c[j] = *reinterpret_cast<const u32x4 *>(base + 16u * (uint32_t)(r * KB + min(4 * at + q, KB - 1)));
             if (++at == steps) {
@@ -523,7 +532,7 @@ __global__ __launch_bounds__(64 * OD_W) void moe_one_down_kernel(const FewArgs p
 #pragma unroll
         for (int w = 0; w < W; ++w)
             v += part[w * 16 + tid];
-        p.y[c0 + tid] = (uint16_t)f32x2_to_act2<DT_BF16>(v, v);
+        p.y[(size_t)blockIdx.y * p.N + c0 + tid] = (uint16_t)f32x2_to_act2<DT_BF16>(v, v);
     }
 }
 
@@ -564,10 +573,10 @@ bool layer_few(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
            few_lds<true, 4, 2>((int)T, (int)H) <= FEW_LDS && few_lds<false, 4, 2>((int)T, (int)I) <= FEW_LDS;
 }
 
-template <bool UP, bool ONE, int V, int W, int G>
+template <bool UP, bool ONE, int V, int W, int G, int SPW>
 hipError_t launch_few_as(FewArgs a, hipStream_t stream)
 {
-    auto kern = moe_few_kernel<UP, ONE, V, W, G>;
+    auto kern = moe_few_kernel<UP, ONE, V, W, G, SPW>;
     static std::atomic<uint64_t> lds_set{0};
     if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), FEW_LDS, lds_set);
         e != hipSuccess)
@@ -580,12 +589,41 @@ hipError_t launch_few_as(FewArgs a, hipStream_t stream)
     return hipGetLastError();
 }
 
+// Steps of a wave at a time: two where those cover K, so that no wave is left without any
+// (8 tokens, 64 experts, top 6, H = 2048, I = 2880: 75.3 us, with three 83.8).
+template <bool UP, bool ONE, int V, int W, int G>
+hipError_t launch_few_steps(const FewArgs &a, hipStream_t stream)
+{
+    if (a.K <= 2 * W * 128)
+        return launch_few_as<UP, ONE, V, W, G, 2>(a, stream);
+    return launch_few_as<UP, ONE, V, W, G, 3>(a, stream);
+}
+
 template <bool UP, bool ONE, int V>
 hipError_t launch_few(const FewArgs &a, hipStream_t stream)
 {
     if (ONE || a.T <= FE_NARROW)
-        return launch_few_as<UP, ONE, V, 8, 1>(a, stream);
-    return launch_few_as<UP, false, V, 4, 2>(a, stream);
+        return launch_few_steps<UP, ONE, V, 8, 1>(a, stream);
+    return launch_few_steps<UP, false, V, 4, 2>(a, stream);
+}
+
+// Whether the second product is made token by token.
+bool token_down(int T, int topk, int I)
+{
+    return (T <= 4 || (T <= 8 && I <= 2048)) && token_down_lds(topk, I) <= FEW_LDS;
+}
+
+template <bool ONE, int W>
+hipError_t launch_token_down(const FewArgs &a, hipStream_t stream)
+{
+    auto kern = moe_token_down_kernel<ONE, W>;
+    static std::atomic<uint64_t> lds_set{0};
+    if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), FEW_LDS, lds_set);
+        e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(a.N / 16), (unsigned)a.T), dim3(64 * W),
+                       token_down_lds(a.topk, a.K), stream, a);
+    return hipGetLastError();
 }
 
 hipError_t launch_layer_few(const MoeLayerArgs &m, void *workspace, hipStream_t stream)
@@ -629,16 +667,8 @@ hipError_t launch_layer_few(const MoeLayerArgs &m, void *workspace, hipStream_t 
     a.ws = m.w2s;
     a.K = m.I;
     a.N = m.H;
-    if (m.T == 1 && one_down_lds(m.topk, m.I) <= FEW_LDS) {
-        auto kern = moe_one_down_kernel;
-        static std::atomic<uint64_t> lds_set{0};
-        e = lds_optin(reinterpret_cast<const void *>(kern), FEW_LDS, lds_set);
-        if (e != hipSuccess)
-            return e;
-        hipLaunchKernelGGL(kern, dim3((unsigned)(m.H / 16)), dim3(64 * OD_W),
-                           one_down_lds(m.topk, m.I), stream, a);
-        return hipGetLastError();
-    }
+    if (token_down(m.T, m.topk, m.I))
+        return m.T == 1 ? launch_token_down<true, 16>(a, stream) : launch_token_down<false, 8>(a, stream);
     e = launch_few<false, false, 1>(a, stream);
     if (e != hipSuccess)
         return e;
