@@ -213,10 +213,19 @@ hipError_t launch_few(const uint8_t *x, const uint8_t *xs, const uint8_t *w, con
 //
 // A workgroup of 4 waves (WN along n, 4 / WN along m) owns TN weight rows x TM
 // activation rows; a wave owns NB x MB blocks of 32 x 32 outputs.  K advances
-// in stages of 128 (64 code bytes a row), NS = 4 of them in LDS at a time; four
-// stages, a span of 512, share the 16 scale bytes a row has per 512 k.  Codes and
-// scales are copied by global_load_lds (16 rows x 64 code bytes, or 16 rows x
-// 16 scale bytes, per wave instruction), NS - 1 stages ahead of their use.
+// in stages of 128 (64 code bytes a row).  GS of them form a group, which is copied
+// as one piece of 64 GS bytes a row; NG groups are in LDS at a time.  Four stages, a
+// span of 512, share the 16 scale bytes a row has per 512 k.  Codes and scales
+// are copied by global_load_lds (1 KB of codes, or 16 rows x 16 scale bytes, per wave
+// instruction), NG - 1 groups ahead of their use.
+//
+// The copies' cost is one cache look-up a row and instruction, 59 B/ns a CU with 64
+// bytes of a row and 113 with whole lines.  Groups of two stages (whole lines) against
+// single ones: 100 x 5376 x 21504 23.4 us and 25.0, 200 x 16384 x 2880 18.2 and 21.0,
+// 100 x 5760 x 2880 11.2 and 11.9.  (Of the first's times plain reads of its codes in
+// that order are 13.9 and 16.2; eight waves instead of four change nothing.)  The 256 x
+// 256 tile has no room for three groups of two.
+//
 // Copied from rows K / 32 bytes apart, the scales cost as many cache look-ups a
 // row as the codes do.  PACKED: a kernel before this one lays the scales out span
 // by span, the 16 bytes of successive rows side by side, so that one copy takes
@@ -225,31 +234,38 @@ hipError_t launch_few(const uint8_t *x, const uint8_t *xs, const uint8_t *w, con
 // a larger share, 2.4 us less straight than packed.  Rows that are not
 // 4-byte aligned (K % 128 != 0) are always packed.
 //
+// 2048 x 16384 x 5376, 108 us: 3.4 PFLOP/s.  The clock falls to 1.5 GHz: with zero
+// codes, which switch little, the same launches take 92 us.  Packing takes 5 of it,
+// the stores of 67 MB 9 (few of them overlap), the copies 3 beyond copies that hit;
+// x straight from memory into registers, which halves the traffic of LDS, brings
+// nothing.
+//
 // A stage is two MFMA steps of 64 k: in step j the lane half h = lane / 32
 // supplies block 2 h + j of its row, so a lane needs bytes 2 h, 2 h + 1 of each
 // of the span's four scale dwords: a byte permute packs those of two stages into
 // one register, and the instruction selects the byte.
 //
-// LDS row R (weight rows, then activation rows) holds 64 bytes of a stage; its
-// 16-byte piece p lies at position p ^ ((R >> 2) & 3), so the 16 rows that one
-// piece is read from at a time cover all 64 banks.
+// LDS row R (weight rows, then activation rows) holds 64 GS bytes of a group; its
+// 16-byte piece p lies at position p ^ swizzle(R), so the rows that one piece
+// is read from at a time cover all 64 banks.
 //
-// Order within stage t (see run_span): step 0 reads step 1's operands and
-// multiplies; then stage t + 1's copies are waited for, a barrier makes them
-// visible and frees stage t's place (every wave has its last operands in
-// registers), and step 1 reads stage t + 1's first operands and starts the
-// copies of stage t + NS while it multiplies.  No operand read and no copy is
+// Order within a group (see run_span): its steps but the last read the next
+// step's operands and multiply; then group g + 1's copies are waited for, a barrier
+// makes them visible and frees group g's place (every wave has its last operands in
+// registers), and the last step reads group g + 1's first operands and starts the
+// copies of group g + NG while it multiplies.  No operand read and no copy is
 // waited for in the step that issues it.
-template <int WN_, int NB_, int MB_, int NS_>
+template <int WN_, int NB_, int MB_, int GS_, int NG_>
 struct MxTile {
-    static constexpr int WN = WN_, WM = 4 / WN_, NB = NB_, MB = MB_, NS = NS_;
+    static constexpr int WN = WN_, WM = 4 / WN_, NB = NB_, MB = MB_, GS = GS_, NG = NG_;
     static constexpr int TN = 32 * NB * WN, TM = 32 * MB * WM, ROWS = TN + TM;
-    static constexpr int STAGE = ROWS * 64;              // code bytes of one stage
-    static constexpr int ND = ROWS / 64;                 // code copies per wave and stage
+    static constexpr int SEG = 64 * GS;                  // code bytes of a row in a group
+    static constexpr int GROUP = ROWS * SEG;             // code bytes of one group
+    static constexpr int ND = GROUP / 4096;              // code copies per wave and group
     static constexpr int SROWS = (ROWS + 255) & ~255;    // scale rows in LDS
-    static constexpr int LDS = NS * STAGE + 2 * SROWS * 16;
+    static constexpr int LDS = NG * GROUP + 2 * SROWS * 16;
     static constexpr int WSTAGE = LDS / 4 & ~15;         // LDS of one wave in the epilogue
-    static_assert(ROWS % 64 == 0 && NS == 4 && LDS <= 160 * 1024, "tile geometry");
+    static_assert(ROWS % 64 == 0 && (GS == 1 ? NG == 4 : GS == 2 && NG == 3) && LDS <= 160 * 1024, "tile geometry");
 };
 
 constexpr int MX_SPAN = 512;
@@ -360,36 +376,40 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
     const int KB = K >> 5, S = (KB + 15) >> 4; // blocks, spans of a row
     const int s_begin = (int)((int64_t)S * split / splits);
     const int s_end = (int)((int64_t)S * (split + 1) / splits); // > s_begin: splits <= S
-    const int stages = 4 * (s_end - s_begin);
+    constexpr int GS = T::GS, NG = T::NG, GPS = 4 / GS; // stages of a group, groups in LDS, groups of a span
+    const int groups = GPS * (s_end - s_begin);
     const uint32_t rowb = (uint32_t)K >> 1;
-    constexpr int NS = T::NS, ND = T::ND;
+    constexpr int ND = T::ND;
     constexpr int NSC = PACKED ? T::SROWS / 256 : T::ROWS / 64; // scale copies per wave and span
-    constexpr int ND0 = ND / 2; // code copies in a stage's first part
+    constexpr auto part_of = [](int w) { return w * ND / (2 * GS); }; // copies before part w of a group's 2 GS
 
-    // Code copy d of wave v fills LDS rows 16 (4 d + v) .. + 15: lane L the
-    // position L % 4 of row L / 4.  Rows past the matrix repeat its last row
+    // Code copy d of wave v fills LDS rows RI (4 d + v) .. + RI - 1: lane L the
+    // position L % LR of row L / LR.  Rows past the matrix repeat its last row
     // (never stored), pieces past the row its last piece (zeroed before use).
+    constexpr int LR = 4 * GS, RI = 64 / LR; // lanes of a row, rows of a copy
     uint32_t row_at[ND];
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
-        const int R = 16 * (4 * d + wave) + (lane >> 2);
-        row_at[d] = (uint32_t)(64 * d < T::TN ? min(n0 + R, N - 1) : min(m0 + R - T::TN, M - 1)) * rowb;
+        const int R = RI * (4 * d + wave) + lane / LR;
+        row_at[d] = (uint32_t)(4 * RI * d < T::TN ? min(n0 + R, N - 1) : min(m0 + R - T::TN, M - 1)) * rowb;
     }
-    static_assert(T::TN % 64 == 0, "a wave's copy has rows of one operand");
-    const uint32_t piece = 16u * (uint32_t)((lane & 3) ^ (lane >> 4));
+    static_assert(T::TN % (4 * RI) == 0, "a copy has rows of one operand");
+    // position of a row's piece: piece ^ swizzle(row)
+    auto swizzle = [](int R) __attribute__((always_inline)) { return GS == 1 ? (R >> 2) & 3 : (R >> 1) & 7; };
+    const uint32_t piece = 16u * (uint32_t)(lane % LR ^ swizzle(RI * wave + lane / LR));
     const uint32_t lds0 = (uint32_t)(size_t)(lds_ptr_t *)smem;
-    auto code_copy = [&](int t, int d) __attribute__((always_inline)) {
-        const int from = 4 * s_begin + min(t, stages - 1); // past the end: the last stage again
-        const uint32_t k = min((uint32_t)from * 64u + piece, rowb - 16u);
-        const uint32_t to = lds0 + (uint32_t)((t & (NS - 1)) * T::STAGE + wave * 1024);
-        lds_dma16(64 * d < T::TN ? w : x, row_at[d] + k, to + (uint32_t)(4096 * d));
+    auto code_copy = [&](int g, int b, int d) __attribute__((always_inline)) { // group g into buffer b
+        const int from = GPS * s_begin + min(g, groups - 1); // past the end: the last group again
+        const uint32_t k = min((uint32_t)from * (uint32_t)T::SEG + piece, rowb - 16u);
+        const uint32_t to = lds0 + (uint32_t)(b * T::GROUP + wave * 1024);
+        lds_dma16(4 * RI * d < T::TN ? w : x, row_at[d] + k, to + (uint32_t)(4096 * d));
     };
 
     // Scale copy i of wave v fills LDS scale rows 64 (4 i + v) .. + 63 (PACKED:
     // lane L all 16 bytes of row L) or 16 (4 i + v) .. + 15 (lane L dword L % 4 of
     // row L / 4, a dword past the row its last one: a finite scale or a NaN that
     // the row's result has anyway).
-    constexpr int SC0 = NS * T::STAGE, SBUF = T::SROWS * 16;
+    constexpr int SC0 = NG * T::GROUP, SBUF = T::SROWS * 16;
     uint32_t scale_at[NSC];
     const uint32_t spr = (uint32_t)KB >> 2; // scale dwords per row
 #pragma unroll
@@ -425,22 +445,24 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
                 acc[a][b][e] = 0.f;
 
     const int an = 32 * T::NB * wn + r, bm = T::TN + 32 * T::MB * wm + r; // this lane's first LDS rows
-    uint32_t at[2]; // position of piece 2 h + j in a row of this lane
+    uint32_t at[GS][2]; // position of piece 4 p + 2 h + j in a row of this lane
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        at[j] = 16u * (uint32_t)((2 * h + j) ^ ((r >> 2) & 3));
+    for (int p = 0; p < GS; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            at[p][j] = 16u * (uint32_t)((4 * p + 2 * h + j) ^ swizzle(r));
 
     struct Operands {
         u32x4 a[T::NB], b[T::MB];
     };
     constexpr int NR = T::NB + T::MB;
-    // operand i (weight blocks, then activation blocks) of step j of stage t
-    auto read_operand = [&](int t, int j, int i, Operands &o) __attribute__((always_inline)) {
-        const uint8_t *base = smem + (t & (NS - 1)) * T::STAGE + at[j];
+    // operand i (weight blocks, then activation blocks) of step j of stage p of the group in buffer b
+    auto read_operand = [&](int b, int p, int j, int i, Operands &o) __attribute__((always_inline)) {
+        const uint8_t *base = smem + b * T::GROUP + at[p][j];
         if (i < T::NB)
-            o.a[i] = *reinterpret_cast<const u32x4 *>(base + (an + 32 * i) * 64);
+            o.a[i] = *reinterpret_cast<const u32x4 *>(base + (an + 32 * i) * T::SEG);
         else
-            o.b[i - T::NB] = *reinterpret_cast<const u32x4 *>(base + (bm + 32 * (i - T::NB)) * 64);
+            o.b[i - T::NB] = *reinterpret_cast<const u32x4 *>(base + (bm + 32 * (i - T::NB)) * T::SEG);
     };
     // A lane's scale bytes of span u, in step order.
     struct Scales {
@@ -456,27 +478,28 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
     Scales sc;
     {
 #pragma unroll
-        for (int t = 0; t < NS - 1; ++t) {
-            if (t == 0)
+        for (int g = 0; g < NG - 1; ++g) {
+            if (g == 0)
 #pragma unroll
                 for (int i = 0; i < NSC; ++i)
                     scale_copy(0, i);
 #pragma unroll
             for (int d = 0; d < ND; ++d)
-                code_copy(t, d);
+                code_copy(g, g, d);
         }
 #pragma unroll
-        for (int d = 0; d < ND0; ++d)
-            code_copy(NS - 1, d);
-        // stage 0 and the first scales have landed
-        wait_vmcnt<(NS - 2) * ND + ND0>();
+        for (int d = 0; d < part_of(1); ++d)
+            code_copy(NG - 1, NG - 1, d);
+        // group 0 and the first scales have landed
+        wait_vmcnt<(NG - 2) * ND + part_of(1)>();
         barrier_only();
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             read_scale(0, i, sc);
-            read_operand(0, 0, i, op[0]);
+            read_operand(0, 0, 0, i, op[0]);
         }
     }
+    int cur = 0; // the buffer of the group at hand (NG = 4: of the span's first one, always 0)
 
     // Span u of this part (stages 4 u .. 4 u + 3).  TAIL: the row's partial last
     // span; nothing follows it.
@@ -491,17 +514,27 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
         const int left = KB - 16 * (s_begin + u); // blocks of a partial span
         auto step = [&](auto sel) __attribute__((always_inline)) {
             constexpr int SEL = decltype(sel)::value, j = SEL & 1, p = SEL >> 1;
-            const int t = 4 * u + p;
+            // stage p = GS q + s of the span; a group's last step is its (2 GS)th
+            constexpr int q = p / GS, s = p % GS, in_group = SEL % (2 * GS);
+            constexpr bool END = in_group == 2 * GS - 1;
+            const int g = GPS * u + q;
+            auto buffer = [&](int k) __attribute__((always_inline)) { // of the group k after this one
+                if constexpr (NG == GPS)
+                    return (q + k) & (NG - 1);
+                const int b = cur + k;
+                return b >= NG ? b - NG : b;
+            };
             Operands &now = op[j], &next = op[j ^ 1];
-            if constexpr (j == 1) {
-                // stage t + 1 has landed (and in the last stage the next span's
-                // scales, started in the first): the codes of stages t + 2 and
-                // t + 3 may be in flight, and the scales that were started among them
+            if constexpr (END) {
+                // group g + 1 has landed (and in the span's last group the next span's
+                // scales, started in its first): the codes of groups g + 2 ..
+                // g + NG - 1 may be in flight, and the scales that were started among them
+                constexpr bool AMONG = GS == 1 ? p == 1 || p == 2 : p == 1;
                 if constexpr (TAIL)
                     wait_vmcnt<0>();
                 else
-                    wait_vmcnt<(NS - 2) * ND + (p == 1 || p == 2 ? NSC : 0)>();
-                __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0): this wave's reads of stage t
+                    wait_vmcnt<(NG - 2) * ND + (AMONG ? NSC : 0)>();
+                __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0): this wave's reads of group g
                 barrier_only();
             }
             if constexpr (TAIL) { // blocks past the row: zero weights
@@ -516,19 +549,19 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
             // next step's operands, (SEL 7) the next span's scales, then copies.
             // In the partial last span only the rest of its own fourth stage is
             // still to be copied.
-            constexpr bool LAST = TAIL && SEL != 0;
-            constexpr int C0 = j == 0 ? ND0 : 0, C1 = j == 0 ? ND : ND0;
+            constexpr bool LAST = TAIL && (GS != 1 || SEL != 0);
+            constexpr int PART = END ? 0 : in_group + 1, C0 = part_of(PART), C1 = part_of(PART + 1);
             constexpr int RS = SEL == 7 && !TAIL ? NR : 0, SCC = SEL == 1 && !TAIL ? NSC : 0;
             constexpr int SIDE = NR + RS + SCC + (LAST ? 0 : C1 - C0), NM = T::NB * T::MB;
             auto side = [&](int i) __attribute__((always_inline)) {
                 if (i < NR)
-                    read_operand(t + j, j ^ 1, i, next);
+                    read_operand(buffer(END ? 1 : 0), END ? 0 : s + j, j ^ 1, i, next);
                 else if (i < NR + RS)
                     read_scale(u + 1, i - NR, sc);
                 else if (i < NR + RS + SCC)
                     scale_copy(u + 1, i - NR - RS);
                 else
-                    code_copy(j == 0 ? t + NS - 1 : t + NS, C0 + i - NR - RS - SCC);
+                    code_copy(END ? g + NG : g + NG - 1, buffer(END ? 0 : NG - 1), C0 + i - NR - RS - SCC);
             };
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
@@ -539,10 +572,12 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
                     (int)sv8[SEL >> 2][i], SEL & 3, (int)sv8[SEL >> 2][T::NB + k]);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int q = 0; q < SIDE; ++q)
-                    if (q >= m * SIDE / NM && q < (m + 1) * SIDE / NM)
-                        side(q);
+                for (int z = 0; z < SIDE; ++z)
+                    if (z >= m * SIDE / NM && z < (m + 1) * SIDE / NM)
+                        side(z);
             }
+            if constexpr (END && NG != GPS)
+                cur = buffer(1);
         };
         step(std::integral_constant<int, 0>{});
         step(std::integral_constant<int, 1>{});
@@ -609,14 +644,13 @@ size_t parts_bytes(int64_t M, int64_t N, int splits)
     return splits > 1 ? (size_t)splits * (size_t)M * (size_t)N * sizeof(float) : 0; // N % 8 == 0
 }
 
-template <class T>
+template <class T, bool PACKED>
 hipError_t launch_tile(const uint8_t *x, const uint8_t *xs, const uint8_t *w, const uint8_t *ws,
-                       void *y, int ydt, int M, int N, int K, int splits, bool packed, void *workspace,
-                       hipStream_t stream)
+                       void *y, int ydt, int M, int N, int K, int splits, void *workspace, hipStream_t stream)
 {
-    auto kern = packed ? mxfp4_tile_kernel<T, true> : mxfp4_tile_kernel<T, false>;
-    static std::atomic<uint64_t> lds_set[2];
-    if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), T::LDS, lds_set[packed]);
+    auto kern = mxfp4_tile_kernel<T, PACKED>;
+    static std::atomic<uint64_t> lds_set{0};
+    if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), T::LDS, lds_set);
         e != hipSuccess)
         return e;
     const int tiles_m = (M + T::TM - 1) / T::TM;
@@ -626,7 +660,7 @@ hipError_t launch_tile(const uint8_t *x, const uint8_t *xs, const uint8_t *w, co
     if (grid > INT32_MAX / 256)
         return hipErrorInvalidValue;
     float *part = static_cast<float *>(workspace);
-    if (packed) {
+    if constexpr (PACKED) {
         uint8_t *scales = static_cast<uint8_t *>(workspace) + parts_bytes(M, N, splits);
         const int spans = (K + MX_SPAN - 1) / MX_SPAN;
         hipLaunchKernelGGL(mxfp4_pack_scales_kernel,
@@ -647,9 +681,9 @@ hipError_t launch_tile(const uint8_t *x, const uint8_t *xs, const uint8_t *w, co
     return hipGetLastError();
 }
 
-using TileL = MxTile<2, 4, 4, 4>; // 256 x 256
-using TileM = MxTile<2, 2, 2, 4>; // 128 x 128
-using TileS = MxTile<2, 1, 2, 4>; // 64 weight rows x 128 activation rows
+using TileL = MxTile<2, 4, 4, 1, 4>; // 256 x 256
+using TileM = MxTile<2, 2, 2, 2, 3>; // 128 x 128
+using TileS = MxTile<2, 1, 2, 2, 3>; // 64 weight rows x 128 activation rows
 
 // Rows and scales of x must leave the LDS room for a second workgroup.
 bool few_rows(int64_t M, int64_t K) { return M <= 16 && K <= 65536 && few_lds((int)M, (int)K, 8, 2) <= 80 * 1024; }
@@ -669,7 +703,8 @@ struct Plan {
 // longest workgroup: 100 x 5760 x 2880 11.9 us whole and 13.9 in two parts,
 // 100 x 4096 x 3584 8.6 and 9.9 in three, 100 x 2048 x 4096 9.3 and 8.7 in four,
 // 100 x 512 x 5376 11.7 and 8.0 in five.  Two workgroups on each CU bring nothing:
-// 100 x 16384 x 5376 19.1 us with 256 and 26.3 with 512.
+// 100 x 16384 x 5376 19.1 us with 256 and 26.3 with 512.  (Measured with groups of one
+// stage.)
 int k_parts(int64_t tiles, int64_t K)
 {
     const int64_t spans = (K + MX_SPAN - 1) / MX_SPAN;
@@ -689,13 +724,17 @@ Plan plan(int64_t M, int64_t N, int64_t K)
     const bool packed = K % 128 != 0;
     const int64_t spans = (K + MX_SPAN - 1) / MX_SPAN;
     const int small = k_parts(tile_count<TileS>(M, N), K);
-    // Where the small tile's parts are still long, a tile of twice the weight rows
-    // in more parts: 100 x 5376 x 21504 (14 spans a part) 24.9 us and 27.9 with the
-    // small one, 200 x 5376 x 21504 (42) 34 and 60; 100 x 5376 x 10752 (7 spans) 18.4
-    // and 17.8, 100 x 16384 x 5376 (11) 21.6 and 19.1.  Up to 64 rows, where half of
-    // it is idle, it brings little: 64 x 5376 x 21504 22.2 and 22.8.
-    if (M > 64 && spans > 11 * (int64_t)small)
-        return {Path::Medium, packed, k_parts(tile_count<TileM>(M, N), K)};
+    // A tile of twice the weight rows reads x half as often.  It is taken where the
+    // small tile's parts are still long (100 x 5376 x 21504, 14 spans a part: 23.4 us and
+    // 26.2 with the small one, 200 x 5376 x 21504, 42: 31.5 and 55.4; but 100 x 5376 x 10752,
+    // 7 spans, 17.8 and 17.0, 100 x 16384 x 5376, 11, 20.6 and 18.1), and where its
+    // workgroups are on the CUs all at once and the small one's are not (200 x 16384 x 2880
+    // 18.2 and 20.7, 1000 x 4096 x 5376 20.4 and 24.0; but 600 x 8192 x 2880, 320
+    // workgroups, 27.2 and 25.9).  Up to 64 rows, where half of it is idle, it brings little
+    // (64 x 5376 x 21504 21.3 and 22.6) or loses (64 x 16384 x 5376 18.6 and 15.9).
+    const int64_t medium = tile_count<TileM>(M, N);
+    if (M > 64 && (spans > 11 * (int64_t)small || (medium <= 256 && tile_count<TileS>(M, N) > 256)))
+        return {Path::Medium, packed, k_parts(medium, K)};
     return {Path::Small, packed, small};
 }
 
@@ -727,10 +766,10 @@ hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t 
         return launch_few<4, 1>(x, xs, w, ws, y, ydt, M, N, K, stream);
     }
     if (p.path == Path::Large)
-        return launch_tile<TileL>(x, xs, w, ws, y, ydt, M, N, K, 1, p.packed, workspace, stream);
-    if (p.path == Path::Medium)
-        return launch_tile<TileM>(x, xs, w, ws, y, ydt, M, N, K, p.splits, p.packed, workspace, stream);
-    return launch_tile<TileS>(x, xs, w, ws, y, ydt, M, N, K, p.splits, p.packed, workspace, stream);
+        return launch_tile<TileL, true>(x, xs, w, ws, y, ydt, M, N, K, 1, workspace, stream);
+    auto run = p.path == Path::Medium ? (p.packed ? launch_tile<TileM, true> : launch_tile<TileM, false>)
+                                      : (p.packed ? launch_tile<TileS, true> : launch_tile<TileS, false>);
+    return run(x, xs, w, ws, y, ydt, M, N, K, p.splits, workspace, stream);
 }
 
 } // namespace wob
