@@ -195,7 +195,9 @@ def test_product_long_rows(wob, M, N, K):
 
 @pytest.mark.parametrize("M,N,K", [(1000, 1096, 6144), (1000, 1096, 6240), (1000, 1032, 6560),
                                    (1100, 2040, 6176), (70, 9224, 6336), (127, 5000, 12288),
-                                   (1100, 2040, 512), (1400, 2048, 640), (260, 8200, 352)])
+                                   (1100, 2040, 512), (1400, 2048, 640), (260, 8200, 352),
+                                   (1030, 8192, 480), (20, 16392, 14880), (20, 16392, 14496),
+                                   (1000, 2104, 8160), (1000, 2104, 8224), (70, 9224, 8160)])
 def test_product_many_rows_long(wob, M, N, K):
     """Too few tiles for the largest one, and rows too long or too many for the smallest."""
     _check(wob, _operands(M, N, K, 5, 117, 121), "fp32")

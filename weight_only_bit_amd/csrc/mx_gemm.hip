@@ -227,12 +227,11 @@ hipError_t launch_few(const uint8_t *x, const uint8_t *xs, const uint8_t *w, con
 // 256 tile has no room for three groups of two.
 //
 // Copied from rows K / 32 bytes apart, the scales cost as many cache look-ups a
-// row as the codes do.  PACKED: a kernel before this one lays the scales out span
+// row as the codes do.  Packed: a kernel before this one lays the scales out span
 // by span, the 16 bytes of successive rows side by side, so that one copy takes
 // 64 rows.  2048 x 16384 x 5376: scales 8 bytes a row at a time 118 us, 16 bytes
 // 114, packed 110 with the packing; 100 x 5376 x 21504, where the scales are
-// a larger share, 2.4 us less straight than packed.  Rows that are not
-// 4-byte aligned (K % 128 != 0) are always packed.
+// a larger share, 2.4 us less straight than packed.  (Whole: see tile_scales.)
 //
 // 2048 x 16384 x 5376, 108 us: 3.4 PFLOP/s.  The clock falls to 1.5 GHz: with zero
 // codes, which switch little, the same launches take 92 us.  Packing takes 5 of it,
@@ -264,6 +263,8 @@ struct MxTile {
     static constexpr int ND = GROUP / 4096;              // code copies per wave and group
     static constexpr int SROWS = (ROWS + 255) & ~255;    // scale rows in LDS
     static constexpr int LDS = NG * GROUP + 2 * SROWS * 16;
+    // Scales::Whole: the most spans of a part
+    static constexpr int SPANS = (160 * 1024 - NG * GROUP) / (ROWS * 16);
     static constexpr int WSTAGE = LDS / 4 & ~15;         // LDS of one wave in the epilogue
     static_assert(ROWS % 64 == 0 && (GS == 1 ? NG == 4 : GS == 2 && NG == 3) && LDS <= 160 * 1024, "tile geometry");
 };
@@ -287,9 +288,31 @@ __device__ __forceinline__ void lds_dma4(const void *sbase_any, uint32_t voff, u
                  : "memory");
 }
 
-// Packed scales: span u of row r at ((u * rows) + r) * 16, bytes past the row
-// zero (a finite scale, met by zero codes).  One thread per 16 bytes, the spans
-// of a row side by side, so the reads are contiguous.
+// Scale bytes b .. b + 15 of a row of KB, zeros past its end (a finite scale, met by
+// zero codes).
+__device__ __forceinline__ u32x4 span_scales(const uint8_t *row, int b, int KB)
+{
+    u32x4 v = {0, 0, 0, 0};
+    if (KB >= 16) {
+        // unaligned, which global loads allow; at the end the row's last 16, shifted
+        const int past = max(b + 16 - KB, 0);
+        unsigned __int128 t;
+        __builtin_memcpy(&t, row + b - past, 16);
+        t >>= 8 * past;
+        __builtin_memcpy(&v, &t, 16);
+    } else {
+        for (int i = b; i < KB; ++i) {
+            const uint32_t s = (uint32_t)row[i] << (8 * (i & 3));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) // no indexing by a variable: v stays in registers
+                v[e] |= (i - b) >> 2 == e ? s : 0u;
+        }
+    }
+    return v;
+}
+
+// Packed scales: span u of row r at ((u * rows) + r) * 16.  One thread per 16 bytes,
+// the spans of a row side by side, so the reads are contiguous.
 __global__ __launch_bounds__(256) void mxfp4_pack_scales_kernel(const uint8_t *__restrict__ ws,
                                                                 const uint8_t *__restrict__ xs,
                                                                 u32x4 *__restrict__ out, int N, int M,
@@ -301,20 +324,13 @@ __global__ __launch_bounds__(256) void mxfp4_pack_scales_kernel(const uint8_t *_
     if (r >= rows)
         return;
     const uint8_t *row = r < N ? ws + (size_t)r * KB : xs + (size_t)(r - N) * KB;
-    const int b = 16 * u;
-    u32x4 v = {0, 0, 0, 0};
-    if (b + 16 <= KB) {
-        __builtin_memcpy(&v, row + b, 16); // unaligned, which global loads allow
-    } else {
-        for (int i = b; i < KB; ++i) {
-            const uint32_t s = (uint32_t)row[i] << (8 * (i & 3));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) // no indexing by a variable: v stays in registers
-                v[e] |= (i - b) >> 2 == e ? s : 0u;
-        }
-    }
-    out[(size_t)u * rows + r] = v;
+    out[(size_t)u * rows + r] = span_scales(row, 16 * u, KB);
 }
+
+// How the scales come into LDS: copied span by span from the rows themselves
+// (K % 128 == 0, so a row's scale bytes are whole dwords) or from packed ones,
+// or loaded by the workgroup at its start, all spans of its part.
+enum class Scales { Straight, Packed, Whole };
 
 // A wave's outputs (n from nw, m from mw) through its part of LDS, 32 output
 // rows at a time: rows of 32 NB n are written as the accumulators hold them
@@ -355,9 +371,8 @@ __device__ __forceinline__ void store_wave(const float16_t (&acc)[T::NB][T::MB],
     }
 }
 
-// PACKED: ws holds the packed scales of weight rows, then activation rows; else
-// K % 128 == 0, so a row's scale bytes are whole dwords.
-template <class T, bool PACKED>
+// Packed: ws holds the packed scales of weight rows, then activation rows.
+template <class T, Scales SC>
 __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
     const uint8_t *__restrict__ x, const uint8_t *__restrict__ xs, const uint8_t *__restrict__ w,
     const uint8_t *__restrict__ ws, void *__restrict__ y, int ydt, float *__restrict__ part, int M,
@@ -380,7 +395,8 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
     const int groups = GPS * (s_end - s_begin);
     const uint32_t rowb = (uint32_t)K >> 1;
     constexpr int ND = T::ND;
-    constexpr int NSC = PACKED ? T::SROWS / 256 : T::ROWS / 64; // scale copies per wave and span
+    constexpr bool PACKED = SC == Scales::Packed, WHOLE = SC == Scales::Whole;
+    constexpr int NSC = WHOLE ? 0 : PACKED ? T::SROWS / 256 : T::ROWS / 64; // scale copies per wave and span
     constexpr auto part_of = [](int w) { return w * ND / (2 * GS); }; // copies before part w of a group's 2 GS
 
     // Code copy d of wave v fills LDS rows RI (4 d + v) .. + RI - 1: lane L the
@@ -409,8 +425,8 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
     // lane L all 16 bytes of row L) or 16 (4 i + v) .. + 15 (lane L dword L % 4 of
     // row L / 4, a dword past the row its last one: a finite scale or a NaN that
     // the row's result has anyway).
-    constexpr int SC0 = NG * T::GROUP, SBUF = T::SROWS * 16;
-    uint32_t scale_at[NSC];
+    constexpr int SC0 = NG * T::GROUP, SBUF = (WHOLE ? T::ROWS : T::SROWS) * 16;
+    uint32_t scale_at[NSC + 1];
     const uint32_t spr = (uint32_t)KB >> 2; // scale dwords per row
 #pragma unroll
     for (int i = 0; i < NSC; ++i) {
@@ -470,7 +486,7 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
     };
     const uint32_t pick = h ? 0x07060302u : 0x05040100u; // bytes 2 h, 2 h + 1 of both dwords
     auto read_scale = [&](int u, int i, Scales &o) __attribute__((always_inline)) {
-        const u32x4 *base = reinterpret_cast<const u32x4 *>(smem + SC0 + (u & 1) * SBUF);
+        const u32x4 *base = reinterpret_cast<const u32x4 *>(smem + SC0 + (WHOLE ? min(u, s_end - s_begin - 1) : u & 1) * SBUF);
         o.v[i] = base[i < T::NB ? an + 32 * i : bm + 32 * (i - T::NB)];
     };
 
@@ -490,6 +506,25 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
 #pragma unroll
         for (int d = 0; d < part_of(1); ++d)
             code_copy(NG - 1, NG - 1, d);
+        if constexpr (WHOLE) {
+            const int total = (s_end - s_begin) * T::ROWS;
+            constexpr int B = 4; // loads of a thread under way at a time
+            for (int i0 = tid; i0 < total; i0 += 256 * B) {
+                u32x4 v[B];
+#pragma unroll
+                for (int j = 0; j < B; ++j) {
+                    const int i = min(i0 + 256 * j, total - 1), u = i / T::ROWS, R = i - u * T::ROWS;
+                    v[j] = span_scales(R < T::TN ? ws + (size_t)min(n0 + R, N - 1) * KB
+                                                 : xs + (size_t)min(m0 + R - T::TN, M - 1) * KB,
+                                       16 * (s_begin + u), KB);
+                }
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+                    if (i0 + 256 * j < total)
+                        reinterpret_cast<u32x4 *>(smem + SC0)[i0 + 256 * j] = v[j];
+            }
+            __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0): written before the barrier
+        }
         // group 0 and the first scales have landed
         wait_vmcnt<(NG - 2) * ND + part_of(1)>();
         barrier_only();
@@ -644,13 +679,15 @@ size_t parts_bytes(int64_t M, int64_t N, int splits)
     return splits > 1 ? (size_t)splits * (size_t)M * (size_t)N * sizeof(float) : 0; // N % 8 == 0
 }
 
-template <class T, bool PACKED>
+template <class T, Scales SC>
 hipError_t launch_tile(const uint8_t *x, const uint8_t *xs, const uint8_t *w, const uint8_t *ws,
                        void *y, int ydt, int M, int N, int K, int splits, void *workspace, hipStream_t stream)
 {
-    auto kern = mxfp4_tile_kernel<T, PACKED>;
+    auto kern = mxfp4_tile_kernel<T, SC>;
+    const int spans = (K + MX_SPAN - 1) / MX_SPAN, part_spans = (spans + splits - 1) / splits;
+    const int lds = SC == Scales::Whole ? std::max(T::LDS, T::NG * T::GROUP + part_spans * T::ROWS * 16) : T::LDS;
     static std::atomic<uint64_t> lds_set{0};
-    if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), T::LDS, lds_set);
+    if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), 160 * 1024, lds_set);
         e != hipSuccess)
         return e;
     const int tiles_m = (M + T::TM - 1) / T::TM;
@@ -660,9 +697,8 @@ hipError_t launch_tile(const uint8_t *x, const uint8_t *xs, const uint8_t *w, co
     if (grid > INT32_MAX / 256)
         return hipErrorInvalidValue;
     float *part = static_cast<float *>(workspace);
-    if constexpr (PACKED) {
+    if constexpr (SC == Scales::Packed) {
         uint8_t *scales = static_cast<uint8_t *>(workspace) + parts_bytes(M, N, splits);
-        const int spans = (K + MX_SPAN - 1) / MX_SPAN;
         hipLaunchKernelGGL(mxfp4_pack_scales_kernel,
                            dim3((unsigned)(((int64_t)(M + N) * spans + 255) / 256)), dim3(256), 0, stream,
                            ws, xs, reinterpret_cast<u32x4 *>(scales), N, M, K >> 5, spans);
@@ -670,7 +706,7 @@ hipError_t launch_tile(const uint8_t *x, const uint8_t *xs, const uint8_t *w, co
             return e;
         ws = scales;
     }
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), (size_t)T::LDS, stream, x, xs, w, ws, y,
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), (size_t)lds, stream, x, xs, w, ws, y,
                        ydt, part, M, N, K, tiles_m, (int)tiles, splits, nxcd);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || splits == 1)
@@ -681,19 +717,31 @@ hipError_t launch_tile(const uint8_t *x, const uint8_t *xs, const uint8_t *w, co
     return hipGetLastError();
 }
 
+template <class T, class... A>
+hipError_t launch_scales(Scales scales, A... a)
+{
+    if (scales == Scales::Straight)
+        return launch_tile<T, Scales::Straight>(a...);
+    if (scales == Scales::Packed)
+        return launch_tile<T, Scales::Packed>(a...);
+    return launch_tile<T, Scales::Whole>(a...);
+}
+
 using TileL = MxTile<2, 4, 4, 1, 4>; // 256 x 256
 using TileM = MxTile<2, 2, 2, 2, 3>; // 128 x 128
 using TileS = MxTile<2, 1, 2, 2, 3>; // 64 weight rows x 128 activation rows
 
 // Rows and scales of x must leave the LDS room for a second workgroup.
 bool few_rows(int64_t M, int64_t K) { return M <= 16 && K <= 65536 && few_lds((int)M, (int)K, 8, 2) <= 80 * 1024; }
-bool large_tile(int64_t M, int64_t N) { return ((M + 255) / 256) * ((N + 255) / 256) >= 128; }
+// Its time is that of one tile a CU up to 256 tiles, the next tile's grows with theirs:
+// with 128 of them 45.4 us and 40.6 (2048 x 4096 x 5376), with 192 48.1 and 60.0.
+bool large_tile(int64_t M, int64_t N) { return ((M + 255) / 256) * ((N + 255) / 256) >= 144; }
 
 enum class Path { Few, Large, Medium, Small };
 
 struct Plan {
     Path path;
-    bool packed;
+    Scales scales;
     int splits;
 };
 
@@ -715,13 +763,25 @@ int k_parts(int64_t tiles, int64_t K)
 template <class T>
 int64_t tile_count(int64_t M, int64_t N) { return ((M + T::TM - 1) / T::TM) * ((N + T::TN - 1) / T::TN); }
 
+// Rows whose scale bytes are not whole dwords are loaded at the start where a part's fit:
+// 700 x 2048 x 992 6.8 us and 9.0 packed, 36 x 1768 x 4960 8.8 and 10.9, 100 x 5760 x 4000 16.0 and
+// 16.9.  Others are copied as they are used: 100 x 5760 x 2944 8.4 and 9.6 loaded at the
+// start, 200 x 16384 x 2944 14.1 and 15.9.
+template <class T>
+Scales tile_scales(int64_t K, int parts)
+{
+    const int64_t spans = (K + MX_SPAN - 1) / MX_SPAN;
+    if (K % 128 == 0)
+        return Scales::Straight;
+    return (spans + parts - 1) / parts <= T::SPANS ? Scales::Whole : Scales::Packed;
+}
+
 Plan plan(int64_t M, int64_t N, int64_t K)
 {
     if (few_rows(M, K))
-        return {Path::Few, false, 1};
+        return {Path::Few, Scales::Straight, 1};
     if (large_tile(M, N))
-        return {Path::Large, true, 1};
-    const bool packed = K % 128 != 0;
+        return {Path::Large, Scales::Packed, 1};
     const int64_t spans = (K + MX_SPAN - 1) / MX_SPAN;
     const int small = k_parts(tile_count<TileS>(M, N), K);
     // A tile of twice the weight rows reads x half as often.  It is taken where the
@@ -729,13 +789,16 @@ Plan plan(int64_t M, int64_t N, int64_t K)
     // 26.2 with the small one, 200 x 5376 x 21504, 42: 31.5 and 55.4; but 100 x 5376 x 10752,
     // 7 spans, 17.8 and 17.0, 100 x 16384 x 5376, 11, 20.6 and 18.1), and where its
     // workgroups are on the CUs all at once and the small one's are not (200 x 16384 x 2880
-    // 18.2 and 20.7, 1000 x 4096 x 5376 20.4 and 24.0; but 600 x 8192 x 2880, 320
-    // workgroups, 27.2 and 25.9).  Up to 64 rows, where half of it is idle, it brings little
-    // (64 x 5376 x 21504 21.3 and 22.6) or loses (64 x 16384 x 5376 18.6 and 15.9).
+    // 18.2 and 20.7, 1000 x 4096 x 5376 20.4 and 24.0) or fill their second round (1024 x
+    // 8192 x 5376, 512 workgroups, 39.9 and 46.0; but 600 x 8192 x 2880, 320, 27.2 and 25.9,
+    // 250 x 24576 x 2880, 384, 31.5 and 30.1).  Up to 64 rows, where half of it is
+    // idle, it brings little (64 x 5376 x 21504 21.3 and 22.6) or loses (64 x 16384 x 5376
+    // 18.6 and 15.9).
     const int64_t medium = tile_count<TileM>(M, N);
-    if (M > 64 && (spans > 11 * (int64_t)small || (medium <= 256 && tile_count<TileS>(M, N) > 256)))
-        return {Path::Medium, packed, k_parts(medium, K)};
-    return {Path::Small, packed, small};
+    const bool fills = tile_count<TileS>(M, N) > 256 && (medium <= 256 || medium > 384);
+    if (M > 64 && (spans > 11 * (int64_t)small || fills))
+        return {Path::Medium, tile_scales<TileM>(K, k_parts(medium, K)), k_parts(medium, K)};
+    return {Path::Small, tile_scales<TileS>(K, small), small};
 }
 
 } // namespace
@@ -746,7 +809,7 @@ size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K)
         return 0;
     const Plan p = plan(M, N, K);
     const int64_t spans = (K + MX_SPAN - 1) / MX_SPAN;
-    return parts_bytes(M, N, p.splits) + (p.packed ? (size_t)(M + N) * (size_t)spans * 16 : 0);
+    return parts_bytes(M, N, p.splits) + (p.scales == Scales::Packed ? (size_t)(M + N) * (size_t)spans * 16 : 0);
 }
 
 hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t *w,
@@ -766,10 +829,10 @@ hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t 
         return launch_few<4, 1>(x, xs, w, ws, y, ydt, M, N, K, stream);
     }
     if (p.path == Path::Large)
-        return launch_tile<TileL, true>(x, xs, w, ws, y, ydt, M, N, K, 1, workspace, stream);
-    auto run = p.path == Path::Medium ? (p.packed ? launch_tile<TileM, true> : launch_tile<TileM, false>)
-                                      : (p.packed ? launch_tile<TileS, true> : launch_tile<TileS, false>);
-    return run(x, xs, w, ws, y, ydt, M, N, K, p.splits, workspace, stream);
+        return launch_tile<TileL, Scales::Packed>(x, xs, w, ws, y, ydt, M, N, K, 1, workspace, stream);
+    if (p.path == Path::Medium)
+        return launch_scales<TileM>(p.scales, x, xs, w, ws, y, ydt, M, N, K, p.splits, workspace, stream);
+    return launch_scales<TileS>(p.scales, x, xs, w, ws, y, ydt, M, N, K, p.splits, workspace, stream);
 }
 
 } // namespace wob
