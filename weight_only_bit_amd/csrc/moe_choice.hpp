@@ -26,6 +26,7 @@
 #pragma once
 
 #include "wob_device.hpp"
+#include "wob_internal.hpp"
 
 namespace wob {
 

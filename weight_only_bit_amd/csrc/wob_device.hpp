@@ -27,7 +27,7 @@ typedef __bf16 bf168_t __attribute__((ext_vector_type(8)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-enum { DT_F16 = 0, DT_BF16 = 1, DT_F32 = 3 };
+enum { DT_F16 = 0, DT_BF16 = 1 };
 
 template <typename To, typename From>
 __device__ __forceinline__ To bitcast(const From &f)

@@ -74,6 +74,10 @@ hipError_t launch_mxfp4_moe(const void *x, const int32_t *ids, const uint8_t *w_
                             const uint8_t *w_scale, void *y, int T, int topk, int E, int N, int K,
                             int act, int tile_m, void *workspace, hipStream_t stream);
 
+// binary32 beside DT_F16 and DT_BF16 (WOB_F32): scores, rows to quantise, outputs of
+// the MXFP4 product.
+constexpr int DT_F32 = 3;
+
 // Whole mixture-of-experts layer and the choice of experts.
 struct MoeLayerArgs {
     const void *x, *logits;
