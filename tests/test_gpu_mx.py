@@ -197,10 +197,22 @@ def test_product_long_rows(wob, M, N, K):
                                    (1100, 2040, 6176), (70, 9224, 6336), (127, 5000, 12288),
                                    (1100, 2040, 512), (1400, 2048, 640), (260, 8200, 352),
                                    (1030, 8192, 480), (20, 16392, 14880), (20, 16392, 14496),
-                                   (1000, 2104, 8160), (1000, 2104, 8224), (70, 9224, 8160)])
+                                   (1000, 2104, 8160), (1000, 2104, 8224), (70, 9224, 8160),
+                                   (1030, 14000, 96), (2048, 8704, 64), (300, 16384, 224)])
 def test_product_many_rows_long(wob, M, N, K):
     """Too few tiles for the largest one, and rows too long or too many for the smallest."""
     _check(wob, _operands(M, N, K, 5, 117, 121), "fp32")
+
+
+@pytest.mark.parametrize("K", [32, 96, 128, 480, 512, 544, 992, 1056, 2080])
+def test_product_largest_tile(wob, K):
+    """Ragged in rows, columns and spans."""
+    _check(wob, _operands(2050, 4360, K, K, 117, 121), "fp32")
+
+
+@pytest.mark.parametrize("out", DTYPES)
+def test_product_largest_tile_output_types(wob, out):
+    _check(wob, _operands(2045, 4360, 160, 3, 117, 121), out)
 
 
 @pytest.mark.parametrize("M", [1, 5, 40, 140, 300])

@@ -733,10 +733,6 @@ using TileS = MxTile<2, 1, 2, 2, 3>; // 64 weight rows x 128 activation rows
 
 // Rows and scales of x must leave the LDS room for a second workgroup.
 bool few_rows(int64_t M, int64_t K) { return M <= 16 && K <= 65536 && few_lds((int)M, (int)K, 8, 2) <= 80 * 1024; }
-// Its time is that of one tile a CU up to 256 tiles, the next tile's grows with theirs:
-// with 128 of them 45.4 us and 40.6 (2048 x 4096 x 5376), with 192 48.1 and 60.0.
-bool large_tile(int64_t M, int64_t N) { return ((M + 255) / 256) * ((N + 255) / 256) >= 144; }
-
 enum class Path { Few, Large, Medium, Small };
 
 struct Plan {
@@ -774,6 +770,16 @@ Scales tile_scales(int64_t K, int parts)
     if (K % 128 == 0)
         return Scales::Straight;
     return (spans + parts - 1) / parts <= T::SPANS ? Scales::Whole : Scales::Packed;
+}
+
+// The 256 x 256 tile: a round of one a CU takes as long as 2.5 of the 128 x 128 tile, a
+// quarter of it.  Rounds of both, us: 1 and 3, 48.1 and 60.0 (2048 x 6144 x 5376); 1 and 2, 45.4
+// and 40.6 (2048 x 4096 x 5376); 2 and 5, 86.2 and 90.1 (2048 x 8704 x 5376), 67.9 and 67.8 (1100 x
+// 16384 x 2880); 2 and 4, 58.7 and 54.3 (1030 x 14000 x 2880).
+bool large_tile(int64_t M, int64_t N)
+{
+    const int64_t large = (tile_count<TileL>(M, N) + 255) / 256, medium = (tile_count<TileM>(M, N) + 255) / 256;
+    return 2 * medium >= 5 * large;
 }
 
 Plan plan(int64_t M, int64_t N, int64_t K)
