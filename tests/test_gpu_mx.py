@@ -204,6 +204,13 @@ def test_product_many_rows_long(wob, M, N, K):
     _check(wob, _operands(M, N, K, 5, 117, 121), "fp32")
 
 
+@pytest.mark.parametrize("M", [17, 33, 64, 65])
+@pytest.mark.parametrize("N,K", [(72, 5376), (2056, 6240), (16392, 1056), (72, 453664), (72, 475168)])
+def test_product_narrow(wob, M, N, K):
+    """17 to 64 rows: whole and in parts, scales from the rows, loaded at the start, packed."""
+    _check(wob, _operands(M, N, K, K + M, 117, 121), "fp32")
+
+
 @pytest.mark.parametrize("K", [32, 96, 128, 480, 512, 544, 992, 1056, 2080])
 def test_product_largest_tile(wob, K):
     """Ragged in rows, columns and spans."""

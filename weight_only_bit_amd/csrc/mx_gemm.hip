@@ -730,10 +730,11 @@ hipError_t launch_scales(Scales scales, A... a)
 using TileL = MxTile<2, 4, 4, 1, 4>; // 256 x 256
 using TileM = MxTile<2, 2, 2, 2, 3>; // 128 x 128
 using TileS = MxTile<2, 1, 2, 2, 3>; // 64 weight rows x 128 activation rows
+using TileN = MxTile<2, 1, 1, 2, 3>; // 64 x 64
 
 // Rows and scales of x must leave the LDS room for a second workgroup.
 bool few_rows(int64_t M, int64_t K) { return M <= 16 && K <= 65536 && few_lds((int)M, (int)K, 8, 2) <= 80 * 1024; }
-enum class Path { Few, Large, Medium, Small };
+enum class Path { Few, Large, Medium, Small, Narrow };
 
 struct Plan {
     Path path;
@@ -798,12 +799,15 @@ Plan plan(int64_t M, int64_t N, int64_t K)
     // 18.2 and 20.7, 1000 x 4096 x 5376 20.4 and 24.0) or fill their second round (1024 x
     // 8192 x 5376, 512 workgroups, 39.9 and 46.0; but 600 x 8192 x 2880, 320, 27.2 and 25.9,
     // 250 x 24576 x 2880, 384, 31.5 and 30.1).  Up to 64 rows, where half of it is
-    // idle, it brings little (64 x 5376 x 21504 21.3 and 22.6) or loses (64 x 16384 x 5376
-    // 18.6 and 15.9).
+    // idle, it brings little or loses (64 x 16384 x 5376 18.6 and 15.9).
     const int64_t medium = tile_count<TileM>(M, N);
     const bool fills = tile_count<TileS>(M, N) > 256 && (medium <= 256 || medium > 384);
     if (M > 64 && (spans > 11 * (int64_t)small || fills))
         return {Path::Medium, tile_scales<TileM>(K, k_parts(medium, K)), k_parts(medium, K)};
+    // 17 to 64 rows: 32 x 5760 x 2880 7.8 us and 9.2 in the small tile, 64 x 16384 x 5376 14.8 and 16.0,
+    // 32 x 5376 x 21504 19.5 and 20.7 (128 weight rows: 9.8, 17.9, 18.7).
+    if (M <= 64)
+        return {Path::Narrow, tile_scales<TileN>(K, small), small};
     return {Path::Small, tile_scales<TileS>(K, small), small};
 }
 
@@ -838,6 +842,8 @@ hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t 
         return launch_tile<TileL, Scales::Packed>(x, xs, w, ws, y, ydt, M, N, K, 1, workspace, stream);
     if (p.path == Path::Medium)
         return launch_scales<TileM>(p.scales, x, xs, w, ws, y, ydt, M, N, K, p.splits, workspace, stream);
+    if (p.path == Path::Narrow)
+        return launch_scales<TileN>(p.scales, x, xs, w, ws, y, ydt, M, N, K, p.splits, workspace, stream);
     return launch_scales<TileS>(p.scales, x, xs, w, ws, y, ydt, M, N, K, p.splits, workspace, stream);
 }
 
