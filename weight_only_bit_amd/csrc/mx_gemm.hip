@@ -233,7 +233,7 @@ hipError_t launch_few(const uint8_t *x, const uint8_t *xs, const uint8_t *w, con
 // 114, packed 110 with the packing; 100 x 5376 x 21504, where the scales are
 // a larger share, 2.4 us less straight than packed.  (Whole: see tile_scales.)
 //
-// 2048 x 16384 x 5376, 108 us: 3.4 PFLOP/s.  The clock falls to 1.5 GHz: with zero
+// 2048 x 16384 x 5376, 108 us: 3.4 PFLOP/s.  The clock falls to 1.6 GHz: with zero
 // codes, which switch little, the same launches take 92 us.  Packing takes 5 of it,
 // the stores of 67 MB 9 (few of them overlap), the copies 3 beyond copies that hit;
 // x straight from memory into registers, which halves the traffic of LDS, brings
@@ -421,7 +421,7 @@ __global__ __launch_bounds__(256) void mxfp4_tile_kernel(
         lds_dma16(4 * RI * d < T::TN ? w : x, row_at[d] + k, to + (uint32_t)(4096 * d));
     };
 
-    // Scale copy i of wave v fills LDS scale rows 64 (4 i + v) .. + 63 (PACKED:
+    // Scale copy i of wave v fills LDS scale rows 64 (4 i + v) .. + 63 (Packed:
     // lane L all 16 bytes of row L) or 16 (4 i + v) .. + 15 (lane L dword L % 4 of
     // row L / 4, a dword past the row its last one: a finite scale or a NaN that
     // the row's result has anyway).
