@@ -336,6 +336,9 @@ size_t mxfp4_moe_layer_workspace_size(int64_t T, int64_t topk, int64_t E, int64_
  *  [E][H][I/2], w2_scale [E][H][I/32]; y [T][H] bf16.
  *  The function of moe_topk, mxfp4_moe_gemm (WOB_ACT_SILU_MUL) and
  *  mxfp4_moe_stage2 in turn; the sums are fp32 and their order may differ.
+ *  A sum that holds an infinity of one sign is that infinity.  (Where the layer
+ *  is those three calls, and H or I is an odd multiple of 64, an infinity in the
+ *  last 64 elements of a row may become a NaN instead, as it does in the stages.)
  *  H % 64 == 0, H >= 64, I % 64 == 0, I >= 64, T >= 0, 1 <= topk <= 64,
  *  topk <= E, 1 <= E <= 4096, T below 2^25, T*H*2, T*topk*I*2 and I*H below
  *  2^32, E*I*H at most 2^40 (else WOB_INVALID_ARG).  T == 0 is a no-op returning WOB_OK.

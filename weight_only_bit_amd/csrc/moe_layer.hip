@@ -211,14 +211,16 @@ __global__ __launch_bounds__(RT_THREADS) void moe_few_route_kernel(const FewArgs
     }
 }
 
-// Bytes between staged rows: K rounded up to whole steps (zeros), 16 mod 128,
-// which makes the operand reads conflict-free.
+// Bytes between staged rows, 16 mod 128, which makes the operand reads conflict-free
+// (K % 64 == 0).  Token by token the rows are rounded up to whole steps; in units each
+// has at least one block of zeros behind it, which is what blocks past the row read.
 __host__ __device__ inline int few_pitch(int K) { return ((K + 127) & ~127) * 2 + 16; }
+__host__ __device__ inline int unit_pitch(int K) { return 2 * K + 144; }
 __host__ __device__ inline int few_rows(int T) { return T < FE_UNIT ? T : FE_UNIT; } // a unit's pairs have different tokens
 template <bool UP, int W, int G>
 size_t few_lds(int T, int K)
 {
-    const size_t staged = (size_t)few_rows(T) * few_pitch(K) + (size_t)G * (UP ? 32 : 16) * (K >> 5);
+    const size_t staged = (size_t)few_rows(T) * unit_pitch(K) + (size_t)G * (UP ? 32 : 16) * (K >> 5);
     const size_t sums = (size_t)G * W * (UP ? 2 : 1) * 1024;
     return (std::max(staged, sums) + 15) & ~(size_t)15;
 }
@@ -243,7 +245,7 @@ __global__ __launch_bounds__(64 * W * G, 8) void moe_few_kernel(const FewArgs p)
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), k = wave % W, g = wave / W;
-    const int KB = p.K >> 5, steps = (KB + 3) >> 2, pitch = few_pitch(p.K);
+    const int KB = p.K >> 5, steps = (KB + 3) >> 2, pitch = unit_pitch(p.K);
     const int un = blockIdx.x / p.slices, slice = blockIdx.x - un * p.slices;
 
     int e, pairs;
@@ -372,8 +374,9 @@ __global__ __launch_bounds__(64 * W * G, 8) void moe_few_kernel(const FewArgs p)
 #pragma unroll
         for (int j = 0; j < SPW; ++j) {
             // (past the row: zero codes under one of the row's own scale bytes, so a NaN
-            // there is the row's result anyway, and the zeros behind the staged row)
-            const int b = block(round, j), bc = min(b, KB - 1), bx = min(b, 4 * steps - 1);
+            // there is the row's result anyway, and the zeros behind the staged row, not
+            // the row, which may hold an infinity: 0 x infinity is NaN)
+            const int b = block(round, j), bc = min(b, KB - 1), bx = min(b, KB);
             u32x4 x[4];
 #pragma unroll
             for (int s = 0; s < 4; ++s)
