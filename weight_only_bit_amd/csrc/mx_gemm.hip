@@ -732,6 +732,10 @@ using TileM = MxTile<2, 2, 2, 2, 3>; // 128 x 128
 using TileS = MxTile<2, 1, 2, 2, 3>; // 64 weight rows x 128 activation rows
 using TileN = MxTile<2, 1, 1, 2, 3>; // 64 x 64
 
+// Spans of a part of the 64 x 128 tile, at most (see plan): their scales always fit.
+constexpr int SMALL_SPANS = 11;
+static_assert(TileS::SPANS >= SMALL_SPANS, "no packed form of the 64 x 128 tile");
+
 // Rows and scales of x must leave the LDS room for a second workgroup.
 bool few_rows(int64_t M, int64_t K) { return M <= 16 && K <= 65536 && few_lds((int)M, (int)K, 8, 2) <= 80 * 1024; }
 enum class Path { Few, Large, Medium, Small, Narrow };
@@ -802,7 +806,7 @@ Plan plan(int64_t M, int64_t N, int64_t K)
     // idle, it brings little or loses (64 x 16384 x 5376 18.6 and 15.9).
     const int64_t medium = tile_count<TileM>(M, N);
     const bool fills = tile_count<TileS>(M, N) > 256 && (medium <= 256 || medium > 384);
-    if (M > 64 && (spans > 11 * (int64_t)small || fills))
+    if (M > 64 && (spans > SMALL_SPANS * (int64_t)small || fills))
         return {Path::Medium, tile_scales<TileM>(K, k_parts(medium, K)), k_parts(medium, K)};
     // 17 to 64 rows: 32 x 5760 x 2880 7.8 us and 9.2 in the small tile, 64 x 16384 x 5376 14.8 and 16.0,
     // 32 x 5376 x 21504 19.5 and 20.7 (128 weight rows: 9.8, 17.9, 18.7).
@@ -844,7 +848,9 @@ hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t 
         return launch_scales<TileM>(p.scales, x, xs, w, ws, y, ydt, M, N, K, p.splits, workspace, stream);
     if (p.path == Path::Narrow)
         return launch_scales<TileN>(p.scales, x, xs, w, ws, y, ydt, M, N, K, p.splits, workspace, stream);
-    return launch_scales<TileS>(p.scales, x, xs, w, ws, y, ydt, M, N, K, p.splits, workspace, stream);
+    if (p.scales == Scales::Straight)
+        return launch_tile<TileS, Scales::Straight>(x, xs, w, ws, y, ydt, M, N, K, p.splits, workspace, stream);
+    return launch_tile<TileS, Scales::Whole>(x, xs, w, ws, y, ydt, M, N, K, p.splits, workspace, stream);
 }
 
 } // namespace wob
