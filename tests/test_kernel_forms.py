@@ -1,7 +1,7 @@
-"""The forms of the MXFP4 product's tiles that are built (CPU: compiles to gfx950
-assembly).
+"""The forms of the MXFP4 product's tiles and of the layer's products that are built
+(CPU: compiles to gfx950 assembly).
 
-Every form that is built is reached by some call: the list below holds one for
+Every form that is built is reached by some call: the lists below hold one for
 each, and nothing else is in the assembly."""
 import os
 import re
@@ -27,6 +27,15 @@ TILES = {
     (64, 64, "whole"): (17, 72, 453664),           # 56 spans a part: the most that fit
     (64, 64, "packed"): (17, 72, 475168),          # 59
 }
+# moe_few_kernel: (up, one token, scores a lane, waves, groups, steps) -> T, E, topk, H, I
+FEW = {
+    (1, 1, 2, 8, 1, 2): (1, 32, 4, 2048, 64), (1, 1, 2, 8, 1, 3): (1, 32, 4, 2112, 64),
+    (1, 1, 16, 8, 1, 2): (1, 33, 4, 2048, 64), (1, 1, 16, 8, 1, 3): (1, 33, 4, 2112, 64),
+    (1, 0, 1, 8, 1, 2): (8, 8, 2, 2048, 64), (1, 0, 1, 8, 1, 3): (8, 8, 2, 2112, 64),
+    (1, 0, 1, 4, 2, 2): (9, 8, 2, 1024, 64), (1, 0, 1, 4, 2, 3): (9, 8, 2, 1088, 64),
+    (0, 0, 1, 8, 1, 2): (4, 40, 35, 128, 1792), (0, 0, 1, 8, 1, 3): (5, 8, 2, 64, 2112),
+    (0, 0, 1, 4, 2, 2): (9, 8, 2, 64, 1024), (0, 0, 1, 4, 2, 3): (9, 8, 2, 64, 1088),
+}
 SCALES = ("straight", "packed", "whole")
 
 
@@ -37,7 +46,7 @@ def assembly(tmp_path_factory):
              "--cuda-device-only", "-S"]
     td = tmp_path_factory.mktemp("asm")
     procs = {}
-    for src in ("mx_gemm.hip",):
+    for src in ("mx_gemm.hip", "moe_layer.hip"):
         out = str(td / (src + ".s"))
         procs[src] = (out, subprocess.Popen([HIPCC] + flags + ["-o", out, os.path.join(CSRC, src)],
                                             stdout=subprocess.PIPE, stderr=subprocess.STDOUT))
@@ -51,6 +60,7 @@ def assembly(tmp_path_factory):
 
 TILE = re.compile(r"^\S*mxfp4_tile_kernelINS0_6MxTileILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)EEE"
                   r"LNS0_6ScalesE(\d)E\S*:\s*;", re.M)
+LAYER = re.compile(r"^\S*moe_few_kernelILb(\d)ELb(\d)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)E\S*:\s*;", re.M)
 
 
 def tile_forms(text):
@@ -62,3 +72,8 @@ def tile_forms(text):
 @needs_hipcc
 def test_tile_forms_are_those_that_calls_reach(assembly):
     assert tile_forms(assembly["mx_gemm.hip"]) == set(TILES)
+
+
+@needs_hipcc
+def test_layer_forms_are_those_that_calls_reach(assembly):
+    assert {tuple(map(int, m.groups())) for m in LAYER.finditer(assembly["moe_layer.hip"])} == set(FEW)

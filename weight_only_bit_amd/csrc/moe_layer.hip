@@ -605,9 +605,10 @@ hipError_t launch_few_steps(const FewArgs &a, hipStream_t stream)
 template <bool UP, bool ONE, int V>
 hipError_t launch_few(const FewArgs &a, hipStream_t stream)
 {
-    if (ONE || a.T <= FE_NARROW)
-        return launch_few_steps<UP, ONE, V, 8, 1>(a, stream);
-    return launch_few_steps<UP, false, V, 4, 2>(a, stream);
+    if constexpr (!ONE)
+        if (a.T > FE_NARROW)
+            return launch_few_steps<UP, false, V, 4, 2>(a, stream);
+    return launch_few_steps<UP, ONE, V, 8, 1>(a, stream);
 }
 
 // Whether the second product is made token by token.
