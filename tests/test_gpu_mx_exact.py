@@ -119,3 +119,11 @@ def test_layer_at_the_limits_of_its_kernels(wob, T, E, topk, H, I):
 @pytest.mark.parametrize("H,I", [(64, 64), (128, 192), (320, 128), (704, 1216), (1152, 640)])
 def test_layer_ragged_steps(wob, T, H, I):
     _check_layer(wob, T, 5, 2, H, I)
+
+
+@pytest.mark.parametrize("T,E,topk,H,I", [
+    (64, 4, 4, 128, 192), (32, 8, 8, 192, 128), (33, 8, 8, 192, 128), (40, 32, 8, 128, 64), (41, 32, 8, 128, 64),
+    (64, 64, 8, 128, 64), (64, 16, 8, 576, 448), (48, 8, 2, 4096, 64), (49, 8, 2, 4096, 64), (48, 8, 2, 64, 7168),
+    (49, 8, 2, 64, 7168), (64, 64, 4, 4096, 128), (33, 64, 8, 4096, 64), (8, 8, 8, 7168, 128)])
+def test_layer_at_the_limits_of_pairs(wob, T, E, topk, H, I):
+    _check_layer(wob, T, E, topk, H, I)

@@ -60,7 +60,7 @@ hipError_t launch_topk_v(const void *logits, const float *bias, int32_t *ids, fl
 
 // ---- The layer for a few tokens --------------------------------------------
 //
-// Bound by the bytes of the chosen experts' weights, each read once.  The pairs
+// Bound by the bytes of the chosen experts' weights, read once a unit.  The pairs
 // p = (token, place) are grouped into units of up to 8 pairs of one expert;
 //
 //  route: one workgroup makes the choice and writes the units (one token: the up
@@ -94,10 +94,8 @@ hipError_t launch_topk_v(const void *logits, const float *bias, int32_t *ids, fl
 // B columns, their rows staged in LDS.
 constexpr int FE_NARROW = 8;    // tokens with W = 8, G = 1, at most; more: W = 4, G = 2
 constexpr int FE_UNIT = 8;      // pairs of a unit, at most
-// Tokens, at most: 16 lanes each in the choice.  64 take 136 us here and 164 through
-// the tile kernels of the two stages, which 33 take as well (here 104).
-constexpr int MF_TOKENS = 64;
-constexpr int MF_PAIRS = 512;   // pairs, at most
+constexpr int MF_TOKENS = 64;   // tokens, at most: 16 lanes each in the choice
+constexpr int MF_PAIRS = 512;   // pairs, at most: the lists' room
 constexpr int MF_EXPERTS = 256; // experts, at most: 16 scores a lane
 constexpr int RT_THREADS = 1024;
 constexpr size_t FEW_LDS = 150 * 1024; // of a workgroup, at most, besides its lists
@@ -569,11 +567,35 @@ __global__ __launch_bounds__(256) void moe_few_join_kernel(const float *__restri
         uint2{f32x2_to_act2<DT_BF16>(v[0], v[1]), f32x2_to_act2<DT_BF16>(v[2], v[3])};
 }
 
-// Whether the kernels above take the layer: their lists and the staged rows fit.
+// Whether the kernels above take the layer: their lists and the staged rows fit, and
+// there are few pairs.  Up to 8 tokens an expert's pairs are one unit, so its weights are
+// read once.  With more an expert of c pairs has them read (most of it from caches)
+// ceil(c / 8) times, where the tile kernels of the two stages read them once and take
+// 32 rows at a time; and rows that leave a CU room for fewer than three workgroups
+// make each unit slower.  us, here / by the stages (graph replay):
+//   H x I         E   pairs: us
+//   2880 x 2880   4   128: 55 / 91   256: 82 / 95
+//                 8   256: 96 / 97   320: 105 / 100   384: 126 / 99   512: 148 / 102
+//                16   256: 110 / 127   320: 130 / 126   384: 145 / 126   512: 172 / 137
+//                32   256: 137 / 164   320: 149 / 169   384: 172 / 168   512: 207 / 170
+//                64   320: 213 / 311   512: 276 / 312
+//   2048 x 1408  64   384: 106 / 115   512: 126 / 118;   128   512: 169 / 193
+//   2048 x 768   32   384: 60 / 49;   64   384: 76 / 78;   128   512: 118 / 113
+//   4096 x 1792   8    64: 47 / 65   128: 63 / 67   256: 96 / 76
+//                16   256: 111 / 75;   32   256: 140 / 127;   64   256: 199 / 217   384: 231 / 220
+//   5120 x 2048  16    64: 88 / 93   128: 113 / 94
+//   7168 x 2048   8    64: 79 / 94;   64   128: 344 / 386   256: 411 / 400   512: 575 / 406
+//   2048 x 7168  32   128: 205 / 228
+//   8192 x 3584   8    32: 116 / 124    64: 150 / 127
 bool layer_few(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
 {
-    return T <= MF_TOKENS && T * topk <= MF_PAIRS && E <= MF_EXPERTS && H <= 32768 && I <= 32768 &&
-           few_lds<true, 4, 2>((int)T, (int)H) <= FEW_LDS && few_lds<false, 4, 2>((int)T, (int)I) <= FEW_LDS;
+    const int64_t P = T * topk;
+    if (T > MF_TOKENS || P > MF_PAIRS || E > MF_EXPERTS || H > 32768 || I > 32768)
+        return false;
+    const size_t lds = std::max(few_lds<true, 4, 2>((int)T, (int)H), few_lds<false, 4, 2>((int)T, (int)I));
+    if (lds > FEW_LDS)
+        return false;
+    return T <= FE_UNIT || P <= (3 * lds <= 160 * 1024 ? std::max<int64_t>(256, 10 * E) : std::max<int64_t>(96, 4 * E));
 }
 
 template <bool UP, bool ONE, int V, int W, int G, int SPW>
