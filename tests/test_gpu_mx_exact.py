@@ -127,3 +127,11 @@ def test_layer_ragged_steps(wob, T, H, I):
     (49, 8, 2, 64, 7168), (64, 64, 4, 4096, 128), (33, 64, 8, 4096, 64), (8, 8, 8, 7168, 128)])
 def test_layer_at_the_limits_of_pairs(wob, T, E, topk, H, I):
     _check_layer(wob, T, E, topk, H, I)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (1, 4104, 4096), (1, 4104, 4064), (8, 4112, 2880), (9, 4112, 2880),
+                                   (9, 4096, 2880), (9, 4112, 2048), (9, 4112, 2080), (16, 4104, 8192),
+                                   (16, 4096, 8192), (2, 8200, 1056)])
+def test_product_few_rows_workgroup_shapes(wob, M, N, K):
+    """One and two groups of rows a workgroup, eight and four waves a group."""
+    _check_product(wob, M, N, K)

@@ -832,11 +832,20 @@ hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t 
 {
     const Plan p = plan(M, N, K);
     if (p.path == Path::Few) {
-        // Eight waves on a group of rows and two groups where that still makes 128
-        // workgroups; with fewer rows one group each (2048 x 2048: 5.1 us with two
-        // groups, 2.9 with one), four waves if K leaves them no more than a few steps.
+        // Two groups of eight waves where one group a workgroup would be more than one a CU,
+        // and K gives the waves work; else one group, of four waves below 4096.  us, two
+        // groups / one:
+        //   256 workgroups of one group: 1 x 4096 x 14336 12.1 / 9.2, 8 x 4096 x 4096 6.9 / 5.5,
+        //   16 x 4096 x 8192 11.1 / 9.9
+        //   more: 1 x 5376 x 21504 17.0 / 17.8, 16 x 6144 x 8192 11.7 / 12.1, 8 x 16384 x 5376
+        //   11.2 / 12.4; but 1 x 16384 x 5376 10.7 / 10.4, 1 x 43008 x 5376 23.7 / 22.1
+        //   below 4096 (one group of four waves), more than 8 rows: 16 x 4104 x 2880 4.8 / 5.5,
+        //   13 x 5760 x 2880 5.2 / 5.7, 16 x 8192 x 2880 5.2 / 6.7; up to 8: 8 x 43008 x 2880
+        //   16.1 / 15.1, 1 x 16384 x 2880 7.4 / 6.8 (but 8 x 8192 x 2880 4.8 / 5.2)
+        //   up to 2048: 1 x 43008 x 2048 19.7 / 11.3, 16 x 43008 x 2048 20.5 / 15.1,
+        //   1 x 2048 x 2048 4.9 / 2.9
         const int groups = (N + FR_ROWS - 1) / FR_ROWS;
-        if (groups >= 256)
+        if (groups > 256 && (K >= 4096 || (K > 2048 && M > 8)))
             return launch_few<8, 2>(x, xs, w, ws, y, ydt, M, N, K, stream);
         if (K >= 4096)
             return launch_few<8, 1>(x, xs, w, ws, y, ydt, M, N, K, stream);
