@@ -59,7 +59,11 @@ __device__ __forceinline__ float4_t logit_value4(const void *p, int dt, int64_t 
                     act_to_f32((uint16_t)(v.y & 0xFFFFu), dt), act_to_f32((uint16_t)(v.y >> 16), dt)};
 }
 
-// exp(l - top) for l <= top; 1 where both are +inf, 0 for l = -inf below any top.
+// exp(l - top) for l <= top; 1 where both are +inf, 0 for l = -inf below any top.  The
+// hardware's exponential of d log2(e): off by 2^-22 and, from the rounding of d and of
+// the product, 2^-23 |d| of the value (4e-6 for a score 32 below the largest, where the
+// weight itself is 1e-14).  With expf 16384 tokens of 256 experts take 10.8 us instead of
+// 10.1, and 11.3 instead of 10.0 with the sum over all experts.
 __device__ __forceinline__ float exp_below(float l, float top)
 {
     return l == top ? 1.0f : __expf(l - top);

@@ -749,11 +749,12 @@ struct Plan {
 // K parts for `tiles` tiles so that up to one workgroup reaches each CU, at least
 // two spans each.  A part costs its sums' way through memory and the launch that
 // adds them, about 4.5 us, so there is one only where it takes five spans off the
-// longest workgroup: 100 x 5760 x 2880 11.9 us whole and 13.9 in two parts,
-// 100 x 4096 x 3584 8.6 and 9.9 in three, 100 x 2048 x 4096 9.3 and 8.7 in four,
-// 100 x 512 x 5376 11.7 and 8.0 in five.  Two workgroups on each CU bring nothing:
-// 100 x 16384 x 5376 19.1 us with 256 and 26.3 with 512.  (Measured with groups of one
-// stage.)
+// longest workgroup.  us, in parts / whole: 100 x 5376 x 21504 24.1 / 63.9, 32 x 5376 x
+// 21504 21.6 / 37.6, 100 x 2048 x 4096 (eight spans in four) 9.2 / 11.5, 48 x 5376 x 5376
+// 10.9 / 12.4; where the rule says whole: 100 x 5760 x 2880 13.4 / 13.0, 20 x 8192 x 3584 9.7 /
+// 9.2, but 100 x 4096 x 3584 (seven spans in three) 10.8 / 11.4.  Two workgroups on each CU
+// bring nothing, one / two: 100 x 16384 x 5376 18.6 / 22.8, 64 x 16384 x 5376 15.0 / 20.7, 100 x
+// 5376 x 21504 24.1 / 28.3 (32 x 5376 x 21504 21.6 / 20.7).
 int k_parts(int64_t tiles, int64_t K)
 {
     const int64_t spans = (K + MX_SPAN - 1) / MX_SPAN;
