@@ -233,11 +233,14 @@ hipError_t launch_few(const uint8_t *x, const uint8_t *xs, const uint8_t *w, con
 // 114, packed 110 with the packing; 100 x 5376 x 21504, where the scales are
 // a larger share, 2.4 us less straight than packed.  (Whole: see tile_scales.)
 //
-// 2048 x 16384 x 5376, 108 us: 3.4 PFLOP/s.  The clock falls to 1.6 GHz: with zero
-// codes, which switch little, the same launches take 92 us.  Packing takes 5 of it,
-// the stores of 67 MB 9 (few of them overlap), the copies 3 beyond copies that hit;
-// x straight from memory into registers, which halves the traffic of LDS, brings
-// nothing.
+// 2048 x 16384 x 5376, 107 us: 3.4 PFLOP/s, MFMA busy 53 % of the time.  Timing-only
+// forms: the MFMAs alone, from registers, 47 us; with the reads of their operands from
+// LDS 60; all but the copies and the stores 75; without the packing 101.  So the
+// pipeline's waits and barriers take 15, the copies about 15, the stores of 67 MB 9 to 11
+// (nothing multiplies meanwhile on the CU, and 48 of the 512 registers of the 256 x 256
+// tile spill where they begin), the packing 5.6.  The clock is at 1.6 GHz meanwhile: with
+// zero codes, which switch little, the same launches take 92.  x straight from memory
+// into registers, which halves the traffic of LDS, brings nothing.
 //
 // A stage is two MFMA steps of 64 k: in step j the lane half h = lane / 32
 // supplies block 2 h + j of its row, so a lane needs bytes 2 h, 2 h + 1 of each
