@@ -135,3 +135,11 @@ def test_layer_at_the_limits_of_pairs(wob, T, E, topk, H, I):
 def test_product_few_rows_workgroup_shapes(wob, M, N, K):
     """One and two groups of rows a workgroup, eight and four waves a group."""
     _check_product(wob, M, N, K)
+
+
+@pytest.mark.parametrize("M,N,K", [(2048, 8704, 96), (2048, 4096, 96), (1030, 14000, 96), (1030, 14000, 640),
+                                   (300, 16384, 224), (300, 16392, 224), (128, 16384, 96), (128, 16400, 128),
+                                   (250, 8192, 96), (250, 8256, 96), (64, 16384, 96), (65, 16384, 96)])
+def test_product_on_both_sides_of_the_tiles_limits(wob, M, N, K):
+    """By rounds of 256 x 256 and 128 x 128 tiles, by the number of small and middle tiles, by rows."""
+    _check_product(wob, M, N, K)
