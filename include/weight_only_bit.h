@@ -75,6 +75,15 @@ extern "C" {
 #define WOB_ACT_NONE 0     /* pre-activation output [T][topk][N] */
 #define WOB_ACT_SILU_MUL 1 /* silu(gate) * up: output [T][topk][N/2] */
 
+/* What residual_norm writes its normed rows as (the `quant` argument). */
+#define WOB_QUANT_NONE 0  /* values of the block's type */
+#define WOB_QUANT_INT8 1  /* int8 codes and one fp32 scale a row, as int8_quantize */
+#define WOB_QUANT_MXFP4 2 /* E2M1 codes and one E8M0 scale per 32, as mxfp4_quantize */
+
+/* Scores of moe_route (the `score` argument). */
+#define WOB_SCORE_SIGMOID 0
+#define WOB_SCORE_SOFTMAX 1
+
 /* Kernel path selection for w4a16_gemm_ex. */
 #define WOB_PATH_AUTO 0   /* M <= 8 (and X fits the skinny kernel's LDS) -> skinny, else tiled */
 #define WOB_PATH_SKINNY 1 /* split-K GEMV; requires M <= 8 */
@@ -351,6 +360,121 @@ int mxfp4_moe_layer(const void *x, const void *logits, int logits_dtype, const f
                     const uint8_t *w2_scale, void *y, int64_t T, int64_t topk, int64_t E, int64_t H,
                     int64_t I, int renormalize, void *workspace, size_t workspace_bytes,
                     void *stream);
+
+/*
+ * Rows in 8 bits: codes and one scale for each row (token), the operands of
+ * int8_gemm.  With
+ *   v_k = x_k (act == WOB_ACT_NONE), or
+ *   v_k = silu(x_k) * x_{K+k} (WOB_ACT_SILU_MUL; a row of x holds a gate half and an
+ *         up half, 2 K elements; silu(v) = v / (1 + e^-v)), in fp32:
+ *   amax = max |v_k|,  scale = amax / 127,
+ *   code_k = v_k * (127 / amax) rounded to nearest, ties to even: -127 .. 127
+ * A row of zeros gets scale 0 and codes 0.  A row with a v_k that is not finite
+ * gets scale NaN and codes 0: it reads back as NaN.
+ *
+ *  x: R rows, `ldx` elements from one row's start to the next's (ldx >= K, or 2 K);
+ *    x_dtype WOB_F16, WOB_BF16 or WOB_F32 (else WOB_DTYPE).
+ *  codes [R][K] int8, scale [R] fp32; both contiguous.
+ *  K % 16 == 0, 16 <= K <= 65536, R >= 0, R*K at most 2^34; rows start 16-byte
+ *  aligned: ldx % 8 == 0 (% 4 for WOB_F32) (else WOB_INVALID_ARG).
+ *  R == 0 is a no-op returning WOB_OK.
+ */
+int int8_quantize(const void *x, int x_dtype, int64_t ldx, int act, int8_t *codes, float *scale,
+                  int64_t R, int64_t K, void *stream);
+
+/*
+ * Rows in 8 bits read back: out[r][k] = codes[r][k] * scale[r], rounded once to
+ * out_dtype (WOB_F16, WOB_BF16 or WOB_F32, else WOB_DTYPE).  codes [R][K] int8, scale
+ * [R] fp32, out [R][K]; shapes as for int8_quantize.
+ */
+int int8_dequant(const int8_t *codes, const float *scale, void *out, int out_dtype, int64_t R,
+                 int64_t K, void *stream);
+
+/*
+ * Bytes of device workspace int8_gemm needs (0 when it needs none, and for
+ * arguments it refuses on sight: a negative size, K outside 16 .. 131056).
+ */
+size_t int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/*
+ * 8-bit product with a scale for each token and each channel:
+ *   y[m][n] = x_scale[m] * w_scale[n] * sum_k x_q[m][k] * w_q[n][k] + bias[n]
+ *  x_q [M][K], w_q [N][K] int8 (all 256 values); x_scale [M], w_scale [N] fp32; bias
+ *  [N] fp32 or NULL; y [M][N] of y_dtype WOB_F16, WOB_BF16 or WOB_F32 (else WOB_DTYPE).
+ *  The sum is exact in 32 bits.  It is rounded to fp32, multiplied with x_scale[m],
+ *  then with w_scale[n], the bias is added, each in fp32, and y is rounded once more,
+ *  to nearest even.  A NaN scale makes every output of its row or column NaN.
+ *  K % 16 == 0, 16 <= K <= 131056, N % 8 == 0, M >= 0, N >= 0, M*K and N*K below
+ *  2^32, M and N below 2^27 (else WOB_INVALID_ARG).  M == 0 or N == 0 is a no-op
+ *  returning WOB_OK.
+ *  workspace: device memory of at least int8_gemm_workspace_size(M, N, K) bytes,
+ *  16-byte aligned (may be NULL when that is 0, else WOB_INVALID_ARG); its contents on
+ *  entry do not matter.  Calls that share one workspace must be ordered on one stream.
+ */
+int int8_gemm(const int8_t *x_q, const float *x_scale, const int8_t *w_q, const float *w_scale,
+              const float *bias, void *y, int y_dtype, int64_t M, int64_t N, int64_t K,
+              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The norms after a block and before the next, with the block's gate and residual
+ * scale, in one pass over T rows of H elements:
+ *   t = y, or y / sqrt(mean(y^2) + eps) * post_weight   (post_weight != NULL)
+ *   h = residual + alpha * gate * t                     (gate NULL: 1)
+ *   n = h / sqrt(mean(h^2) + eps) * weight
+ * in fp32.  residual_out = h rounded once to the residual's type; n, from the
+ * unrounded h, as `quant` says: rounded once to `dtype`, in 8-bit rows as by
+ * int8_quantize, or in MXFP4 blocks as by mxfp4_quantize.
+ *
+ *  dtype (of y, post_weight, gate, weight and n): WOB_F16, WOB_BF16 or WOB_F32;
+ *  residual_dtype (of residual and residual_out): dtype or WOB_F32 (else WOB_DTYPE).
+ *  y [T] rows, `ldy` elements apart (ldy >= H).  y NULL: h = residual; post_weight and
+ *    gate must be NULL, residual_out may be.
+ *  residual, residual_out [T][H] contiguous; residual_out may be residual itself.
+ *  gate: rows `ldg` elements apart (ldg >= H), or ldg == 0 for one row [H] that all
+ *    rows share.  post_weight, weight [H].
+ *  weight NULL: n is not computed (n and n_scale NULL, quant WOB_QUANT_NONE); y must
+ *    be given.
+ *  n [T][H] of dtype, n_scale NULL; or codes [T][H] int8 and n_scale [T] fp32; or codes
+ *    [T][H/2] uint8 and n_scale [T][H/32] uint8.  Outputs overlap no operand and no
+ *    other output, but for residual_out as said.
+ *  eps >= 0 and alpha finite; 8 <= H <= 32768, H % 8 == 0 (H % 16 == 0 for 8-bit rows,
+ *  H % 32 == 0 for MXFP4), T >= 0, T*H at most 2^34; rows start 16-byte aligned: ldy
+ *  and ldg % 8 == 0 (% 4 for WOB_F32) (else WOB_INVALID_ARG).
+ *  T == 0 is a no-op returning WOB_OK.
+ */
+int residual_norm(const void *y, int dtype, int64_t ldy, const void *residual, int residual_dtype,
+                  const void *post_weight, const void *gate, int64_t ldg, float alpha,
+                  const void *weight, float eps, int quant, void *n, void *n_scale,
+                  void *residual_out, int64_t T, int64_t H, void *stream);
+
+/*
+ * Group-limited choice of experts.  For each of T tokens, with E experts in `groups`
+ * groups of E / groups consecutive ones:
+ *   s_e = 1 / (1 + e^-l_e) (WOB_SCORE_SIGMOID), or exp(l_e - max l) / sum exp(l - max l)
+ *         (WOB_SCORE_SOFTMAX, over all experts), rounded correctly to fp32 (but for
+ *         one value in about 2^28, which may be its neighbour)
+ *   c_e = s_e + bias_e in fp32 (bias NULL: s_e); it decides the choice alone
+ *   kept groups: the topk_groups with the largest value, the value being the sum (fp32)
+ *         of the group's group_top (1 or 2) largest c; ties to the lowest group
+ *   ids     [T][topk] int32: the topk largest c in the kept groups, largest first, ties
+ *           to the lowest expert
+ *   weights [T][topk] fp32: scale * s_id, over the sum of the chosen s (renormalize != 0;
+ *           0 where that sum is 0)
+ * An expert whose logit or choice value is -inf or NaN is never chosen, and adds nothing
+ * to its group; a group without another is not kept.  Places left over get id -1 and weight 0.
+ * Where the largest logit is +inf, the softmax shares equally among the experts that
+ * have it.
+ *
+ *  logits [T][E] of logits_dtype WOB_F16, WOB_BF16 or WOB_F32 (else WOB_DTYPE), bias [E]
+ *  fp32 or NULL.
+ *  T >= 0, T below 2^25, 1 <= E <= 1024, 1 <= groups <= 64, E % groups == 0,
+ *  1 <= topk_groups <= groups, group_top 1 or 2, 1 <= topk <= 64, topk at most
+ *  topk_groups * (E / groups), scale finite (else WOB_INVALID_ARG).  T == 0 is a no-op
+ *  returning WOB_OK.
+ */
+int moe_route(const void *logits, int logits_dtype, const float *bias, int32_t *ids, float *weights,
+              int64_t T, int64_t E, int64_t topk, int score, int64_t groups, int64_t topk_groups,
+              int group_top, int renormalize, float scale, void *stream);
 
 /*
  * Dequantization probes: write out the weights as the GEMM kernels form them,

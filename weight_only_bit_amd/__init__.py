@@ -13,6 +13,10 @@ fallback.
     y = mxfp4_moe_layer(x, logits, topk, w1_fp4, w1_scale, w2_fp4, w2_scale)  # a whole MoE layer
     codes, scale = mxfp4_quantize(x)                        # 16/32-bit rows -> MXFP4
     y = mxfp4_gemm(x_fp4, x_scale, w_fp4, w_scale)          # MXFP4 x MXFP4
+    codes, scale = int8_quantize(x)                         # 16/32-bit rows -> int8 rows
+    y = int8_gemm(x_q, x_scale, w_q, w_scale)               # int8 x int8, scales per row and column
+    n, h = residual_norm(y, residual, weight)               # the norms around a block
+    ids, weights = moe_route(logits, topk, bias, groups=8, topk_groups=4)  # group-limited choice
 
 Layouts are those of ``include/weight_only_bit.h``.
 """
@@ -22,31 +26,34 @@ import functools
 
 from . import _lib
 from ._lib import (ACT_NONE, ACT_SILU_MUL, BF16, DTYPE, F16, F32, INVALID_ARG, OK, PATH_AUTO,
-                   PATH_SKINNY, PATH_TILED, U4X8_I32, UNSUPPORTED, WobArgError, WobDtypeError,
-                   WobError)
+                   PATH_SKINNY, PATH_TILED, QUANT_INT8, QUANT_MXFP4, QUANT_NONE, SCORE_SIGMOID,
+                   SCORE_SOFTMAX, U4X8_I32, UNSUPPORTED, WobArgError, WobDtypeError, WobError)
 
 __all__ = [
     "gemm", "gemm_grouped", "mxfp4_moe_gemm", "moe_workspace_size", "mxfp4_moe_stage2",
     "moe_stage2_workspace_size", "moe_topk", "mxfp4_moe_layer", "moe_layer_workspace_size",
-    "mxfp4_quantize", "mxfp4_gemm", "mxfp4_gemm_workspace_size", "w4a16_dequant",
-    "mxfp4_dequant", "stream_read", "device_check", "WobError", "WobDtypeError", "WobArgError",
-    "PATH_AUTO", "PATH_SKINNY", "PATH_TILED", "ACT_NONE", "ACT_SILU_MUL",
+    "mxfp4_quantize", "mxfp4_gemm", "mxfp4_gemm_workspace_size", "int8_quantize",
+    "int8_dequant", "int8_gemm", "int8_gemm_workspace_size", "residual_norm", "moe_route",
+    "w4a16_dequant", "mxfp4_dequant", "stream_read", "device_check", "WobError", "WobDtypeError",
+    "WobArgError", "PATH_AUTO", "PATH_SKINNY", "PATH_TILED", "ACT_NONE", "ACT_SILU_MUL",
+    "QUANT_NONE", "QUANT_INT8", "QUANT_MXFP4", "SCORE_SIGMOID", "SCORE_SOFTMAX",
 ]
 
 
 _torch_mod = None
 _tags = None
-_raw_stream = _get_device = _values = _bytes = None
+_raw_stream = _get_device = _values = _bytes = _int8 = _fp32 = None
 
 
 def _torch():
     """torch, imported on first use; the dtype tags and the device and stream queries with it."""
-    global _torch_mod, _tags, _values, _bytes, _raw_stream, _get_device
+    global _torch_mod, _tags, _values, _bytes, _int8, _fp32, _raw_stream, _get_device
     if _torch_mod is None:
         import torch
         _tags = {torch.float16: F16, torch.bfloat16: BF16, torch.int32: U4X8_I32,
                  torch.float32: F32}
         _values, _bytes = (torch.float16, torch.bfloat16, torch.float32), (torch.uint8,)
+        _int8, _fp32 = (torch.int8,), (torch.float32,)
         # the current stream's handle without building a Stream object: 0.1
         # against 1.9 us, in calls whose launch takes 3
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -430,6 +437,233 @@ def mxfp4_moe_layer(x, logits, topk: int, w1_fp4, w1_scale, w2_fp4, w2_scale, bi
                _ptr(workspace), ws_bytes)
     _lib.check(st, "mxfp4_moe_layer")
     return out
+
+
+def _row_count(lead):
+    R = 1
+    for n in lead:
+        R *= n
+    return R
+
+
+def _row_stride(x, name):
+    """Elements from one row of x [..., K] to the next: x is contiguous, or 2-D with
+    contiguous elements in each row (a column slice)."""
+    K = x.shape[-1]
+    if x.is_contiguous():
+        return K
+    if x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= K:
+        return x.stride(0)
+    raise ValueError(f"{name} must be contiguous, or a 2-D column slice of a contiguous tensor")
+
+
+def int8_quantize(x, act: int = ACT_NONE, out=None, out_scale=None):
+    """Rows in 8 bits: x [..., K] fp16/bf16/fp32 -> (codes [..., K] int8, scale [...]
+    float32), scale = amax / 127 of each row, the operands of int8_gemm.  act=ACT_SILU_MUL:
+    x [..., 2K] holds gate and up halves, and silu(gate) * up is quantised.  x is
+    contiguous, or 2-D with contiguous elements in each row and rows any 16-byte aligned
+    distance apart (a column slice)."""
+    torch = _torch()
+    if x.dim() < 1:
+        raise ValueError("x must be [..., K]")
+    _want(x, "x", x.shape, _values)
+    if act not in (ACT_NONE, ACT_SILU_MUL):
+        raise ValueError(f"unknown activation {act}")
+    K = x.shape[-1]
+    if act == ACT_SILU_MUL:
+        if K % 2 != 0:
+            raise ValueError(f"x has {K} columns; gate and up halves make an even number")
+        K //= 2
+    if not 16 <= K <= 65536 or K % 16 != 0:
+        raise ValueError(f"K={K} must be a multiple of 16, up to 65536")
+    lead = x.shape[:-1]
+    ldx = _row_stride(x, "x")
+    dev = x.device
+    out = _output(out, "out", (*lead, K), torch.int8, dev)
+    out_scale = _output(out_scale, "out_scale", tuple(lead), torch.float32, dev)
+    if x.get_device() < 0:
+        raise ValueError("all operands must be device tensors")
+    st = _run(_lib.lib().int8_quantize, dev, x.data_ptr(), _tags[x.dtype], ldx, act, out.data_ptr(),
+              out_scale.data_ptr(), _row_count(lead), K)
+    _lib.check(st, "int8_quantize")
+    return out, out_scale
+
+
+def int8_dequant(codes, scale, out_dtype=None, out=None):
+    """Rows in 8 bits read back: codes [..., K] int8 and scale [...] float32 -> values
+    [..., K] in out_dtype (bfloat16 when neither it nor out is given)."""
+    torch = _torch()
+    if codes.dim() < 1:
+        raise ValueError("codes must be [..., K]")
+    _want(codes, "codes", codes.shape, _int8)
+    lead, K = codes.shape[:-1], codes.shape[-1]
+    if not 16 <= K <= 65536 or K % 16 != 0:
+        raise ValueError(f"K={K} must be a multiple of 16, up to 65536")
+    _want(scale, "scale", lead, _fp32)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    if out_dtype not in _values:
+        raise TypeError(f"out_dtype {out_dtype} must be float16, bfloat16 or float32")
+    dev = codes.device
+    out = _output(out, "out", tuple(codes.shape), out_dtype, dev)
+    _check_device(codes, scale)
+    st = _run(_lib.lib().int8_dequant, dev, codes.data_ptr(), scale.data_ptr(), out.data_ptr(),
+              _tags[out_dtype], _row_count(lead), K)
+    _lib.check(st, "int8_dequant")
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def int8_gemm_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes of workspace int8_gemm needs (0 also for arguments it refuses)."""
+    return int(_lib.lib().int8_gemm_workspace_size(M, N, K))
+
+
+def int8_gemm(x_q, x_scale, w_q, w_scale, bias=None, out=None, out_dtype=None, workspace=None):
+    """8-bit product: x_q [M,K] int8 with x_scale [M] float32 (a token's), w_q [N,K] int8
+    with w_scale [N] float32 (a channel's) -> y [M,N] = x_scale * w_scale * (x_q . w_q^T)
+    (+ bias [N] float32) in out_dtype (bfloat16 when neither it nor out is given; float16
+    and float32 too).  The sum over K is exact."""
+    torch = _torch()
+    if x_q.dim() != 2 or w_q.dim() != 2:
+        raise ValueError("x_q must be [M, K] and w_q [N, K]")
+    M, K = x_q.shape
+    N = w_q.shape[0]
+    _want(x_q, "x_q", (M, K), _int8)
+    _want(x_scale, "x_scale", (M,), _fp32)
+    _want(w_q, "w_q", (N, K), _int8)
+    _want(w_scale, "w_scale", (N,), _fp32)
+    if bias is not None:
+        _want(bias, "bias", (N,), _fp32)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    if out_dtype not in _values:
+        raise TypeError(f"out_dtype {out_dtype} must be float16, bfloat16 or float32")
+    dev = x_q.device
+    out = _output(out, "out", (M, N), out_dtype, dev)
+    workspace, ws_bytes = _workspace(workspace, int8_gemm_workspace_size(M, N, K), dev)
+    _check_device(x_q, x_scale, w_q, w_scale, bias, workspace)
+    st = _run(_lib.lib().int8_gemm, dev, x_q.data_ptr(), x_scale.data_ptr(), w_q.data_ptr(),
+              w_scale.data_ptr(), _ptr(bias), out.data_ptr(), _tags[out_dtype], M, N, K,
+              _ptr(workspace), ws_bytes)
+    _lib.check(st, "int8_gemm")
+    return out
+
+
+def residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: float = 1.0,
+                  eps: float = 1e-6, quant: int = QUANT_NONE, out=None, out_scale=None,
+                  residual_out=None):
+    """The norms after a block and before the next, with its gate and residual scale:
+
+        t = y, or y / rms(y) * post_weight;  h = residual + alpha * gate * t
+        n = h / rms(h) * weight,             rms(v) = sqrt(mean(v^2) + eps)
+
+    y [T,H] fp16/bf16/fp32 (contiguous or a column slice); residual [T,H] in y's dtype
+    or float32; weight, post_weight [H]; gate [H] or [T,H] (contiguous or a column slice).
+    Returns (n, h) with h in residual's dtype and n in y's, or (codes, scale, h) with
+    quant=QUANT_INT8 (as int8_quantize) or QUANT_MXFP4 (as mxfp4_quantize).  residual_out
+    may be residual itself.  y=None: n of the residual alone (then h is residual, and n has
+    weight's dtype).  weight=None: no n (it is returned as None)."""
+    torch = _torch()
+    if residual.dim() != 2:
+        raise ValueError("residual must be [T, H]")
+    T, H = residual.shape
+    block = y if y is not None else weight
+    if block is None:
+        raise ValueError("y and weight are both missing: there is nothing to compute")
+    dt = block.dtype
+    if dt not in _values:
+        raise TypeError(f"dtype {dt} must be float16, bfloat16 or float32")
+    own, shape = (dt,), (T, H)
+    _want(residual, "residual", shape, (dt, torch.float32))
+    if quant not in (QUANT_NONE, QUANT_INT8, QUANT_MXFP4):
+        raise ValueError(f"unknown quant {quant}")
+    whole = 32 if quant == QUANT_MXFP4 else 16 if quant == QUANT_INT8 else 8
+    if not whole <= H <= 32768 or H % whole != 0:
+        raise ValueError(f"H={H} must be a multiple of {whole}, up to 32768")
+    ldy = ldg = 0
+    dev = residual.device
+    if y is not None:
+        _want(y, "y", shape, own)
+        ldy = _row_stride(y, "y")
+        if post_weight is not None:
+            _want(post_weight, "post_weight", (H,), own)
+        if gate is not None:
+            if gate.dim() == 1:
+                _want(gate, "gate", (H,), own)
+                if not gate.is_contiguous():
+                    raise ValueError("gate [H] must be contiguous")
+            else:
+                _want(gate, "gate", shape, own)
+                ldg = _row_stride(gate, "gate")
+        if residual_out is not residual:
+            residual_out = _output(residual_out, "residual_out", shape, residual.dtype, dev)
+    elif post_weight is not None or gate is not None:
+        raise ValueError("without y there is no post_weight and no gate")
+    elif residual_out is not None:
+        raise ValueError("without y the residual does not change: residual_out must be None")
+    if weight is None:
+        if quant != QUANT_NONE or out is not None or out_scale is not None:
+            raise ValueError("without weight there are no normed rows")
+    else:
+        _want(weight, "weight", (H,), own)
+        if quant == QUANT_NONE:
+            if out_scale is not None:
+                raise ValueError("out_scale without quantised rows")
+            out = _output(out, "out", shape, dt, dev)
+        elif quant == QUANT_INT8:
+            out = _output(out, "out", shape, torch.int8, dev)
+            out_scale = _output(out_scale, "out_scale", (T,), torch.float32, dev)
+        else:
+            out = _output(out, "out", (T, H // 2), torch.uint8, dev)
+            out_scale = _output(out_scale, "out_scale", (T, H // 32), torch.uint8, dev)
+    _check_device(residual, weight, post_weight)
+    for t in (y, gate):  # these may be column slices
+        if t is not None and t.device != dev:
+            raise ValueError("operands live on different devices")
+    st = _run(_lib.lib().residual_norm, dev, _ptr(y), _tags[dt], ldy, residual.data_ptr(),
+              _tags[residual.dtype], _ptr(post_weight), _ptr(gate), ldg, alpha, _ptr(weight), eps,
+              quant, _ptr(out), _ptr(out_scale), _ptr(residual_out), T, H)
+    _lib.check(st, "residual_norm")
+    h = residual if y is None else residual_out
+    return (out, h) if quant == QUANT_NONE else (out, out_scale, h)
+
+
+def moe_route(logits, topk: int, bias=None, score: int = SCORE_SIGMOID, groups: int = 1,
+              topk_groups: int = 1, group_top: int = 2, renormalize: bool = True,
+              scale: float = 1.0, ids=None, weights=None):
+    """Group-limited choice of experts: logits [T,E] fp16/bf16/fp32 -> (ids [T,topk] int32,
+    weights [T,topk] float32), what the MoE stages take.  Scores s: sigmoid of the logits,
+    or their softmax over all experts.  The choice goes by s + bias (bias [E] float32): the
+    topk_groups groups with the largest sum of their group_top (1 or 2) best, then the topk
+    best experts in them, ties to the lowest index.  weights: scale * s, over the chosen
+    experts' sum with renormalize.  Places without an expert hold id -1 and weight 0."""
+    torch = _torch()
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    _want(logits, "logits", logits.shape, _values)
+    T, E = logits.shape
+    if score not in (SCORE_SIGMOID, SCORE_SOFTMAX):
+        raise ValueError(f"unknown score {score}")
+    if not 1 <= groups <= 64 or not 1 <= E <= 1024 or E % groups != 0:
+        raise ValueError(f"E={E} (up to 1024) must be a multiple of groups={groups} (up to 64)")
+    if not 1 <= topk_groups <= groups:
+        raise ValueError(f"topk_groups={topk_groups} must be between 1 and groups={groups}")
+    if not 1 <= topk <= min(64, topk_groups * (E // groups)):
+        raise ValueError(f"topk={topk} must be between 1 and 64 and at most the kept groups' experts")
+    if group_top not in (1, 2):
+        raise ValueError(f"group_top={group_top} must be 1 or 2")
+    if bias is not None:
+        _want(bias, "bias", (E,), _fp32)
+    dev = logits.device
+    ids = _output(ids, "ids", (T, topk), torch.int32, dev)
+    weights = _output(weights, "weights", (T, topk), torch.float32, dev)
+    _check_device(logits, bias)
+    st = _run(_lib.lib().moe_route, dev, logits.data_ptr(), _tags[logits.dtype], _ptr(bias),
+              ids.data_ptr(), weights.data_ptr(), T, E, topk, score, groups, topk_groups, group_top,
+              1 if renormalize else 0, scale)
+    _lib.check(st, "moe_route")
+    return ids, weights
 
 
 def w4a16_dequant(qweight, scales, qzeros, group_size: int, out_dtype=None):

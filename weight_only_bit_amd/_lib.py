@@ -16,6 +16,8 @@ OK, INVALID_ARG, DTYPE, UNSUPPORTED, HIP = 0, 1, 2, 3, 4
 F16, BF16, U4X8_I32, F32 = 0, 1, 2, 3
 PATH_AUTO, PATH_SKINNY, PATH_TILED = 0, 1, 2
 ACT_NONE, ACT_SILU_MUL = 0, 1
+QUANT_NONE, QUANT_INT8, QUANT_MXFP4 = 0, 1, 2
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
 
 EXPORTS = [
     "wob_status_str", "wob_last_error", "wob_device_check",
@@ -25,6 +27,8 @@ EXPORTS = [
     "mxfp4_moe_stage2_workspace_size", "mxfp4_moe_stage2",
     "mxfp4_quantize", "mxfp4_gemm_workspace_size", "mxfp4_gemm",
     "moe_topk", "mxfp4_moe_layer_workspace_size", "mxfp4_moe_layer",
+    "int8_quantize", "int8_dequant", "int8_gemm_workspace_size", "int8_gemm",
+    "residual_norm", "moe_route",
     "w4a16_dequant", "mxfp4_dequant", "wob_stream_read",
 ]
 
@@ -32,6 +36,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
+_f = ctypes.c_float
 
 _SIGNATURES = {
     "wob_status_str": (ctypes.c_char_p, [_i]),
@@ -58,6 +63,13 @@ _SIGNATURES = {
     "mxfp4_moe_layer_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i64]),
     "mxfp4_moe_layer": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
                              _i64, _i, _vp, _sz, _vp]),
+    "int8_quantize": (_i, [_vp, _i, _i64, _i, _vp, _vp, _i64, _i64, _vp]),
+    "int8_dequant": (_i, [_vp, _vp, _vp, _i, _i64, _i64, _vp]),
+    "int8_gemm_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "int8_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i64, _i64, _i64, _vp, _sz, _vp]),
+    "residual_norm": (_i, [_vp, _i, _i64, _vp, _i, _vp, _vp, _i64, _f, _vp, _f, _i, _vp, _vp, _vp,
+                           _i64, _i64, _vp]),
+    "moe_route": (_i, [_vp, _i, _vp, _vp, _vp, _i64, _i64, _i64, _i, _i64, _i64, _i, _i, _f, _vp]),
     "w4a16_dequant": (_i, [_vp, _vp, _i, _vp, _i, _vp, _i, _i64, _i64, _i64, _vp]),
     "mxfp4_dequant": (_i, [_vp, _vp, _vp, _i64, _i64, _vp]),
     "wob_stream_read": (_i, [_vp, _sz, _vp, _vp]),

@@ -6,6 +6,7 @@
 #include "wob_internal.hpp"
 
 #include <limits.h>
+#include <math.h>
 #include <stdint.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -587,6 +588,238 @@ int mxfp4_moe_layer(const void *x, const void *logits, int logits_dtype, const f
     a.renormalize = renormalize != 0;
     return launched(wob::launch_mxfp4_moe_layer(a, workspace, static_cast<hipStream_t>(stream)),
                     "mxfp4 moe layer");
+}
+
+namespace {
+
+constexpr int64_t ELEMENTS = (int64_t)1 << 34; // of one operand of the row operators, at most
+
+bool value_dtype(int dt) { return dt == WOB_F16 || dt == WOB_BF16 || dt == WOB_F32; }
+
+// A row stride in elements that covers `width` and keeps rows 16-byte aligned.
+bool row_stride(int64_t ld, int64_t width, int dt)
+{
+    return ld >= width && ld % (dt == WOB_F32 ? 4 : 8) == 0 && ld <= ((int64_t)1 << 40);
+}
+
+int check_int8_rows(int64_t R, int64_t K)
+{
+    if (R < 0 || K < 16 || K > 65536 || K % 16 != 0)
+        return fail(WOB_INVALID_ARG, "bad shape R=%lld K=%lld (K: a multiple of 16, up to 65536)",
+                    (long long)R, (long long)K);
+    if (R > ELEMENTS / K)
+        return fail(WOB_INVALID_ARG, "shape too large");
+    return WOB_OK;
+}
+
+} // namespace
+
+int int8_quantize(const void *x, int x_dtype, int64_t ldx, int act, int8_t *codes, float *scale,
+                  int64_t R, int64_t K, void *stream)
+{
+    if (!value_dtype(x_dtype))
+        return fail(WOB_DTYPE, "x dtype tag %d is not F16, BF16 or F32", x_dtype);
+    if (act != WOB_ACT_NONE && act != WOB_ACT_SILU_MUL)
+        return fail(WOB_INVALID_ARG, "unknown activation %d", act);
+    int s = check_int8_rows(R, K);
+    if (s != WOB_OK)
+        return s;
+    const int64_t width = act == WOB_ACT_SILU_MUL ? 2 * K : K;
+    if (!row_stride(ldx, width, x_dtype) || (R && ldx > ((int64_t)1 << 60) / R))
+        return fail(WOB_INVALID_ARG, "row stride %lld is below %lld, too large or leaves rows unaligned",
+                    (long long)ldx, (long long)width);
+    if (R == 0)
+        return ok();
+    if (!x || !codes || !scale)
+        return fail(WOB_INVALID_ARG, "null operand pointer");
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scale))
+        return fail(WOB_INVALID_ARG, "operand pointers must be 16-byte aligned");
+    s = arch_gate();
+    if (s != WOB_OK)
+        return s;
+    return launched(wob::launch_int8_quantize(x, x_dtype, ldx, act, codes, scale, R, (int)K,
+                                              static_cast<hipStream_t>(stream)),
+                    "int8 quantize");
+}
+
+int int8_dequant(const int8_t *codes, const float *scale, void *out, int out_dtype, int64_t R,
+                 int64_t K, void *stream)
+{
+    if (!value_dtype(out_dtype))
+        return fail(WOB_DTYPE, "out dtype tag %d is not F16, BF16 or F32", out_dtype);
+    int s = check_int8_rows(R, K);
+    if (s != WOB_OK)
+        return s;
+    if (R == 0)
+        return ok();
+    if (!codes || !scale || !out)
+        return fail(WOB_INVALID_ARG, "null operand pointer");
+    if (!aligned16(codes) || !aligned16(scale) || !aligned16(out))
+        return fail(WOB_INVALID_ARG, "operand pointers must be 16-byte aligned");
+    s = arch_gate();
+    if (s != WOB_OK)
+        return s;
+    return launched(wob::launch_int8_dequant(codes, scale, out, out_dtype, R, (int)K,
+                                             static_cast<hipStream_t>(stream)),
+                    "int8 dequant");
+}
+
+namespace {
+
+constexpr int64_t INT8_K = 131056; // the largest K % 16 == 0 whose sums of (-128)^2 stay below 2^31
+
+} // namespace
+
+size_t int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 0 || N < 0 || K < 16 || M >= GEMM_ROWS || N >= GEMM_ROWS || K > INT8_K)
+        return 0;
+    return wob::int8_gemm_workspace_bytes(M, N, K);
+}
+
+int int8_gemm(const int8_t *x_q, const float *x_scale, const int8_t *w_q, const float *w_scale,
+              const float *bias, void *y, int y_dtype, int64_t M, int64_t N, int64_t K,
+              void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!value_dtype(y_dtype))
+        return fail(WOB_DTYPE, "y dtype tag %d is not F16, BF16 or F32", y_dtype);
+    if (M < 0 || N < 0 || K < 16 || K > INT8_K)
+        return fail(WOB_INVALID_ARG, "bad shape M=%lld N=%lld K=%lld", (long long)M, (long long)N,
+                    (long long)K);
+    if (K % 16 != 0 || N % 8 != 0)
+        return fail(WOB_INVALID_ARG, "need K %% 16 == 0 and N %% 8 == 0 (K=%lld N=%lld)",
+                    (long long)K, (long long)N);
+    // 32-bit in-kernel offsets into each operand's codes
+    if (M >= GEMM_ROWS || N >= GEMM_ROWS || M * K > (int64_t)UINT32_MAX || N * K > (int64_t)UINT32_MAX)
+        return fail(WOB_INVALID_ARG, "shape too large");
+    if (M == 0 || N == 0)
+        return ok();
+    if (!x_q || !x_scale || !w_q || !w_scale || !y)
+        return fail(WOB_INVALID_ARG, "null operand pointer");
+    if (!aligned16(x_q) || !aligned16(x_scale) || !aligned16(w_q) || !aligned16(w_scale) ||
+        !aligned16(bias) || !aligned16(y))
+        return fail(WOB_INVALID_ARG, "operand pointers must be 16-byte aligned");
+    const size_t need = wob::int8_gemm_workspace_bytes(M, N, K);
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+        return fail(WOB_INVALID_ARG, "workspace needs %zu bytes, 16-byte aligned (got %zu)", need,
+                    workspace_bytes);
+    int s = arch_gate();
+    if (s != WOB_OK)
+        return s;
+    const wob::Int8GemmArgs a{x_q, x_scale, w_q, w_scale, bias, y, y_dtype};
+    return launched(wob::launch_int8_gemm(a, (int)M, (int)N, (int)K, workspace,
+                                          static_cast<hipStream_t>(stream)),
+                    "int8 gemm");
+}
+
+int residual_norm(const void *y, int dtype, int64_t ldy, const void *residual, int residual_dtype,
+                  const void *post_weight, const void *gate, int64_t ldg, float alpha,
+                  const void *weight, float eps, int quant, void *n, void *n_scale,
+                  void *residual_out, int64_t T, int64_t H, void *stream)
+{
+    if (!value_dtype(dtype))
+        return fail(WOB_DTYPE, "dtype tag %d is not F16, BF16 or F32", dtype);
+    if (residual_dtype != dtype && residual_dtype != WOB_F32)
+        return fail(WOB_DTYPE, "residual dtype tag %d is neither the block's %d nor F32", residual_dtype,
+                    dtype);
+    if (quant != WOB_QUANT_NONE && quant != WOB_QUANT_INT8 && quant != WOB_QUANT_MXFP4)
+        return fail(WOB_INVALID_ARG, "unknown quant %d", quant);
+    const int64_t whole = quant == WOB_QUANT_MXFP4 ? 32 : quant == WOB_QUANT_INT8 ? 16 : 8;
+    if (T < 0 || H < 8 || H > 32768 || H % whole != 0)
+        return fail(WOB_INVALID_ARG, "bad shape T=%lld H=%lld (H: a multiple of %lld, up to 32768)",
+                    (long long)T, (long long)H, (long long)whole);
+    if (T > ELEMENTS / H)
+        return fail(WOB_INVALID_ARG, "shape too large");
+    if (!(eps >= 0.0f) || !isfinite(eps) || !isfinite(alpha))
+        return fail(WOB_INVALID_ARG, "eps must be finite and not negative, alpha finite");
+    if (!y && (post_weight || gate || !weight))
+        return fail(WOB_INVALID_ARG, "without y there is no post_weight and no gate, and weight is required");
+    if (!weight && (quant != WOB_QUANT_NONE || n || n_scale))
+        return fail(WOB_INVALID_ARG, "without weight there are no normed rows");
+    if (y && !row_stride(ldy, H, dtype))
+        return fail(WOB_INVALID_ARG, "row stride %lld of y is below H=%lld, too large or leaves rows unaligned",
+                    (long long)ldy, (long long)H);
+    if (gate && ldg != 0 && !row_stride(ldg, H, dtype))
+        return fail(WOB_INVALID_ARG, "row stride %lld of gate is neither 0 nor at least H=%lld and aligned",
+                    (long long)ldg, (long long)H);
+    if (T && ((y && ldy > ((int64_t)1 << 60) / T) || (gate && ldg > ((int64_t)1 << 60) / T)))
+        return fail(WOB_INVALID_ARG, "shape too large");
+    if (T == 0)
+        return ok();
+    if (!residual || (y && !residual_out) || (weight && !n) || (quant != WOB_QUANT_NONE && !n_scale))
+        return fail(WOB_INVALID_ARG, "null operand pointer");
+    if (quant == WOB_QUANT_NONE && n_scale)
+        return fail(WOB_INVALID_ARG, "n_scale without quantised rows");
+    if (!aligned16(y) || !aligned16(residual) || !aligned16(post_weight) || !aligned16(gate) ||
+        !aligned16(weight) || !aligned16(n) || !aligned16(n_scale) || !aligned16(residual_out))
+        return fail(WOB_INVALID_ARG, "operand pointers must be 16-byte aligned");
+    int s = arch_gate();
+    if (s != WOB_OK)
+        return s;
+    wob::NormArgs a;
+    a.y = y;
+    a.ldy = ldy;
+    a.residual = residual;
+    a.post = post_weight;
+    a.gate = gate;
+    a.ldg = ldg;
+    a.weight = weight;
+    a.n = n;
+    a.n_scale = n_scale;
+    a.residual_out = residual_out;
+    a.T = T;
+    a.H = (int)H;
+    a.quant = quant;
+    a.alpha = alpha;
+    a.eps = eps;
+    return launched(wob::launch_residual_norm(a, dtype, residual_dtype, static_cast<hipStream_t>(stream)),
+                    "residual norm");
+}
+
+int moe_route(const void *logits, int logits_dtype, const float *bias, int32_t *ids, float *weights,
+              int64_t T, int64_t E, int64_t topk, int score, int64_t groups, int64_t topk_groups,
+              int group_top, int renormalize, float scale, void *stream)
+{
+    if (!value_dtype(logits_dtype))
+        return fail(WOB_DTYPE, "logits dtype tag %d is not F16, BF16 or F32", logits_dtype);
+    if (score != WOB_SCORE_SIGMOID && score != WOB_SCORE_SOFTMAX)
+        return fail(WOB_INVALID_ARG, "unknown score %d", score);
+    if (T < 0 || E < 1 || E > 1024 || topk < 1 || topk > 64 || T > INT_MAX / 64)
+        return fail(WOB_INVALID_ARG, "bad shape T=%lld E=%lld topk=%lld", (long long)T, (long long)E,
+                    (long long)topk);
+    if (groups < 1 || groups > 64 || E % groups != 0 || topk_groups < 1 || topk_groups > groups ||
+        topk > topk_groups * (E / groups))
+        return fail(WOB_INVALID_ARG, "bad groups: %lld of %lld kept, E=%lld topk=%lld",
+                    (long long)topk_groups, (long long)groups, (long long)E, (long long)topk);
+    if (group_top != 1 && group_top != 2)
+        return fail(WOB_INVALID_ARG, "group_top %d is not 1 or 2", group_top);
+    if (!isfinite(scale))
+        return fail(WOB_INVALID_ARG, "scale must be finite");
+    if (T == 0)
+        return ok();
+    if (!logits || !ids || !weights)
+        return fail(WOB_INVALID_ARG, "null operand pointer");
+    if (!aligned16(logits) || !aligned16(ids) || !aligned16(weights) || !aligned16(bias))
+        return fail(WOB_INVALID_ARG, "operand pointers must be 16-byte aligned");
+    int s = arch_gate();
+    if (s != WOB_OK)
+        return s;
+    wob::RouteArgs a;
+    a.logits = logits;
+    a.bias = bias;
+    a.ids = ids;
+    a.weights = weights;
+    a.scale = scale;
+    a.dt = logits_dtype;
+    a.T = (int)T;
+    a.E = (int)E;
+    a.topk = (int)topk;
+    a.score = score;
+    a.groups = (int)groups;
+    a.topk_groups = (int)topk_groups;
+    a.group_top = group_top;
+    a.renormalize = renormalize != 0;
+    return launched(wob::launch_moe_route(a, static_cast<hipStream_t>(stream)), "moe route");
 }
 
 int w4a16_dequant(const int32_t *qweight, const void *scales, int scales_dtype,

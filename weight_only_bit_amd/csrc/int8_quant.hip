@@ -1,0 +1,147 @@
+// Rows in 8 bits on gfx950: one binary32 scale a row, codes half to even.
+//
+//     v_k   = x_k, or silu(x_k) * x_{K + k} (the gate and up halves of a row of 2 K)
+//     scale = max |v| / 127,   code_k = round(v_k * (127 / max |v|))
+//
+// and the codes read back as values.  Bound by memory: x is read once, the row stays in
+// registers between its maximum and its codes.
+#include "weight_only_bit.h"
+#include "wob_rows.hpp"
+
+#include <algorithm>
+
+namespace wob {
+
+namespace {
+
+// silu(g) * u; exp overflows to infinity for large negative g, where the quotient is -0.
+__device__ __forceinline__ float silu_mul(float g, float u)
+{
+    return g / (1.0f + __expf(-g)) * u;
+}
+
+// NT threads share a row, V pieces of eight elements a thread: piece j of thread t is j NT + t.
+template <int DT, bool ACT, int NT, int V>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void int8_quantize_kernel(
+    const void *__restrict__ x, int64_t ldx, uint2 *__restrict__ codes, float *__restrict__ scale,
+    int64_t R, int K)
+{
+    constexpr int ROWS = NT < 256 ? 256 / NT : 1, ES = elem_size<DT>();
+    __shared__ uint32_t part[2][NT / 64];
+    const int t = threadIdx.x % NT, pieces = K / RV;
+    int turn = 0;
+    for (int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / NT; r < R; r += (int64_t)gridDim.x * ROWS) {
+        const uint8_t *row = static_cast<const uint8_t *>(x) + r * ldx * ES;
+        float v[V][RV];
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int p = j * NT + t;
+            if (p < pieces) {
+                load8<DT>(row + (int64_t)p * RV * ES, v[j]);
+                if constexpr (ACT) {
+                    float up[RV];
+                    load8<DT>(row + ((int64_t)K + p * RV) * ES, up);
+#pragma unroll
+                    for (int i = 0; i < RV; ++i)
+                        v[j][i] = silu_mul(v[j][i], up[i]);
+                }
+                top = max(top, magnitude8(v[j]));
+            }
+        }
+        const Int8Row s = int8_row(row_max<NT>(top, part[turn]));
+        turn ^= 1; // the next row's maxima may be written while this one's are read
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int p = j * NT + t;
+            if (p < pieces)
+                codes[r * pieces + p] = int8_codes8(v[j], s);
+        }
+        if (t == 0)
+            scale[r] = s.scale;
+    }
+}
+
+template <int DT, bool ACT, int NT, int V>
+hipError_t launch_rows(const void *x, int64_t ldx, int8_t *codes, float *scale, int64_t R, int K,
+                       hipStream_t stream)
+{
+    constexpr int ROWS = NT < 256 ? 256 / NT : 1;
+    const int64_t grid = std::min<int64_t>((R + ROWS - 1) / ROWS, (int64_t)1 << 20);
+    hipLaunchKernelGGL((int8_quantize_kernel<DT, ACT, NT, V>), dim3((unsigned)grid), dim3(NT * ROWS), 0,
+                       stream, x, ldx, reinterpret_cast<uint2 *>(codes), scale, R, K);
+    return hipGetLastError();
+}
+
+template <int DT, bool ACT>
+hipError_t launch(const void *x, int64_t ldx, int8_t *codes, float *scale, int64_t R, int K,
+                  hipStream_t stream)
+{
+    if (K <= 512)
+        return launch_rows<DT, ACT, 64, 1>(x, ldx, codes, scale, R, K, stream);
+    if (K <= 2048)
+        return launch_rows<DT, ACT, 256, 1>(x, ldx, codes, scale, R, K, stream);
+    if (K <= 8192)
+        return launch_rows<DT, ACT, 256, 4>(x, ldx, codes, scale, R, K, stream);
+    if (K <= 32768)
+        return launch_rows<DT, ACT, 1024, 4>(x, ldx, codes, scale, R, K, stream);
+    return launch_rows<DT, ACT, 1024, 8>(x, ldx, codes, scale, R, K, stream);
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void int8_dequant_kernel(const uint2 *__restrict__ codes,
+                                                           const float *__restrict__ scale,
+                                                           void *__restrict__ out, int64_t R, int pieces)
+{
+    const int64_t n = R * pieces;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const uint2 c = codes[i];
+        const float s = scale[i / pieces];
+        float v[RV];
+#pragma unroll
+        for (int e = 0; e < RV; ++e)
+            v[e] = (float)(int8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3))) * s;
+        store8<DT>(static_cast<uint8_t *>(out) + i * RV * elem_size<DT>(), v);
+    }
+}
+
+template <int DT>
+hipError_t launch_dequant(const int8_t *codes, const float *scale, void *out, int64_t R, int K,
+                          hipStream_t stream)
+{
+    const int64_t blocks = (R * (K / RV) + 255) / 256;
+    hipLaunchKernelGGL(int8_dequant_kernel<DT>, dim3((unsigned)std::min<int64_t>(blocks, 1 << 20)),
+                       dim3(256), 0, stream, reinterpret_cast<const uint2 *>(codes), scale, out, R, K / RV);
+    return hipGetLastError();
+}
+
+} // namespace
+
+hipError_t launch_int8_quantize(const void *x, int dt, int64_t ldx, int act, int8_t *codes,
+                                float *scale, int64_t R, int K, hipStream_t stream)
+{
+    if (act == WOB_ACT_SILU_MUL) {
+        if (dt == DT_F16)
+            return launch<DT_F16, true>(x, ldx, codes, scale, R, K, stream);
+        if (dt == DT_BF16)
+            return launch<DT_BF16, true>(x, ldx, codes, scale, R, K, stream);
+        return launch<DT_F32, true>(x, ldx, codes, scale, R, K, stream);
+    }
+    if (dt == DT_F16)
+        return launch<DT_F16, false>(x, ldx, codes, scale, R, K, stream);
+    if (dt == DT_BF16)
+        return launch<DT_BF16, false>(x, ldx, codes, scale, R, K, stream);
+    return launch<DT_F32, false>(x, ldx, codes, scale, R, K, stream);
+}
+
+hipError_t launch_int8_dequant(const int8_t *codes, const float *scale, void *out, int dt, int64_t R,
+                               int K, hipStream_t stream)
+{
+    if (dt == DT_F16)
+        return launch_dequant<DT_F16>(codes, scale, out, R, K, stream);
+    if (dt == DT_BF16)
+        return launch_dequant<DT_BF16>(codes, scale, out, R, K, stream);
+    return launch_dequant<DT_F32>(codes, scale, out, R, K, stream);
+}
+
+} // namespace wob

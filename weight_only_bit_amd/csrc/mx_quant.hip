@@ -11,15 +11,14 @@
 //
 // floor(log2 amax) is the exponent field of amax as binary32 (a binary32
 // subnormal has field 0 and meets the clamp), so no logarithm is taken.
-#include "wob_device.hpp"
-#include "wob_internal.hpp"
+#include "wob_rows.hpp"
 
 namespace wob {
 
 namespace {
 
 constexpr int QT = 256; // threads per workgroup
-constexpr int QE = 8;   // elements per thread: a quarter of a block
+constexpr int QE = RV;  // elements per thread: a quarter of a block
 
 // n / d for n < 2^31: (n * m) >> (31 + l), l = ceil(log2 d), m = ceil(2^(31+l) / d) < 2^32.
 struct FastDiv {
@@ -38,35 +37,6 @@ struct FastDiv {
         return (uint32_t)(((uint64_t)n * m) >> s);
     }
 };
-
-// Eight consecutive elements in binary32 (exact for every input type).
-template <int DT>
-__device__ __forceinline__ void load8(const void *p, float (&v)[QE])
-{
-    if constexpr (DT == DT_F32) {
-        const float4_t *s = static_cast<const float4_t *>(p);
-        const float4_t a = s[0], b = s[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-    } else {
-        const u32x4 a = *static_cast<const u32x4 *>(p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = act_to_f32<DT>((uint16_t)(a[i] & 0xFFFFu));
-            v[2 * i + 1] = act_to_f32<DT>((uint16_t)(a[i] >> 16));
-        }
-    }
-}
-
-// Maximum over the four lanes of a quad.
-__device__ __forceinline__ uint32_t quad_max(uint32_t v)
-{
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true)); // 1,0,3,2
-    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true)); // 2,3,0,1
-}
 
 // Thread u takes elements 8 u .. 8 u + 7 of the rows laid end to end; a quad
 // of lanes shares a block (K % 32 == 0, so no block crosses a row, and the
@@ -93,20 +63,8 @@ __global__ __launch_bounds__(QT) void mxfp4_quantize_kernel(const void *__restri
     constexpr int ES = DT == DT_F32 ? 4 : 2;
     float v[QE];
     load8<DT>(static_cast<const uint8_t *>(x) + at * ES, v);
-    uint32_t top = 0; // magnitudes order as their bit patterns do, NaN above infinity
-#pragma unroll
-    for (int i = 0; i < QE; ++i)
-        top = max(top, bitcast<uint32_t>(v[i]) & 0x7FFFFFFFu);
-    top = quad_max(top);
-    const uint32_t field = top >> 23;
-    const uint32_t b = field == 255u ? 255u : (field > 2u ? field - 2u : 0u);
-    const float s = e8m0_to_f32(b == 255u ? 127u : b);
-    uint32_t c = 0;
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], s, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], s, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], s, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], s, 3);
-    codes[u] = b == 255u ? 0u : c;
+    uint32_t b;
+    codes[u] = mxfp4_codes8(v, b);
     if ((threadIdx.x & 3) == 0)
         scale[u >> 2] = (uint8_t)b;
 }

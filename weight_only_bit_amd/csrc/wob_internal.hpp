@@ -104,6 +104,52 @@ hipError_t launch_mxfp4_gemm(const uint8_t *x, const uint8_t *xs, const uint8_t 
                              const uint8_t *ws, void *y, int ydt, int M, int N, int K,
                              void *workspace, hipStream_t stream);
 
+// Rows in 8 bits: one scale a row; act: WOB_ACT_NONE, or WOB_ACT_SILU_MUL on rows of 2 K.
+hipError_t launch_int8_quantize(const void *x, int dt, int64_t ldx, int act, int8_t *codes,
+                                float *scale, int64_t R, int K, hipStream_t stream);
+hipError_t launch_int8_dequant(const int8_t *codes, const float *scale, void *out, int dt, int64_t R,
+                               int K, hipStream_t stream);
+
+// 8-bit product.
+struct Int8GemmArgs {
+    const int8_t *x;
+    const float *xs;
+    const int8_t *w;
+    const float *ws;
+    const float *bias; // nullptr: none
+    void *y;
+    int ydt; // DT_F16 / DT_BF16 / DT_F32
+};
+size_t int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_int8_gemm(const Int8GemmArgs &a, int M, int N, int K, void *workspace,
+                            hipStream_t stream);
+
+// The norms around a block.
+struct NormArgs {
+    const void *y; // nullptr: no block, h is the residual
+    int64_t ldy;
+    const void *residual;
+    const void *post, *gate; // nullptr: none
+    int64_t ldg;             // 0: one gate for all rows
+    const void *weight;      // nullptr: no norm before the next block
+    void *n, *n_scale, *residual_out;
+    int64_t T;
+    int H, quant;
+    float alpha, eps;
+};
+hipError_t launch_residual_norm(const NormArgs &a, int dt, int residual_dt, hipStream_t stream);
+
+// Group-limited choice of experts.
+struct RouteArgs {
+    const void *logits;
+    const float *bias; // nullptr: none
+    int32_t *ids;
+    float *weights;
+    float scale;
+    int dt, T, E, topk, score, groups, topk_groups, group_top, renormalize;
+};
+hipError_t launch_moe_route(const RouteArgs &a, hipStream_t stream);
+
 // Dequantization probes.
 hipError_t launch_w4a16_dequant(const uint32_t *qweight, const void *scales, const uint32_t *qzeros,
                                 void *out, int dt, bool out_f32, int N, int K, int g,

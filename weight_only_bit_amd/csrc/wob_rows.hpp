@@ -1,0 +1,156 @@
+// Rows shared by the threads of a workgroup: loads, reductions and the 8- and 4-bit
+// forms that the quantising kernels write.
+#pragma once
+
+#include "wob_device.hpp"
+#include "wob_internal.hpp"
+
+namespace wob {
+
+constexpr int RV = 8; // consecutive elements of a thread: 16 bytes of 16-bit values
+
+// Eight consecutive elements in binary32 (exact for every input type).
+template <int DT>
+__device__ __forceinline__ void load8(const void *p, float (&v)[RV])
+{
+    if constexpr (DT == DT_F32) {
+        const float4_t *s = static_cast<const float4_t *>(p);
+        const float4_t a = s[0], b = s[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+    } else {
+        const u32x4 a = *static_cast<const u32x4 *>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = act_to_f32<DT>((uint16_t)(a[i] & 0xFFFFu));
+            v[2 * i + 1] = act_to_f32<DT>((uint16_t)(a[i] >> 16));
+        }
+    }
+}
+
+// Eight consecutive elements, each rounded once to the type.
+template <int DT>
+__device__ __forceinline__ void store8(void *p, const float (&v)[RV])
+{
+    if constexpr (DT == DT_F32) {
+        float4_t *d = static_cast<float4_t *>(p);
+        d[0] = float4_t{v[0], v[1], v[2], v[3]};
+        d[1] = float4_t{v[4], v[5], v[6], v[7]};
+    } else {
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = f32x2_to_act2<DT>(v[2 * i], v[2 * i + 1]);
+        *static_cast<u32x4 *>(p) = o;
+    }
+}
+
+template <int DT>
+constexpr int elem_size() { return DT == DT_F32 ? 4 : 2; }
+
+// Maximum over the four lanes of a quad.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v)
+{
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true)); // 1,0,3,2
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true)); // 2,3,0,1
+}
+
+// f over the NT threads that share a row, the result in every one of them.  NT = 64: a
+// wave; more: the waves' results meet in `part` (NT / 64 words of LDS that nothing else
+// is read from until the next barrier).
+template <int NT, class F>
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, uint32_t *part, F f)
+{
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));  // lane ^ 1
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));  // lane ^ 2
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true)); // 7 - lane of 8
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true)); // 15 - lane of 16
+    v = f(v, (uint32_t)__shfl_xor((int)v, 16));
+    v = f(v, (uint32_t)__shfl_xor((int)v, 32));
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0)
+            part[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = part[0];
+#pragma unroll
+        for (int i = 1; i < NT / 64; ++i)
+            v = f(v, part[i]);
+    }
+    return v;
+}
+
+template <int NT>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *part)
+{
+    return row_reduce<NT>(v, part, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+
+template <int NT>
+__device__ __forceinline__ float row_sum(float v, uint32_t *part)
+{
+    return bitcast<float>(row_reduce<NT>(bitcast<uint32_t>(v), part, [](uint32_t a, uint32_t b) {
+        return bitcast<uint32_t>(bitcast<float>(a) + bitcast<float>(b));
+    }));
+}
+
+// The largest magnitude as a bit pattern (magnitudes order as their patterns do, NaN
+// above infinity).
+__device__ __forceinline__ uint32_t magnitude8(const float (&v)[RV])
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < RV; ++i)
+        top = max(top, bitcast<uint32_t>(v[i]) & 0x7FFFFFFFu);
+    return top;
+}
+
+// A row in 8 bits: scale = amax / 127, code = round(v * (127 / amax)), half to even.  Rows
+// with a NaN or an infinity get a NaN scale and codes 0, rows of zeros scale 0 and codes 0.
+// v * (127 / amax) is at most 127 (1 + 2^-23), so no code passes 127.  127 / amax would pass
+// binary32's range below 2^-121: such rows are taken 2^64 times as large, which is exact.
+struct Int8Row {
+    float scale, lift, inv;
+};
+
+__device__ __forceinline__ Int8Row int8_row(uint32_t top)
+{
+    const float amax = bitcast<float>(top);
+    Int8Row r;
+    r.lift = amax < 0x1p-100f ? 0x1p64f : 1.0f;
+    const bool finite = top < 0x7F800000u;
+    r.scale = finite ? amax / 127.0f : bitcast<float>(0x7FC00000u);
+    r.inv = finite && top != 0u ? 127.0f / (amax * r.lift) : 0.0f;
+    return r;
+}
+
+// Eight codes; a row that is not finite is given as zeros (0 * inf is no code).
+__device__ __forceinline__ uint2 int8_codes8(const float (&v)[RV], const Int8Row &r)
+{
+    uint32_t o[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < RV; ++i) {
+        const int q = r.inv == 0.0f ? 0 : (int)__builtin_rintf(v[i] * r.lift * r.inv);
+        o[i / 4] |= ((uint32_t)q & 0xFFu) << (8 * (i & 3));
+    }
+    return uint2{o[0], o[1]};
+}
+
+// A quarter of an MXFP4 block: the eight codes of this lane and the block's E8M0 byte (see
+// mx_quant.hip).  The four lanes of a quad hold the block and call together.
+__device__ __forceinline__ uint32_t mxfp4_codes8(const float (&v)[RV], uint32_t &b)
+{
+    const uint32_t field = quad_max(magnitude8(v)) >> 23;
+    b = field == 255u ? 255u : (field > 2u ? field - 2u : 0u);
+    const float s = e8m0_to_f32(b == 255u ? 127u : b);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], s, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], s, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], s, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], s, 3);
+    return b == 255u ? 0u : c;
+}
+
+} // namespace wob
