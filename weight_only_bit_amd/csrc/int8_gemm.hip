@@ -1,10 +1,22 @@
 // 8-bit product on gfx950:
 //     y[m][n] = x_scale[m] * w_scale[n] * sum_k x[m][k] * w[n][k]  (+ bias[n])
 //
-// The sums are exact in 32 bits (K 2^14 < 2^31); they are converted to binary32, scaled
-// twice, added to the bias and rounded once to y's type.  A holds weight rows and B
-// activation rows, so a lane ends with runs of four consecutive n of one output row.
+// The sums are exact in 32 bits (K 2^14 < 2^31), so their order and their split do not
+// show in the result; they are converted to binary32, scaled twice, added to the bias
+// and rounded once to y's type.  A holds weight rows and B activation rows, so a lane ends
+// with runs of four consecutive n of one output row.  Which 16 k of a row meet in one
+// instruction is free as long as both operands agree.
+//
+// Two kernels:
+//  * few rows (M <= 16): waves own 16 weight rows each and may split K; the weights go
+//    from memory straight into registers (v_mfma_i32_16x16x64_i8); bound by their bytes.
+//  * tiles: both operands through LDS (v_mfma_i32_32x32x32_i8), K optionally split over
+//    workgroups with a sum in a second kernel.
 #include "wob_rows.hpp"
+#include "wob_tile.hpp"
+
+#include <algorithm>
+#include <type_traits>
 
 namespace wob {
 
@@ -26,62 +38,537 @@ __device__ __forceinline__ void store4(void *y, int ydt, size_t at, const float4
             uint2{f32x2_to_act2<DT_BF16>(v[0], v[1]), f32x2_to_act2<DT_BF16>(v[2], v[3])};
 }
 
-// Four sums of row m (scale xs), columns n .. n + 3, scaled.
-__device__ __forceinline__ float4_t scaled4(const i32x4 &sum, float xs, const float *ws, const float *bias, int n)
+// Four sums of one row, scaled: binary32 steps in the order that the contract names.
+__device__ __forceinline__ float4_t scaled4(const i32x4 &sum, float xs, const float4_t &ws, const float4_t &bias,
+                                            bool biased)
 {
-    const float4_t w = *reinterpret_cast<const float4_t *>(ws + n);
     float4_t v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        v[e] = (float)sum[e] * xs * w[e];
-    if (bias)
-        v += *reinterpret_cast<const float4_t *>(bias + n);
+    for (int e = 0; e < 4; ++e) {
+        v[e] = (float)sum[e] * xs * ws[e];
+        v[e] = biased ? v[e] + bias[e] : v[e];
+    }
     return v;
 }
 
-// A workgroup of 2 x 2 waves owns 64 weight rows x 64 activation rows, a wave a block of
-// 32 x 32; operands straight from memory.
-__global__ __launch_bounds__(256) void int8_simple_kernel(const int8_t *__restrict__ x,
-                                                          const float *__restrict__ xs,
-                                                          const int8_t *__restrict__ w,
-                                                          const float *__restrict__ ws,
-                                                          const float *__restrict__ bias,
-                                                          void *__restrict__ y, int ydt, int M, int N, int K)
+// ---- Few rows --------------------------------------------------------------
+//
+// M <= 16.  A wave owns 16 weight rows; W waves share them and split K, in pairs of steps
+// of 64 k (in a step lane (r, q) = (lane % 16, lane / 16) holds the 16 k of block 4 j + q of
+// row r, so a pair is one whole cache line of each row), and their sums are joined in
+// LDS.  A workgroup has G such groups of rows.  The weights go from memory into registers,
+// FR_D loads of a lane ahead; only x passes through LDS (pitch 16 mod 128 bytes, which makes
+// its reads conflict-free), with its loads ahead of the weights' so that they land first.
+constexpr int FR_ROWS = 16;
+constexpr int FR_D = 6;  // loads ahead
+constexpr int FR_CH = 2; // neighbouring steps of a wave
+
+__host__ __device__ inline int few_pitch(int K) { return (K + 127 - 16) / 128 * 128 + 16; }
+inline size_t few_lds(int M, int K, int W, int G)
 {
-    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5, wave = threadIdx.x >> 6;
-    const int tiles_n = (N + 63) / 64, n0 = blockIdx.x % tiles_n * 64 + (wave & 1) * 32;
-    const int m0 = blockIdx.x / tiles_n * 64 + (wave >> 1) * 32;
-    const int8_t *wr = w + (size_t)min(n0 + r, N - 1) * K, *xr = x + (size_t)min(m0 + r, M - 1) * K;
-    i32x16 acc = {};
-    for (int k = 16 * h; k < K + 16 * h; k += 32) {
-        i32x4 a = {}, b = {};
-        if (k < K) { // the last step may be half a step
-            a = *reinterpret_cast<const i32x4 *>(wr + k);
-            b = *reinterpret_cast<const i32x4 *>(xr + k);
-        }
-        acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc, 0, 0, 0);
-    }
-    const int m = m0 + r;
-    if (m >= M)
-        return;
+    const size_t sums = W > 1 ? (size_t)W * G * 1024 : 0;
+    return std::max((size_t)M * few_pitch(K), sums);
+}
+
+template <int W, int G>
+__global__ __launch_bounds__(64 * W * G) void int8_few_kernel(Int8GemmArgs a, int M, int N, int K)
+{
+    constexpr int NT = 64 * W * G;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), k = wave % W, g = wave / W;
+    const int KB = K >> 4, steps = (KB + 3) >> 2, pitch = few_pitch(K);
+    const int n0 = (blockIdx.x * G + g) * FR_ROWS;
+
+    // Staging of x, 16 bytes a thread, the first round's loads ahead of the weights'.
+    const int nx = M * KB;
+    const u32x4 *xg = reinterpret_cast<const u32x4 *>(a.x);
+    const u32x4 x_first = xg[min(tid, nx - 1)];
+
+    const u32x4 *wr = reinterpret_cast<const u32x4 *>(a.w) + (size_t)min(n0 + r, N - 1) * KB;
+    const int mine = FR_CH * (((steps + FR_CH - 1) / FR_CH - k + W - 1) / W); // steps of this wave
+    auto block = [&](int i) __attribute__((always_inline)) { // this lane's in step i
+        return 4 * (FR_CH * (k + W * (i / FR_CH)) + i % FR_CH) + q;
+    };
+    u32x4 ring[FR_D];
+    auto load = [&](int i, u32x4 &s) __attribute__((always_inline)) {
+        int b = min(block(i), KB - 1);
+        asm volatile("" : "+v"(b)); // one address per load, not one pointer kept per slot
+        s = wr[b];
+    };
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int n = n0 + 8 * g + 4 * h;
-        if (n < N)
-            store4(y, ydt, (size_t)m * N + n,
-                   scaled4(i32x4{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]}, xs[m], ws, bias, n));
+    for (int d = 0; d < FR_D; ++d)
+        load(min(d, max(mine - 1, 0)), ring[d]);
+    __builtin_amdgcn_sched_barrier(0);
+
+    auto put_x = [&](int i, const u32x4 &v) __attribute__((always_inline)) {
+        const int m = M == 1 ? 0 : i / KB;
+        *reinterpret_cast<u32x4 *>(smem + (size_t)m * pitch + (size_t)(i - m * KB) * 16) = v;
+    };
+    if (tid < nx)
+        put_x(tid, x_first);
+    for (int i = tid + NT; i < nx; i += NT)
+        put_x(i, xg[i]);
+    __syncthreads();
+
+    const uint8_t *xrow = smem + (size_t)min(r, M - 1) * pitch;
+    i32x4 acc = {0, 0, 0, 0};
+    auto multiply = [&](int i, u32x4 wv) __attribute__((always_inline)) {
+        const int b = block(i);
+        const bool in = b < KB; // the last steps may leave some lanes without a block
+        const u32x4 xv = *reinterpret_cast<const u32x4 *>(xrow + 16 * min(b, KB - 1));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            wv[e] = in ? wv[e] : 0u;
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(bitcast<i32x4>(wv), bitcast<i32x4>(xv), acc, 0, 0, 0);
+    };
+    int i = 0;
+    for (; i + FR_D < mine; i += FR_D) {
+#pragma unroll
+        for (int d = 0; d < FR_D; ++d) {
+            if (i + d < mine)
+                multiply(i + d, ring[d]);
+            __builtin_amdgcn_sched_barrier(0);
+            load(min(i + d + FR_D, mine - 1), ring[d]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
+#pragma unroll
+    for (int d = 0; d < FR_D; ++d)
+        if (i + d < mine)
+            multiply(i + d, ring[d]);
+    // Lane (r, q) holds n = 4 q + e of output row r in acc[e]; the waves of a
+    // group are summed in order.
+    if constexpr (W > 1) {
+        __syncthreads();
+        i32x4 *part = reinterpret_cast<i32x4 *>(smem);
+        part[wave * 64 + lane] = acc;
+        __syncthreads();
+        if (k != 0)
+            return;
+#pragma unroll
+        for (int j = 1; j < W; ++j)
+            acc += part[(wave + j) * 64 + lane];
+    }
+    const int n = n0 + 4 * q;
+    if (r < M && n < N) {
+        float4_t bias = {};
+        if (a.bias)
+            bias = *reinterpret_cast<const float4_t *>(a.bias + n);
+        store4(a.y, a.ydt, (size_t)r * N + n,
+               scaled4(acc, a.xs[r], *reinterpret_cast<const float4_t *>(a.ws + n), bias, a.bias != nullptr));
+    }
+}
+
+template <int W, int G>
+hipError_t launch_few(const Int8GemmArgs &a, int M, int N, int K, hipStream_t stream)
+{
+    auto kern = int8_few_kernel<W, G>;
+    static std::atomic<uint64_t> lds_set{0};
+    if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), 160 * 1024, lds_set);
+        e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(kern, dim3((N + FR_ROWS * G - 1) / (FR_ROWS * G)), dim3(64 * W * G),
+                       few_lds(M, K, W, G), stream, a, M, N, K);
+    return hipGetLastError();
+}
+
+// ---- Tiles -----------------------------------------------------------------
+//
+// A workgroup of 4 waves (WN along n, 4 / WN along m) owns TN weight rows x TM activation
+// rows; a wave owns NB x MB blocks of 32 x 32 outputs.  K advances in stages of 64 (64
+// bytes a row).  GS of them form a group, which is copied as one piece of 64 GS bytes a
+// row; NG groups are in LDS at a time, copied by global_load_lds (1 KB a wave
+// instruction), NG - 1 groups ahead of their use.
+//
+// A stage is two MFMA steps of 32 k: in step j the lane half h = lane / 32 supplies the 16
+// bytes of piece 2 h + j of its row.  LDS row R (weight rows, then activation rows) holds
+// 64 GS bytes of a group; its 16-byte piece p lies at position p ^ swizzle(R), so the rows
+// that one piece is read from at a time cover all 64 banks.
+//
+// Order within a group: its steps but the last read the next step's operands and multiply;
+// then group g + 1's copies are waited for, a barrier makes them visible and frees group g's
+// place (every wave has its last operands in registers), and the last step reads group
+// g + 1's first operands and starts the copies of group g + NG while it multiplies.
+template <int WN_, int NB_, int MB_, int GS_, int NG_>
+struct Int8Tile {
+    static constexpr int WN = WN_, WM = 4 / WN_, NB = NB_, MB = MB_, GS = GS_, NG = NG_;
+    static constexpr int TN = 32 * NB * WN, TM = 32 * MB * WM, ROWS = TN + TM;
+    static constexpr int SEG = 64 * GS;                  // bytes of a row in a group
+    static constexpr int GROUP = ROWS * SEG;             // bytes of one group
+    static constexpr int ND = GROUP / 4096;              // copies per wave and group
+    static constexpr int SCALES = 4 * (2 * TN + TM);     // scales and bias of the tile, in the epilogue
+    static constexpr int WSTAGE = 32 * (128 * NB + 16);  // LDS of one wave in the epilogue
+    static constexpr int LDS = std::max(NG * GROUP, SCALES + 4 * WSTAGE);
+    static_assert(ROWS % 64 == 0 && (GS == 1 || GS == 2) && NG >= 2 && LDS <= 160 * 1024, "tile geometry");
+};
+
+// A wave's outputs (n from nw, m from mw) through its part of LDS, 32 output rows at a
+// time: rows of 32 NB n are written as the accumulators hold them (acc[i][k][4 g + e] is n =
+// 32 i + 8 g + 4 h + e, m = 32 k + r) and read back 16 bytes a lane, so a store covers
+// whole runs of a row.  The LDS serves a wave's accesses in order, and no other wave uses
+// this part.  RAW: the sums themselves, as one of the K parts.
+template <class T, int DT, bool RAW>
+__device__ __forceinline__ void store_wave(const i32x16 (&acc)[T::NB][T::MB], void *y, bool biased, int M, int N,
+                                           int nw, int mw, const float *ws, const float *bias, const float *xs,
+                                           uint8_t *stage)
+{
+    constexpr int ES = DT == DT_F32 ? 4 : 2, ROW = 32 * T::NB * ES, PITCH = ROW + 16;
+    constexpr int VECS = ROW / 16, RPI = 64 / VECS; // 16-byte pieces of a row; rows per instruction
+    static_assert(32 * PITCH <= T::WSTAGE && 64 % VECS == 0, "staging space");
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    const int n = nw + lane % VECS * (16 / ES);
+#pragma unroll
+    for (int k = 0; k < T::MB; ++k) {
+        const float x = RAW ? 0.f : xs[32 * k + r];
+#pragma unroll
+        for (int i = 0; i < T::NB; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const i32x4 sum{acc[i][k][4 * g], acc[i][k][4 * g + 1], acc[i][k][4 * g + 2], acc[i][k][4 * g + 3]};
+                const int at = 32 * i + 8 * g + 4 * h;
+                uint8_t *to = stage + r * PITCH + at * ES;
+                if constexpr (RAW) {
+                    *reinterpret_cast<i32x4 *>(to) = sum;
+                } else {
+                    const float4_t v = scaled4(sum, x, *reinterpret_cast<const float4_t *>(ws + at),
+                                               *reinterpret_cast<const float4_t *>(bias + at), biased);
+                    if constexpr (DT == DT_F32)
+                        *reinterpret_cast<float4_t *>(to) = v;
+                    else
+                        *reinterpret_cast<uint2 *>(to) =
+                            uint2{f32x2_to_act2<DT>(v[0], v[1]), f32x2_to_act2<DT>(v[2], v[3])};
+                }
+            }
+#pragma unroll
+        for (int q = 0; q < 32 / RPI; ++q) {
+            const int row = q * RPI + lane / VECS, m = mw + 32 * k + row;
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(stage + row * PITCH + lane % VECS * 16);
+            if (m < M && n < N) // N % 8 == 0: a piece is whole
+                *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(y) + ((size_t)m * N + n) * ES) = v;
+        }
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__restrict__ part, int M, int N, int K,
+                                                        int tiles_m, int tiles, int splits, int nxcd)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int id = xcd_tile(tiles * splits, nxcd);
+    if (id < 0)
+        return;
+    // activation tiles fastest, then weight tiles, then K parts
+    const int split = id / tiles, tile = id - split * tiles;
+    const int n0 = tile / tiles_m * T::TN, m0 = tile % tiles_m * T::TM;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave % T::WN, wm = wave / T::WN;
+    constexpr int GS = T::GS, NG = T::NG, STEPS = 2 * GS, ND = T::ND;
+    const int row_groups = (K + T::SEG - 1) / T::SEG;
+    const int g_begin = (int)((int64_t)row_groups * split / splits);
+    const int g_end = (int)((int64_t)row_groups * (split + 1) / splits); // > g_begin: splits <= row_groups
+    const int groups = g_end - g_begin;
+    const uint32_t rowb = (uint32_t)K;
+    constexpr auto part_of = [](int w) { return w * ND / STEPS; }; // copies before part w of a group's STEPS
+
+    // Copy d of wave v fills LDS rows RI (4 d + v) .. + RI - 1: lane L the position L % LR of
+    // row L / LR.  Rows past the matrix repeat its last row (never stored), pieces past the
+    // row its last piece (zeroed before use).
+    constexpr int LR = 4 * GS, RI = 64 / LR; // lanes of a row, rows of a copy
+    uint32_t row_at[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+        const int R = RI * (4 * d + wave) + lane / LR;
+        row_at[d] = (uint32_t)(4 * RI * d < T::TN ? min(n0 + R, N - 1) : min(m0 + R - T::TN, M - 1)) * rowb;
+    }
+    static_assert(T::TN % (4 * RI) == 0, "a copy has rows of one operand");
+    // position of a row's piece: piece ^ swizzle(row)
+    auto swizzle = [](int R) __attribute__((always_inline)) { return GS == 1 ? (R >> 2) & 3 : (R >> 1) & 7; };
+    const uint32_t piece = 16u * (uint32_t)(lane % LR ^ swizzle(RI * wave + lane / LR));
+    const uint32_t lds0 = (uint32_t)(size_t)(lds_ptr_t *)smem;
+    auto copy = [&](int g, int b, int d) __attribute__((always_inline)) { // group g into buffer b
+        const int from = g_begin + min(g, groups - 1); // past the end: the last group again
+        const uint32_t k = min((uint32_t)from * (uint32_t)T::SEG + piece, rowb - 16u);
+        const uint32_t to = lds0 + (uint32_t)(b * T::GROUP + wave * 1024);
+        lds_dma16(4 * RI * d < T::TN ? a.w : a.x, row_at[d] + k, to + (uint32_t)(4096 * d));
+    };
+
+    i32x16 acc[T::NB][T::MB] = {};
+
+    const int an = 32 * T::NB * wn + r, bm = T::TN + 32 * T::MB * wm + r; // this lane's first LDS rows
+    uint32_t at[GS][2]; // position of piece 4 p + 2 h + j in a row of this lane
+#pragma unroll
+    for (int p = 0; p < GS; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            at[p][j] = 16u * (uint32_t)((4 * p + 2 * h + j) ^ swizzle(r));
+
+    struct Operands {
+        i32x4 a[T::NB], b[T::MB];
+    };
+    constexpr int NR = T::NB + T::MB, NM = T::NB * T::MB;
+    // operand i (weight blocks, then activation blocks) of step s of the group in buffer b
+    auto read_operand = [&](int b, int s, int i, Operands &o) __attribute__((always_inline)) {
+        const uint8_t *base = smem + b * T::GROUP + at[s >> 1][s & 1];
+        if (i < T::NB)
+            o.a[i] = *reinterpret_cast<const i32x4 *>(base + (an + 32 * i) * T::SEG);
+        else
+            o.b[i - T::NB] = *reinterpret_cast<const i32x4 *>(base + (bm + 32 * (i - T::NB)) * T::SEG);
+    };
+
+    Operands op[2];
+#pragma unroll
+    for (int g = 0; g < NG - 1; ++g)
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+            copy(g, g, d);
+#pragma unroll
+    for (int d = 0; d < part_of(1); ++d)
+        copy(NG - 1, NG - 1, d);
+    wait_vmcnt<(NG - 2) * ND + part_of(1)>(); // group 0 has landed
+    barrier_only();
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+        read_operand(0, 0, i, op[0]);
+    int cur = 0; // the buffer of the group at hand
+
+    // Group g of this part.  TAIL: the row's partial last group; nothing follows it.
+    auto run_group = [&](int g, auto tail) __attribute__((always_inline)) {
+        constexpr bool TAIL = decltype(tail)::value;
+        const int left = (int)((rowb - (uint32_t)(g_begin + g) * (uint32_t)T::SEG) >> 4); // pieces of a partial group
+        const int before = cur == 0 ? NG - 1 : cur - 1, after = cur == NG - 1 ? 0 : cur + 1;
+        auto step = [&](auto sel) __attribute__((always_inline)) {
+            constexpr int S = decltype(sel)::value;
+            constexpr bool END = S == STEPS - 1;
+            Operands &now = op[S & 1], &next = op[(S & 1) ^ 1];
+            if constexpr (END && !TAIL) {
+                // group g + 1 has landed: the copies of groups g + 2 .. g + NG - 1 may be in flight
+                wait_vmcnt<(NG - 2) * ND>();
+                __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0): this wave's reads of group g
+                barrier_only();
+            }
+            if constexpr (TAIL) { // pieces past the row: zero weights
+                const bool in = 4 * (S >> 1) + 2 * h + (S & 1) < left;
+#pragma unroll
+                for (int i = 0; i < T::NB; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        now.a[i][e] = in ? now.a[i][e] : 0;
+            }
+            // The step's other work, one piece at a time between the MFMAs: the next step's
+            // operands, then copies: those of group g - 1 + NG into the place of g - 1, in the
+            // last step the first ones of g + NG.
+            constexpr int PART = END ? 0 : S + 1, C0 = part_of(PART), C1 = part_of(PART + 1);
+            constexpr int READS = TAIL && END ? 0 : NR, SIDE = READS + (TAIL ? 0 : C1 - C0);
+            auto side = [&](int i) __attribute__((always_inline)) {
+                if (i < READS)
+                    read_operand(END ? after : cur, END ? 0 : S + 1, i, next);
+                else
+                    copy(END ? g + NG : g + NG - 1, END ? cur : before, C0 + i - READS);
+            };
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                const int i = m / T::MB, k = m % T::MB;
+                __builtin_amdgcn_sched_barrier(0);
+                acc[i][k] = __builtin_amdgcn_mfma_i32_32x32x32_i8(now.a[i], now.b[k], acc[i][k], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int z = 0; z < SIDE; ++z)
+                    if (z >= m * SIDE / NM && z < (m + 1) * SIDE / NM)
+                        side(z);
+            }
+        };
+        step(std::integral_constant<int, 0>{});
+        if (TAIL && left <= 1)
+            return; // (the same for the whole workgroup)
+        step(std::integral_constant<int, 1>{});
+        if constexpr (GS == 2) {
+            if (TAIL && left <= 4)
+                return;
+            step(std::integral_constant<int, 2>{});
+            if (TAIL && left <= 5)
+                return;
+            step(std::integral_constant<int, 3>{});
+        }
+        cur = after;
+    };
+    // the part's last group is run as a tail where the row ends inside it
+    const int full = rowb % T::SEG && g_end == row_groups ? groups - 1 : groups;
+    for (int g = 0; g < full; ++g)
+        run_group(g, std::false_type{});
+    if (full < groups)
+        run_group(full, std::true_type{});
+
+    // The scales (and the bias) of the tile's rows and columns, for the epilogue.
+    const bool raw = splits > 1;
+    float tile_ws = 0.f, tile_bias = 0.f, tile_xs = 0.f;
+    if (!raw) {
+        if (tid < T::TN)
+            tile_ws = a.ws[min(n0 + tid, N - 1)];
+        if (a.bias && tid < T::TN)
+            tile_bias = a.bias[min(n0 + tid, N - 1)];
+        if (tid < T::TM)
+            tile_xs = a.xs[min(m0 + tid, M - 1)];
+    }
+    wait_vmcnt<0>(); // copies past the end: none is in flight when their place is used again
+    // Every wave has read its last operands (the barrier of the last group came before them, so
+    // one more): the buffers become staging space.
+    barrier_only();
+    float *const sws = reinterpret_cast<float *>(smem), *const sb = sws + T::TN, *const sx = sb + T::TN;
+    uint8_t *const stage = smem + T::SCALES + wave * T::WSTAGE;
+    const int nw = n0 + 32 * T::NB * wn, mw = m0 + 32 * T::MB * wm;
+    if (raw) {
+        store_wave<T, DT_F32, true>(acc, part + (size_t)split * M * N, false, M, N, nw, mw, nullptr, nullptr, nullptr,
+                                    stage);
+        return;
+    }
+    if (tid < T::TN) {
+        sws[tid] = tile_ws;
+        sb[tid] = tile_bias;
+    }
+    if (tid < T::TM)
+        sx[tid] = tile_xs;
+    __syncthreads();
+    const float *const pw = sws + 32 * T::NB * wn, *const pb = sb + 32 * T::NB * wn, *const px = sx + 32 * T::MB * wm;
+    if (a.ydt == DT_F32)
+        store_wave<T, DT_F32, false>(acc, a.y, a.bias != nullptr, M, N, nw, mw, pw, pb, px, stage);
+    else if (a.ydt == DT_F16)
+        store_wave<T, DT_F16, false>(acc, a.y, a.bias != nullptr, M, N, nw, mw, pw, pb, px, stage);
+    else
+        store_wave<T, DT_BF16, false>(acc, a.y, a.bias != nullptr, M, N, nw, mw, pw, pb, px, stage);
+}
+
+// y from the sum of the K parts; n4 = N / 4.
+__global__ __launch_bounds__(256) void int8_sum_kernel(Int8GemmArgs a, const i32x4 *__restrict__ part, int64_t total4,
+                                                       int n4, int splits)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total4)
+        return;
+    const int64_t m = i / n4;
+    const int n = (int)(i - m * n4) * 4;
+    const float4_t ws = *reinterpret_cast<const float4_t *>(a.ws + n);
+    float4_t bias = {};
+    if (a.bias)
+        bias = *reinterpret_cast<const float4_t *>(a.bias + n);
+    const float xs = a.xs[m];
+    i32x4 v = part[i];
+    constexpr int B = 4; // parts under way at a time
+    for (int s0 = 1; s0 < splits; s0 += B) {
+        i32x4 p[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            p[j] = part[(size_t)min(s0 + j, splits - 1) * total4 + i];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            if (s0 + j < splits)
+                v += p[j];
+    }
+    store4(a.y, a.ydt, (size_t)i * 4, scaled4(v, xs, ws, bias, a.bias != nullptr));
+}
+
+template <class T>
+hipError_t launch_tile(const Int8GemmArgs &a, int M, int N, int K, int splits, void *workspace, hipStream_t stream)
+{
+    auto kern = int8_tile_kernel<T>;
+    static std::atomic<uint64_t> lds_set{0};
+    if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), 160 * 1024, lds_set);
+        e != hipSuccess)
+        return e;
+    const int tiles_m = (M + T::TM - 1) / T::TM;
+    const int64_t tiles = (int64_t)tiles_m * ((N + T::TN - 1) / T::TN);
+    const int nxcd = device_topology().xcds;
+    const int64_t grid = (int64_t)nxcd * ((tiles * splits + nxcd - 1) / nxcd);
+    if (grid > INT32_MAX / 256)
+        return hipErrorInvalidValue;
+    int *part = static_cast<int *>(workspace);
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), (size_t)T::LDS, stream, a, part, M, N, K, tiles_m,
+                       (int)tiles, splits, nxcd);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || splits == 1)
+        return e;
+    const int64_t total4 = (int64_t)M * N / 4;
+    hipLaunchKernelGGL(int8_sum_kernel, dim3((unsigned)((total4 + 255) / 256)), dim3(256), 0, stream, a,
+                       reinterpret_cast<const i32x4 *>(part), total4, N / 4, splits);
+    return hipGetLastError();
+}
+
+using TileL = Int8Tile<2, 4, 4, 1, 4>; // 256 x 256
+using TileM = Int8Tile<2, 2, 2, 2, 3>; // 128 x 128
+using TileS = Int8Tile<2, 1, 2, 2, 3>; // 64 weight rows x 128 activation rows
+using TileN = Int8Tile<2, 1, 1, 2, 3>; // 64 x 64
+
+bool few_rows(int64_t M, int64_t K) { return M <= 16 && M * few_pitch((int)K) <= 80 * 1024; }
+enum class Path { Few, Large, Medium, Small, Narrow };
+
+struct Plan {
+    Path path;
+    int splits;
+};
+
+template <class T>
+int64_t tile_count(int64_t M, int64_t N) { return ((M + T::TM - 1) / T::TM) * ((N + T::TN - 1) / T::TN); }
+
+// K parts for `tiles` tiles so that up to one workgroup reaches each CU, in units of 256 k.
+int k_parts(int64_t tiles, int64_t K)
+{
+    const int64_t spans = (K + 255) / 256;
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({256 / tiles, spans / 2, 16}));
+    return spans - (spans + parts - 1) / parts >= 5 ? (int)parts : 1;
+}
+
+bool large_tile(int64_t M, int64_t N)
+{
+    const int64_t large = (tile_count<TileL>(M, N) + 255) / 256, medium = (tile_count<TileM>(M, N) + 255) / 256;
+    return 2 * medium >= 5 * large;
+}
+
+Plan plan(int64_t M, int64_t N, int64_t K)
+{
+    if (few_rows(M, K))
+        return {Path::Few, 1};
+    if (large_tile(M, N))
+        return {Path::Large, 1};
+    const int64_t spans = (K + 255) / 256;
+    const int small = k_parts(tile_count<TileS>(M, N), K);
+    const int64_t medium = tile_count<TileM>(M, N);
+    const bool fills = tile_count<TileS>(M, N) > 256 && (medium <= 256 || medium > 384);
+    if (M > 64 && (spans > 11 * (int64_t)small || fills))
+        return {Path::Medium, k_parts(medium, K)};
+    if (M <= 64)
+        return {Path::Narrow, k_parts(tile_count<TileN>(M, N), K)};
+    return {Path::Small, small};
 }
 
 } // namespace
 
-size_t int8_gemm_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K)
+{
+    if (M == 0 || N == 0)
+        return 0;
+    const Plan p = plan(M, N, K);
+    return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(int) : 0;
+}
 
 hipError_t launch_int8_gemm(const Int8GemmArgs &a, int M, int N, int K, void *workspace, hipStream_t stream)
 {
-    hipLaunchKernelGGL(int8_simple_kernel, dim3((unsigned)((int64_t)((N + 63) / 64) * ((M + 63) / 64))), dim3(256), 0, stream, a.x,
-                       a.xs, a.w, a.ws, a.bias, a.y, a.ydt, M, N, K);
-    return hipGetLastError();
+    const Plan p = plan(M, N, K);
+    if (p.path == Path::Few) {
+        const int groups = (N + FR_ROWS - 1) / FR_ROWS;
+        if (groups > 256 && (K >= 2048 || (K > 1024 && M > 8)))
+            return launch_few<8, 2>(a, M, N, K, stream);
+        if (K >= 2048)
+            return launch_few<8, 1>(a, M, N, K, stream);
+        return launch_few<4, 1>(a, M, N, K, stream);
+    }
+    if (p.path == Path::Large)
+        return launch_tile<TileL>(a, M, N, K, 1, workspace, stream);
+    if (p.path == Path::Medium)
+        return launch_tile<TileM>(a, M, N, K, p.splits, workspace, stream);
+    if (p.path == Path::Narrow)
+        return launch_tile<TileN>(a, M, N, K, p.splits, workspace, stream);
+    return launch_tile<TileS>(a, M, N, K, p.splits, workspace, stream);
 }
 
 } // namespace wob
