@@ -178,8 +178,9 @@ hipError_t launch_few(const Int8GemmArgs &a, int M, int N, int K, hipStream_t st
 // A workgroup of 4 waves (WN along n, 4 / WN along m) owns TN weight rows x TM activation
 // rows; a wave owns NB x MB blocks of 32 x 32 outputs.  K advances in stages of 64 (64
 // bytes a row).  GS of them form a group, which is copied as one piece of 64 GS bytes a
-// row; NG groups are in LDS at a time, copied by global_load_lds (1 KB a wave
-// instruction), NG - 1 groups ahead of their use.
+// row.  LDS holds NH half groups (the weight rows' bytes and the activation rows' are halves
+// of a group) in a ring: half i of the sequence A0 B0 A1 B1 .. lies in place i % NH, and is
+// copied by global_load_lds (1 KB a wave instruction) as soon as half i - NH has been used.
 //
 // A stage is two MFMA steps of 32 k: in step j the lane half h = lane / 32 supplies the 16
 // bytes of piece 2 h + j of its row.  LDS row R (weight rows, then activation rows) holds
@@ -188,19 +189,23 @@ hipError_t launch_few(const Int8GemmArgs &a, int M, int N, int K, hipStream_t st
 //
 // Order within a group: its steps but the last read the next step's operands and multiply;
 // then group g + 1's copies are waited for, a barrier makes them visible and frees group g's
-// place (every wave has its last operands in registers), and the last step reads group
-// g + 1's first operands and starts the copies of group g + NG while it multiplies.
-template <int WN_, int NB_, int MB_, int GS_, int NG_>
+// places (every wave has its last operands in registers), and the last step reads group
+// g + 1's first operands and starts the copies into group g's places while it multiplies;
+// the steps of group g + 1 go on with them.
+template <int WN_, int NB_, int MB_, int GS_, int NH_>
 struct Int8Tile {
-    static constexpr int WN = WN_, WM = 4 / WN_, NB = NB_, MB = MB_, GS = GS_, NG = NG_;
+    static constexpr int WN = WN_, WM = 4 / WN_, NB = NB_, MB = MB_, GS = GS_, NH = NH_;
     static constexpr int TN = 32 * NB * WN, TM = 32 * MB * WM, ROWS = TN + TM;
     static constexpr int SEG = 64 * GS;                  // bytes of a row in a group
     static constexpr int GROUP = ROWS * SEG;             // bytes of one group
     static constexpr int ND = GROUP / 4096;              // copies per wave and group
+    static constexpr int NDA = TN * SEG / 4096;          // of them weight rows
+    static constexpr int RING = NH * GROUP / 2;
     static constexpr int SCALES = 4 * (2 * TN + TM);     // scales and bias of the tile, in the epilogue
     static constexpr int WSTAGE = 32 * (128 * NB + 16);  // LDS of one wave in the epilogue
-    static constexpr int LDS = std::max(NG * GROUP, SCALES + 4 * WSTAGE);
-    static_assert(ROWS % 64 == 0 && (GS == 1 || GS == 2) && NG >= 2 && LDS <= 160 * 1024, "tile geometry");
+    static constexpr int LDS = std::max(RING, SCALES + 4 * WSTAGE);
+    static_assert(ROWS % 64 == 0 && (GS == 1 || GS == 2) && NH >= 4 && LDS <= 160 * 1024, "tile geometry");
+    static_assert(NH % 2 == 0 || TN == TM, "halves of one size");
 };
 
 // A wave's outputs (n from nw, m from mw) through its part of LDS, 32 output rows at a
@@ -222,10 +227,16 @@ __device__ __forceinline__ void store_wave(const i32x16 (&acc)[T::NB][T::MB], vo
     for (int k = 0; k < T::MB; ++k) {
         const float x = RAW ? 0.f : xs[32 * k + r];
 #pragma unroll
-        for (int i = 0; i < T::NB; ++i)
+        for (int i = 0; i < T::NB; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            i32x16 block = acc[i][k];
+            // 256 accumulators stay in the accumulator registers up to their use (taken out for
+            // all stores at once, half of them went through memory)
+            if constexpr (T::NB * T::MB == 16)
+                asm volatile("" : "+a"(block));
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const i32x4 sum{acc[i][k][4 * g], acc[i][k][4 * g + 1], acc[i][k][4 * g + 2], acc[i][k][4 * g + 3]};
+                const i32x4 sum{block[4 * g], block[4 * g + 1], block[4 * g + 2], block[4 * g + 3]};
                 const int at = 32 * i + 8 * g + 4 * h;
                 uint8_t *to = stage + r * PITCH + at * ES;
                 if constexpr (RAW) {
@@ -240,6 +251,8 @@ __device__ __forceinline__ void store_wave(const i32x16 (&acc)[T::NB][T::MB], vo
                             uint2{f32x2_to_act2<DT>(v[0], v[1]), f32x2_to_act2<DT>(v[2], v[3])};
                 }
             }
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = 0; q < 32 / RPI; ++q) {
             const int row = q * RPI + lane / VECS, m = mw + 32 * k + row;
@@ -264,13 +277,14 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave % T::WN, wm = wave / T::WN;
-    constexpr int GS = T::GS, NG = T::NG, STEPS = 2 * GS, ND = T::ND;
+    constexpr int GS = T::GS, NH = T::NH, STEPS = 2 * GS, ND = T::ND, NDA = T::NDA;
+    constexpr bool ODD = NH % 2 != 0;
     const int row_groups = (K + T::SEG - 1) / T::SEG;
     const int g_begin = (int)((int64_t)row_groups * split / splits);
     const int g_end = (int)((int64_t)row_groups * (split + 1) / splits); // > g_begin: splits <= row_groups
     const int groups = g_end - g_begin;
     const uint32_t rowb = (uint32_t)K;
-    constexpr auto part_of = [](int w) { return w * ND / STEPS; }; // copies before part w of a group's STEPS
+    constexpr auto part_of = [](int w) { return w * ND / STEPS; }; // copies before part w of STEPS
 
     // Copy d of wave v fills LDS rows RI (4 d + v) .. + RI - 1: lane L the position L % LR of
     // row L / LR.  Rows past the matrix repeat its last row (never stored), pieces past the
@@ -287,16 +301,35 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
     auto swizzle = [](int R) __attribute__((always_inline)) { return GS == 1 ? (R >> 2) & 3 : (R >> 1) & 7; };
     const uint32_t piece = 16u * (uint32_t)(lane % LR ^ swizzle(RI * wave + lane / LR));
     const uint32_t lds0 = (uint32_t)(size_t)(lds_ptr_t *)smem;
-    auto copy = [&](int g, int b, int d) __attribute__((always_inline)) { // group g into buffer b
-        const int from = g_begin + min(g, groups - 1); // past the end: the last group again
+    struct Place { // of a group's halves in LDS
+        int a, b;
+    };
+    auto half_size = [](bool second) { return second ? T::TM * T::SEG : T::TN * T::SEG; };
+    auto following = [&](Place p) __attribute__((always_inline)) { // of the next group
+        if constexpr (!ODD) {
+            const int a = p.a + T::GROUP == T::RING ? 0 : p.a + T::GROUP;
+            return Place{a, a + half_size(false)};
+        }
+        auto two_on = [](int at) { return at + T::GROUP >= T::RING ? at + T::GROUP - T::RING : at + T::GROUP; };
+        return Place{two_on(p.a), two_on(p.b)};
+    };
+    // Copy d of those into the places of group g, once they are free: the next halves of the
+    // sequence that are not in LDS, A and B of group g + NH / 2 (NH odd: B of that one and A of
+    // the one after it).
+    auto copy = [&](int g, const Place &p, int d) __attribute__((always_inline)) {
+        const bool second = d >= (ODD ? ND / 2 : NDA); // into place b
+        const bool b_rows = ODD ? !second : second;
+        const int i = ODD ? (second ? d - ND / 2 : d + ND / 2) : d;
+        // past the end: the last group again
+        const int from = g_begin + min(g + NH / 2 + (ODD && second), groups - 1);
         const uint32_t k = min((uint32_t)from * (uint32_t)T::SEG + piece, rowb - 16u);
-        const uint32_t to = lds0 + (uint32_t)(b * T::GROUP + wave * 1024);
-        lds_dma16(4 * RI * d < T::TN ? a.w : a.x, row_at[d] + k, to + (uint32_t)(4096 * d));
+        const int to = (second ? p.b : p.a) + 4096 * (second ? d - (ODD ? ND / 2 : NDA) : d) + wave * 1024;
+        lds_dma16(b_rows ? a.x : a.w, row_at[i] + k, lds0 + (uint32_t)to);
     };
 
     i32x16 acc[T::NB][T::MB] = {};
 
-    const int an = 32 * T::NB * wn + r, bm = T::TN + 32 * T::MB * wm + r; // this lane's first LDS rows
+    const int an = 32 * T::NB * wn + r, bm = 32 * T::MB * wm + r; // this lane's first rows in LDS
     uint32_t at[GS][2]; // position of piece 4 p + 2 h + j in a row of this lane
 #pragma unroll
     for (int p = 0; p < GS; ++p)
@@ -308,43 +341,65 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
         i32x4 a[T::NB], b[T::MB];
     };
     constexpr int NR = T::NB + T::MB, NM = T::NB * T::MB;
-    // operand i (weight blocks, then activation blocks) of step s of the group in buffer b
-    auto read_operand = [&](int b, int s, int i, Operands &o) __attribute__((always_inline)) {
-        const uint8_t *base = smem + b * T::GROUP + at[s >> 1][s & 1];
+    // operand i (weight blocks, then activation blocks) of step s of the group at p
+    auto read_operand = [&](const Place &p, int s, int i, Operands &o) __attribute__((always_inline)) {
+        const uint32_t lane_at = at[s >> 1][s & 1];
         if (i < T::NB)
-            o.a[i] = *reinterpret_cast<const i32x4 *>(base + (an + 32 * i) * T::SEG);
+            o.a[i] = *reinterpret_cast<const i32x4 *>(smem + p.a + lane_at + (an + 32 * i) * T::SEG);
         else
-            o.b[i - T::NB] = *reinterpret_cast<const i32x4 *>(base + (bm + 32 * (i - T::NB)) * T::SEG);
+            o.b[i - T::NB] = *reinterpret_cast<const i32x4 *>(smem + p.b + lane_at + (bm + 32 * (i - T::NB)) * T::SEG);
     };
 
     Operands op[2];
+    Place now_at = {0, half_size(false)}; // of the group at hand
+    // of the group before it, whose places are being filled again; of group -1 the last ones
+    Place before = {(NH - 2) * (T::GROUP / 2), (NH - 2) * (T::GROUP / 2) + half_size(false)};
+    {
+        // halves 0 .. NH - 3, as the ones that groups -NH / 2 .. -2 (NH odd: and half of one before
+        // them) leave their places to
+        Place p = now_at;
+        if constexpr (ODD) {
 #pragma unroll
-    for (int g = 0; g < NG - 1; ++g)
+            for (int i = 0; i < NH - 2; ++i) {
+                const bool second = i % 2 != 0;
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
-            copy(g, g, d);
+                for (int d = 0; d < ND / 2; ++d) {
+                    const uint32_t k = min((uint32_t)(g_begin + min(i / 2, groups - 1)) * (uint32_t)T::SEG + piece, rowb - 16u);
+                    lds_dma16(second ? a.x : a.w, row_at[second ? d + ND / 2 : d] + k,
+                              lds0 + (uint32_t)(i * (T::GROUP / 2) + 4096 * d + wave * 1024));
+                }
+            }
+        } else {
 #pragma unroll
-    for (int d = 0; d < part_of(1); ++d)
-        copy(NG - 1, NG - 1, d);
-    wait_vmcnt<(NG - 2) * ND + part_of(1)>(); // group 0 has landed
+            for (int g = 0; g < NH / 2 - 1; ++g) {
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+                    copy(g - NH / 2, p, d);
+                p = following(p);
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < part_of(1); ++d)
+            copy(-1, before, d);
+        wait_vmcnt<(NH - 4) * ND / 2 + part_of(1)>(); // group 0 has landed
+    }
     barrier_only();
 #pragma unroll
     for (int i = 0; i < NR; ++i)
-        read_operand(0, 0, i, op[0]);
-    int cur = 0; // the buffer of the group at hand
+        read_operand(now_at, 0, i, op[0]);
 
     // Group g of this part.  TAIL: the row's partial last group; nothing follows it.
     auto run_group = [&](int g, auto tail) __attribute__((always_inline)) {
         constexpr bool TAIL = decltype(tail)::value;
         const int left = (int)((rowb - (uint32_t)(g_begin + g) * (uint32_t)T::SEG) >> 4); // pieces of a partial group
-        const int before = cur == 0 ? NG - 1 : cur - 1, after = cur == NG - 1 ? 0 : cur + 1;
+        const Place after = following(now_at);
         auto step = [&](auto sel) __attribute__((always_inline)) {
             constexpr int S = decltype(sel)::value;
             constexpr bool END = S == STEPS - 1;
             Operands &now = op[S & 1], &next = op[(S & 1) ^ 1];
             if constexpr (END && !TAIL) {
-                // group g + 1 has landed: the copies of groups g + 2 .. g + NG - 1 may be in flight
-                wait_vmcnt<(NG - 2) * ND>();
+                // group g + 1 has landed: the halves behind it may be in flight
+                wait_vmcnt<(NH - 4) * ND / 2>();
                 __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0): this wave's reads of group g
                 barrier_only();
             }
@@ -357,15 +412,15 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
                         now.a[i][e] = in ? now.a[i][e] : 0;
             }
             // The step's other work, one piece at a time between the MFMAs: the next step's
-            // operands, then copies: those of group g - 1 + NG into the place of g - 1, in the
-            // last step the first ones of g + NG.
+            // operands, then copies: those into the places of group g - 1, in the last step the
+            // first ones into the places of g.
             constexpr int PART = END ? 0 : S + 1, C0 = part_of(PART), C1 = part_of(PART + 1);
             constexpr int READS = TAIL && END ? 0 : NR, SIDE = READS + (TAIL ? 0 : C1 - C0);
             auto side = [&](int i) __attribute__((always_inline)) {
                 if (i < READS)
-                    read_operand(END ? after : cur, END ? 0 : S + 1, i, next);
+                    read_operand(END ? after : now_at, END ? 0 : S + 1, i, next);
                 else
-                    copy(END ? g + NG : g + NG - 1, END ? cur : before, C0 + i - READS);
+                    copy(END ? g : g - 1, END ? now_at : before, C0 + i - READS);
             };
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
@@ -391,7 +446,8 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
                 return;
             step(std::integral_constant<int, 3>{});
         }
-        cur = after;
+        before = now_at;
+        now_at = after;
     };
     // the part's last group is run as a tail where the row ends inside it
     const int full = rowb % T::SEG && g_end == row_groups ? groups - 1 : groups;
@@ -494,10 +550,10 @@ hipError_t launch_tile(const Int8GemmArgs &a, int M, int N, int K, int splits, v
     return hipGetLastError();
 }
 
-using TileL = Int8Tile<2, 4, 4, 1, 4>; // 256 x 256
-using TileM = Int8Tile<2, 2, 2, 2, 3>; // 128 x 128
-using TileS = Int8Tile<2, 1, 2, 2, 3>; // 64 weight rows x 128 activation rows
-using TileN = Int8Tile<2, 1, 1, 2, 3>; // 64 x 64
+using TileL = Int8Tile<2, 4, 4, 2, 5>; // 256 x 256
+using TileM = Int8Tile<2, 2, 2, 2, 6>; // 128 x 128
+using TileS = Int8Tile<2, 1, 2, 2, 6>; // 64 weight rows x 128 activation rows
+using TileN = Int8Tile<2, 1, 1, 2, 6>; // 64 x 64
 
 bool few_rows(int64_t M, int64_t K) { return M <= 16 && M * few_pitch((int)K) <= 80 * 1024; }
 enum class Path { Few, Large, Medium, Small, Narrow };
