@@ -18,11 +18,15 @@
 #include "moe_choice.hpp"
 #include "weight_only_bit.h"
 
+#include <type_traits>
+
 namespace wob {
 
 namespace {
 
-constexpr int RT = 256; // threads
+// Threads of a workgroup: its lanes' keys and scores fit in static LDS.
+template <int V>
+constexpr int route_threads() { return V > 16 ? 128 : 256; }
 
 struct RouteSplit { // how a token's experts lie in its lanes
     int span, run;  // lanes of a group, experts of a lane
@@ -120,9 +124,29 @@ __device__ __forceinline__ int lowest_lane(bool on)
     return __ffs(half >> (lane & 16) & 0xFFFFu) - 1;
 }
 
+// Batcher's odd-even merge sort of V values as pairs of places.
+template <int V>
+struct SortNet {
+    int n = 0, a[V * 8] = {}, b[V * 8] = {};
+    constexpr SortNet()
+    {
+        for (int p = 1; p < V; p *= 2)
+            for (int k = p; k >= 1; k /= 2)
+                for (int j = k % p; j + k < V; j += 2 * k)
+                    for (int i = 0; i < k && i + j + k < V; ++i)
+                        if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                            a[n] = i + j;
+                            b[n++] = i + j + k;
+                        }
+    }
+};
+
 template <int DT, int L, int V, bool QUAD>
-__global__ __launch_bounds__(RT) void moe_route_kernel(RouteArgs a, RouteSplit split)
+__global__ __launch_bounds__(route_threads<V>()) void moe_route_kernel(RouteArgs a, RouteSplit split)
 {
+    constexpr int RT = route_threads<V>(), PITCH = V + (V >= 4 ? 4 : 1); // (lanes' rows in different banks)
+    __shared__ __align__(16) uint32_t keys[RT * PITCH];
+    __shared__ __align__(16) float scores[RT * PITCH];
     const int g = threadIdx.x % L, t = blockIdx.x * (RT / L) + threadIdx.x / L;
     const int span = split.span, run = split.run, size = a.E / a.groups;
     const int group = g / span, from = (g - group * span) * run; // of this lane: the group, the first expert in it
@@ -172,11 +196,11 @@ __global__ __launch_bounds__(RT) void moe_route_kernel(RouteArgs a, RouteSplit s
         double q[V], sum = 0.0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            q[v] = exp2_64(fmax(((double)l[v] - (double)top) * LOG2E, -1000.0));
-            q[v] = l[v] == none ? 0.0 : l[v] == top ? 1.0 : q[v];
+            // (no exp2 under a condition: 0 gives exactly 1, -1000 nothing in 32 bits)
+            q[v] = exp2_64(l[v] == top ? 0.0 : fmax(((double)l[v] - (double)top) * LOG2E, -1000.0));
             sum += q[v];
         }
-        const double r = recip_64(fmax(group_sum64<L>(sum), 1.0)); // a row with an expert sums to 1 or more
+        const double r = recip_64(group_sum64<L>(sum)); // (1 or more; of a row without an expert nothing is used)
 #pragma unroll
         for (int v = 0; v < V; ++v)
             p[v] = (float)(q[v] * r);
@@ -211,45 +235,86 @@ __global__ __launch_bounds__(RT) void moe_route_kernel(RouteArgs a, RouteSplit s
             key[v] = kept ? key[v] : 0u;
     }
 
-    // Place after place: the largest key, the lowest expert that has it, its key cleared.
+    // Every lane sorts its keys; then place after place goes to the largest head, of the lowest
+    // lane that has it, and that lane's list moves up.  Which of the lane's experts it was
+    // is looked up afterwards, for all places at once: equal keys of a lane come
+    // one after the other, the n-th of them is the n-th expert with that key.
+    uint32_t *const my_keys = keys + threadIdx.x * PITCH;
+    float *const my_scores = scores + threadIdx.x * PITCH;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        my_keys[v] = key[v];
+        my_scores[v] = p[v];
+    }
+    constexpr SortNet<V> net;
+#pragma unroll
+    for (int i = 0; i < net.n; ++i) {
+        const uint32_t x = key[net.a[i]], y = key[net.b[i]];
+        key[net.a[i]] = max(x, y);
+        key[net.b[i]] = min(x, y);
+    }
     constexpr int PL = (CHOICE_MAX + L - 1) / L; // places of a lane: i L + g
+    uint32_t chosen[PL];                         // key of the place, 0 for none
+    int where[PL];                               // 256 * the lane + which of its equal keys
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+        chosen[j] = 0u;
+        where[j] = 0;
+    }
+    uint32_t last = 0u;
+    int last_where = -1;
+    auto places = [&](auto depth) __attribute__((always_inline)) { // lists no deeper than that are used up
+        constexpr int D = decltype(depth)::value;
+#pragma unroll
+        for (int j = 0; j < PL; ++j)
+            for (int i = 0; i < L && j * L + i < a.topk; ++i) {
+                const uint32_t best = group_reduce<L>(key[0], lane_max);
+                const int owner = lowest_lane<L>(key[0] == best);
+                last_where = best == last && last_where >> 8 == owner ? last_where + 1 : owner << 8;
+                last = best;
+                if (g == i) {
+                    chosen[j] = best;
+                    where[j] = last_where;
+                }
+                const bool pop = g == owner;
+#pragma unroll
+                for (int v = 0; v < D - 1; ++v)
+                    key[v] = pop ? key[v + 1] : key[v];
+                key[D - 1] = pop ? 0u : key[D - 1];
+            }
+    };
+    if constexpr (V > 8) {
+        if (a.topk <= 8)
+            places(std::integral_constant<int, 8>{});
+        else
+            places(std::integral_constant<int, V>{});
+    } else {
+        places(std::integral_constant<int, V>{});
+    }
+    __builtin_amdgcn_wave_barrier(); // a wave reads only what it wrote, in order
     int id[PL];
     float s[PL];
 #pragma unroll
     for (int j = 0; j < PL; ++j) {
         id[j] = -1;
         s[j] = 0.f;
-    }
+        if (j * L >= a.topk)
+            continue;
+        const int owner = where[j] >> 8, row_at = ((int)threadIdx.x - g + owner) * PITCH;
+        int v_at = 0;
+        int seen = where[j] & 255;
+        bool open = true;
 #pragma unroll
-    for (int j = 0; j < PL; ++j) {
-        for (int i = 0; i < L && j * L + i < a.topk; ++i) {
-            uint32_t best = key[0];
-#pragma unroll
-            for (int v = 1; v < V; ++v)
-                best = max(best, key[v]);
-            const uint32_t local = best;
-            best = group_reduce<L>(best, lane_max);
-            if (!__any(best != 0u))
-                break;
-            const int owner = lowest_lane<L>(local == best);
-            bool open = g == owner && best != 0u; // until the owner has found it
-            int e = 0;
-            float own = 0.f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const bool hit = open && key[v] == best;
-                key[v] = hit ? 0u : key[v];
-                e = hit ? v : e;
-                own = hit ? p[v] : own;
-                open = open && !hit;
-            }
-            const int at = (int)(threadIdx.x & 63 & ~(L - 1)) + owner;
-            e = __shfl(e + e0, at);
-            own = __shfl(own, at);
-            if (g == i && best != 0u) {
-                id[j] = e;
-                s[j] = own;
-            }
+        for (int v = 0; v < V; ++v) {
+            const bool match = open && keys[row_at + v] == chosen[j];
+            const bool hit = match && seen == 0;
+            v_at = hit ? v : v_at;
+            open = open && !hit;
+            seen -= match;
+        }
+        if (chosen[j] != 0u) {
+            id[j] = owner / span * size + owner % span * run + v_at;
+            s[j] = scores[row_at + v_at];
         }
     }
     float total = 1.f;
@@ -290,6 +355,7 @@ hipError_t launch_v(const RouteArgs &a, const RouteSplit &split, hipStream_t str
     if constexpr ((L == 16 && V < 16) || (L == 64 && V < 32))
         if (split.run > V)
             return launch_v<DT, L, 2 * V>(a, split, stream);
+    constexpr int RT = route_threads<V>();
     const dim3 grid((unsigned)((a.T + RT / L - 1) / (RT / L)));
     if constexpr (V % 4 == 0) {
         if (a.E / a.groups % 4 == 0) {
