@@ -42,12 +42,12 @@ __all__ = [
 
 _torch_mod = None
 _tags = None
-_raw_stream = _get_device = _values = _bytes = _int8 = _fp32 = None
+_raw_stream = _get_device = _empty_here = _values = _bytes = _int8 = _fp32 = None
 
 
 def _torch():
     """torch, imported on first use; the dtype tags and the device and stream queries with it."""
-    global _torch_mod, _tags, _values, _bytes, _int8, _fp32, _raw_stream, _get_device
+    global _torch_mod, _tags, _values, _bytes, _int8, _fp32, _raw_stream, _get_device, _empty_here
     if _torch_mod is None:
         import torch
         _tags = {torch.float16: F16, torch.bfloat16: BF16, torch.int32: U4X8_I32,
@@ -59,6 +59,9 @@ def _torch():
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        # a contiguous tensor on the current device: 0.8 against 1.7 us
+        guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
+        _empty_here = getattr(guards, "_empty_strided_cuda", None)
         _torch_mod = torch
     return _torch_mod
 
@@ -284,6 +287,10 @@ def mxfp4_moe_stage2(a, topk_ids, topk_weights, w2_fp4, w2_scale, out=None, work
 def _output(t, name, shape, dtype, device):
     """A caller's output on `device`, checked, or a new one, which needs no check."""
     if t is None:
+        index = device.index  # None: the host, which the caller refuses
+        if index is not None and _empty_here is not None and len(shape) <= 2 and 0 not in shape \
+                and _get_device() == index:
+            return _empty_here(shape, (shape[1], 1) if len(shape) == 2 else (1,) * len(shape), dtype)
         return _torch_mod.empty(shape, dtype=dtype, device=device)
     _want(t, name, shape, (dtype,))
     if _check_device(t) != device:

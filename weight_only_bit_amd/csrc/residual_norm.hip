@@ -19,138 +19,148 @@ namespace wob {
 namespace {
 
 // NT threads share a row, V pieces of eight elements a thread: piece j of thread t is j NT + t.
+// All loads of a row are issued before the first of them is used, as far as registers reach.
 // residual_out may be residual: a thread reads its pieces before it writes them.
+//
+// 16384 x 5376 fp16 with a gate per element (881 MB) 151 us, 5.8 TB/s; 2048 x 5376 bf16 with a
+// 32-bit residual into 8 bits 28.  With y read, summed and only then the residual and the gate
+// read, and several rows a workgroup (whose addresses took 40 registers), 222 and 41.  Threads x
+// pieces for the two and one row: 256 x 3 153, 29.2, 4.5; 384 x 2 151, 29.9, 3.9; 512 x 2 152,
+// 28.2, 3.7; 1024 x 1 157, 30.4, 3.6.
 template <int DT, int RDT, int NT, int V>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_kernel(NormArgs a)
 {
+    static_assert(NT == 64 || NT >= 256, "rows that share a workgroup share no barrier");
     constexpr int ROWS = NT < 256 ? 256 / NT : 1, ES = elem_size<DT>(), RES = elem_size<RDT>();
-    __shared__ uint32_t part[4][NT / 64];
+    __shared__ uint32_t part[3][NT / 64];
     const int t = threadIdx.x % NT, pieces = a.H / RV;
-    int turn = 0; // reductions take four slots in turn: none is written while it is read
-    for (int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / NT; row < a.T;
-         row += (int64_t)gridDim.x * ROWS) {
-        float h[V][RV];
-        const uint8_t *r = static_cast<const uint8_t *>(a.residual) + row * a.H * RES;
-        if (a.y) {
-            const uint8_t *y = static_cast<const uint8_t *>(a.y) + row * a.ldy * ES;
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int p = j * NT + t;
-                if (p < pieces) {
-                    load8<DT>(y + (int64_t)p * RV * ES, h[j]);
-#pragma unroll
-                    for (int i = 0; i < RV; ++i)
-                        sum = __builtin_fmaf(h[j][i], h[j][i], sum);
-                }
-            }
-            float rstd = 1.0f;
-            if (a.post)
-                rstd = 1.0f / __builtin_sqrtf(row_sum<NT>(sum, part[turn++ & 3]) / (float)a.H + a.eps);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int p = j * NT + t;
-                if (p < pieces) {
-                    float v[RV], g[RV];
-                    if (a.post) {
-                        load8<DT>(static_cast<const uint8_t *>(a.post) + (int64_t)p * RV * ES, v);
-#pragma unroll
-                        for (int i = 0; i < RV; ++i)
-                            h[j][i] *= rstd * v[i];
-                    }
-                    load8<RDT>(r + (int64_t)p * RV * RES, v);
-                    if (a.gate) {
-                        load8<DT>(static_cast<const uint8_t *>(a.gate) + (row * a.ldg + (int64_t)p * RV) * ES, g);
-#pragma unroll
-                        for (int i = 0; i < RV; ++i)
-                            h[j][i] = __builtin_fmaf(a.alpha * g[i], h[j][i], v[i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < RV; ++i)
-                            h[j][i] = __builtin_fmaf(a.alpha, h[j][i], v[i]);
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int p = j * NT + t;
-                if (p < pieces)
-                    load8<RDT>(r + (int64_t)p * RV * RES, h[j]);
-            }
-        }
-        if (a.residual_out) {
-            uint8_t *out = static_cast<uint8_t *>(a.residual_out) + row * a.H * RES;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int p = j * NT + t;
-                if (p < pieces)
-                    store8<RDT>(out + (int64_t)p * RV * RES, h[j]);
-            }
-        }
-        if (!a.weight)
-            continue;
-        float sum = 0.f;
+    const int64_t row = a.row0 + (int64_t)blockIdx.x * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+    if (row >= a.T) // (NT < 256: waves without a row; no barrier follows there)
+        return;
+    // f(j, p) for every piece p = j NT + t of this thread
+    auto each = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
             if (j * NT + t < pieces)
+                f(j, j * NT + t);
+    };
+    auto row_of = [&](const void *base, int64_t ld, int size) __attribute__((always_inline)) {
+        return static_cast<const uint8_t *>(base) + row * ld * size;
+    };
+    Raw8<RDT> r[V];
+    Raw8<DT> y[V], gate[V], post[V], weight[V];
+    if (a.y)
+        each([&](int j, int p) { load_raw8<DT>(row_of(a.y, a.ldy, ES) + (uint32_t)(p * RV) * ES, y[j]); });
+    each([&](int j, int p) { load_raw8<RDT>(row_of(a.residual, a.H, RES) + (uint32_t)(p * RV) * RES, r[j]); });
+    auto load_gate = [&]() __attribute__((always_inline)) {
+        each([&](int j, int p) { load_raw8<DT>(row_of(a.gate, a.ldg, ES) + (uint32_t)(p * RV) * ES, gate[j]); });
+    };
+    auto load_weights = [&](const void *w, Raw8<DT> (&to)[V]) __attribute__((always_inline)) {
+        each([&](int j, int p) { load_raw8<DT>(static_cast<const uint8_t *>(w) + (uint32_t)(p * RV) * ES, to[j]); });
+    };
+    constexpr bool EARLY = V < 4, GATE_EARLY = EARLY || DT != DT_F32; // (else they do not fit the registers)
+    if (GATE_EARLY && a.gate)
+        load_gate();
+    if (EARLY && a.post)
+        load_weights(a.post, post);
+    if (EARLY && a.weight)
+        load_weights(a.weight, weight);
+
+    float h[V][RV];
+    if (a.y) {
+        each([&](int j, int) { unpack8<DT>(y[j], h[j]); });
+        if (a.post) {
+            float sum = 0.f;
+            each([&](int j, int) {
 #pragma unroll
                 for (int i = 0; i < RV; ++i)
                     sum = __builtin_fmaf(h[j][i], h[j][i], sum);
-        const float rstd = 1.0f / __builtin_sqrtf(row_sum<NT>(sum, part[turn++ & 3]) / (float)a.H + a.eps);
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int p = j * NT + t;
-            if (p < pieces) {
+            });
+            const float rstd = 1.0f / __builtin_sqrtf(row_sum<NT>(sum, part[0]) / (float)a.H + a.eps);
+            if (!EARLY)
+                load_weights(a.post, post);
+            each([&](int j, int) {
                 float w[RV];
-                load8<DT>(static_cast<const uint8_t *>(a.weight) + (int64_t)p * RV * ES, w);
+                unpack8<DT>(post[j], w);
 #pragma unroll
                 for (int i = 0; i < RV; ++i)
                     h[j][i] *= rstd * w[i];
-                top = max(top, magnitude8(h[j]));
-            }
+            });
         }
-        if (a.quant == WOB_QUANT_NONE) {
+        if (!GATE_EARLY && a.gate)
+            load_gate();
+        each([&](int j, int) {
+            float v[RV];
+            unpack8<RDT>(r[j], v);
+            if (a.gate) {
+                float g[RV];
+                unpack8<DT>(gate[j], g);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int p = j * NT + t;
-                if (p < pieces)
-                    store8<DT>(static_cast<uint8_t *>(a.n) + (row * a.H + (int64_t)p * RV) * ES, h[j]);
-            }
-        } else if (a.quant == WOB_QUANT_INT8) {
-            const Int8Row s = int8_row(row_max<NT>(top, part[turn++ & 3]));
+                for (int i = 0; i < RV; ++i)
+                    h[j][i] = __builtin_fmaf(a.alpha * g[i], h[j][i], v[i]);
+            } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int p = j * NT + t;
-                if (p < pieces)
-                    static_cast<uint2 *>(a.n)[row * pieces + p] = int8_codes8(h[j], s);
+                for (int i = 0; i < RV; ++i)
+                    h[j][i] = __builtin_fmaf(a.alpha, h[j][i], v[i]);
             }
-            if (t == 0)
-                static_cast<float *>(a.n_scale)[row] = s.scale;
-        } else {
+        });
+    } else {
+        each([&](int j, int) { unpack8<RDT>(r[j], h[j]); });
+    }
+    if (a.residual_out)
+        each([&](int j, int p) {
+            store8<RDT>(static_cast<uint8_t *>(a.residual_out) + (row * a.H + (uint32_t)(p * RV)) * RES, h[j]);
+        });
+    if (!a.weight)
+        return;
+    float sum = 0.f;
+    each([&](int j, int) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int p = j * NT + t;
-                if (p < pieces) { // H % 32 == 0: a quad of lanes has a block or none
-                    uint32_t b;
-                    static_cast<uint32_t *>(a.n)[row * pieces + p] = mxfp4_codes8(h[j], b);
-                    if ((t & 3) == 0)
-                        static_cast<uint8_t *>(a.n_scale)[(row * pieces + p) >> 2] = (uint8_t)b;
-                }
-            }
-        }
+        for (int i = 0; i < RV; ++i)
+            sum = __builtin_fmaf(h[j][i], h[j][i], sum);
+    });
+    const float rstd = 1.0f / __builtin_sqrtf(row_sum<NT>(sum, part[1]) / (float)a.H + a.eps);
+    if (!EARLY)
+        load_weights(a.weight, weight);
+    each([&](int j, int) {
+        float w[RV];
+        unpack8<DT>(weight[j], w);
+#pragma unroll
+        for (int i = 0; i < RV; ++i)
+            h[j][i] *= rstd * w[i];
+    });
+    if (a.quant == WOB_QUANT_NONE) {
+        each([&](int j, int p) { store8<DT>(static_cast<uint8_t *>(a.n) + (row * a.H + (uint32_t)(p * RV)) * ES, h[j]); });
+    } else if (a.quant == WOB_QUANT_INT8) {
+        uint32_t top = 0;
+        each([&](int j, int) { top = max(top, magnitude8(h[j])); });
+        const Int8Row s = int8_row(row_max<NT>(top, part[2]));
+        each([&](int j, int p) { static_cast<uint2 *>(a.n)[row * pieces + p] = int8_codes8(h[j], s); });
+        if (t == 0)
+            static_cast<float *>(a.n_scale)[row] = s.scale;
+    } else {
+        each([&](int j, int p) { // H % 32 == 0: a quad of lanes has a block or none
+            uint32_t b;
+            static_cast<uint32_t *>(a.n)[row * pieces + p] = mxfp4_codes8(h[j], b);
+            if ((t & 3) == 0)
+                static_cast<uint8_t *>(a.n_scale)[(row * pieces + p) >> 2] = (uint8_t)b;
+        });
     }
 }
 
 template <int DT, int RDT, int NT, int V>
-hipError_t launch_rows(const NormArgs &a, hipStream_t stream)
+hipError_t launch_rows(NormArgs a, hipStream_t stream)
 {
     constexpr int ROWS = NT < 256 ? 256 / NT : 1;
-    const int64_t grid = std::min<int64_t>((a.T + ROWS - 1) / ROWS, (int64_t)1 << 20);
-    hipLaunchKernelGGL((residual_norm_kernel<DT, RDT, NT, V>), dim3((unsigned)grid), dim3(NT * ROWS), 0,
-                       stream, a);
-    return hipGetLastError();
+    constexpr int64_t MOST = (int64_t)1 << 21; // rows of a launch: 2^31 threads at most
+    for (a.row0 = 0; a.row0 < a.T; a.row0 += MOST) {
+        const int64_t rows = std::min(a.T - a.row0, MOST);
+        hipLaunchKernelGGL((residual_norm_kernel<DT, RDT, NT, V>), dim3((unsigned)((rows + ROWS - 1) / ROWS)),
+                           dim3(NT * ROWS), 0, stream, a);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 template <int DT, int RDT>
@@ -160,8 +170,12 @@ hipError_t launch(const NormArgs &a, hipStream_t stream)
         return launch_rows<DT, RDT, 64, 1>(a, stream);
     if (a.H <= 2048)
         return launch_rows<DT, RDT, 256, 1>(a, stream);
+    if (a.H <= 4096)
+        return launch_rows<DT, RDT, 512, 1>(a, stream);
     if (a.H <= 8192)
-        return launch_rows<DT, RDT, 256, 4>(a, stream);
+        return launch_rows<DT, RDT, 512, 2>(a, stream);
+    if (a.H <= 16384)
+        return launch_rows<DT, RDT, 1024, 2>(a, stream);
     return launch_rows<DT, RDT, 1024, 4>(a, stream);
 }
 

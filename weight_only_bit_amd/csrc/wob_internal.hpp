@@ -136,6 +136,7 @@ struct NormArgs {
     int64_t T;
     int H, quant;
     float alpha, eps;
+    int64_t row0 = 0; // the first row of this launch
 };
 hipError_t launch_residual_norm(const NormArgs &a, int dt, int residual_dt, hipStream_t stream);
 
