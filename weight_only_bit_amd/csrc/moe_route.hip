@@ -17,6 +17,7 @@
 // be chosen.
 #include "moe_choice.hpp"
 #include "weight_only_bit.h"
+#include "wob_rows.hpp"
 
 #include <type_traits>
 
@@ -67,31 +68,67 @@ __device__ __forceinline__ double recip_64(double d)
 
 constexpr double LOG2E = 1.44269504088896340736;
 
-__device__ __forceinline__ uint32_t lane_max(uint32_t a, uint32_t b) { return max(a, b); }
-
-// A double from lane ^ D of the group's lanes that hold equal values below D (see group_reduce).
+// From lane ^ D, where lanes whose numbers differ only below D hold the same (see group_reduce).
 template <int D>
 __device__ __forceinline__ uint32_t from_lane(uint32_t v)
 {
+    static_assert(D <= 8, "within a row of 16");
     if constexpr (D == 1)
         return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true);
     else if constexpr (D == 2)
         return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true);
     else if constexpr (D == 4)
         return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true);
-    else if constexpr (D == 8)
-        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true);
     else
-        return (uint32_t)__shfl_xor((int)v, D);
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true);
+}
+
+// v of both lanes that D tells apart, in an order that is the same in both.
+template <int D>
+__device__ __forceinline__ uint2 both_lanes(uint32_t v)
+{
+    if constexpr (D == 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return uint2{(uint32_t)p[0], (uint32_t)p[1]};
+    } else if constexpr (D == 32) {
+        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return uint2{(uint32_t)p[0], (uint32_t)p[1]};
+    } else {
+        return uint2{v, from_lane<D>(v)}; // (the order does not matter to the sums and maxima here)
+    }
+}
+
+// The largest of L lanes, in each of them.
+template <int L, int D = 1>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v)
+{
+    if constexpr (D < L) {
+        const uint2 p = both_lanes<D>(v);
+        return lanes_max<L, 2 * D>(max(p.x, p.y));
+    } else {
+        return v;
+    }
 }
 
 template <int L, int D = 1>
-__device__ __forceinline__ double group_sum64(double v)
+__device__ __forceinline__ float lanes_sum(float v)
+{
+    if constexpr (D < L) {
+        const uint2 p = both_lanes<D>(bitcast<uint32_t>(v));
+        return lanes_sum<L, 2 * D>(bitcast<float>(p.x) + bitcast<float>(p.y));
+    } else {
+        return v;
+    }
+}
+
+template <int L, int D = 1>
+__device__ __forceinline__ double lanes_sum64(double v)
 {
     if constexpr (D < L) {
         const uint64_t b = bitcast<uint64_t>(v);
-        const uint64_t o = (uint64_t)from_lane<D>((uint32_t)(b >> 32)) << 32 | from_lane<D>((uint32_t)b);
-        return group_sum64<L, 2 * D>(v + bitcast<double>(o));
+        const uint2 lo = both_lanes<D>((uint32_t)b), hi = both_lanes<D>((uint32_t)(b >> 32));
+        return lanes_sum64<L, 2 * D>(bitcast<double>((uint64_t)hi.x << 32 | lo.x) +
+                                     bitcast<double>((uint64_t)hi.y << 32 | lo.y));
     } else {
         return v;
     }
@@ -103,15 +140,15 @@ __device__ __forceinline__ void group_best2(uint32_t &first, uint32_t &second, i
 {
     if constexpr (D < L) {
         if (D < span) { // (uniform)
-            const uint32_t f = from_lane<D>(first), s = from_lane<D>(second);
-            second = max(min(first, f), max(second, s));
-            first = max(first, f);
+            const uint2 f = both_lanes<D>(first), s = both_lanes<D>(second);
+            second = max(min(f.x, f.y), max(s.x, s.y));
+            first = max(f.x, f.y);
             group_best2<L, 2 * D>(first, second, span);
         }
     }
 }
 
-// Eight lanes' worth of one token: the lowest lane of this lane's L for which `on` holds
+// The lowest lane of this lane's L for which `on` holds
 // (some lane does).
 template <int L>
 __device__ __forceinline__ int lowest_lane(bool on)
@@ -192,7 +229,7 @@ __global__ __launch_bounds__(route_threads<V>()) void moe_route_kernel(RouteArgs
 #pragma unroll
         for (int v = 0; v < V; ++v)
             k = max(k, order_key(l[v]));
-        const float top = order_value(group_reduce<L>(k, lane_max));
+        const float top = order_value(lanes_max<L>(k));
         double q[V], sum = 0.0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -200,7 +237,7 @@ __global__ __launch_bounds__(route_threads<V>()) void moe_route_kernel(RouteArgs
             q[v] = exp2_64(l[v] == top ? 0.0 : fmax(((double)l[v] - (double)top) * LOG2E, -1000.0));
             sum += q[v];
         }
-        const double r = recip_64(group_sum64<L>(sum)); // (1 or more; of a row without an expert nothing is used)
+        const double r = recip_64(lanes_sum64<L>(sum)); // (1 or more; of a row without an expert nothing is used)
 #pragma unroll
         for (int v = 0; v < V; ++v)
             p[v] = (float)(q[v] * r);
@@ -225,7 +262,7 @@ __global__ __launch_bounds__(route_threads<V>()) void moe_route_kernel(RouteArgs
             value = order_key(order_value(first) + order_value(second) + 0.f);
         bool kept = false;
         for (int i = 0; i < a.topk_groups; ++i) {
-            const uint32_t best = group_reduce<L>(value, lane_max);
+            const uint32_t best = lanes_max<L>(value);
             const bool take = best != 0u && lowest_lane<L>(value == best) / span == group;
             kept = kept || take;
             value = take ? 0u : value;
@@ -268,7 +305,7 @@ __global__ __launch_bounds__(route_threads<V>()) void moe_route_kernel(RouteArgs
 #pragma unroll
         for (int j = 0; j < PL; ++j)
             for (int i = 0; i < L && j * L + i < a.topk; ++i) {
-                const uint32_t best = group_reduce<L>(key[0], lane_max);
+                const uint32_t best = lanes_max<L>(key[0]);
                 const int owner = lowest_lane<L>(key[0] == best);
                 last_where = best == last && last_where >> 8 == owner ? last_where + 1 : owner << 8;
                 last = best;
@@ -323,9 +360,7 @@ __global__ __launch_bounds__(route_threads<V>()) void moe_route_kernel(RouteArgs
 #pragma unroll
         for (int j = 0; j < PL; ++j)
             total += s[j];
-        total = bitcast<float>(group_reduce<L>(bitcast<uint32_t>(total), [](uint32_t x, uint32_t y) {
-            return bitcast<uint32_t>(bitcast<float>(x) + bitcast<float>(y));
-        }));
+        total = lanes_sum<L>(total);
     }
 #pragma unroll
     for (int j = 0; j < PL; ++j) {
@@ -367,16 +402,20 @@ hipError_t launch_v(const RouteArgs &a, const RouteSplit &split, hipStream_t str
     return hipGetLastError();
 }
 
+// 16 lanes a token, or a whole wave where the tokens do not fill the CUs and a lane would have
+// more than four experts.  us, 16 lanes / 64: 256 experts in 8 groups, 1 token 5.9 / 4.7, 1024 7.1 /
+// 5.6, 2048 7.2 / 6.3, 4096 7.7 / 8.0, 16384 15.6 / 19.7; 160 in 8, 2048 tokens 6.3 / 5.7, 4096 6.7 / 7.2;
+// 64 in one, 1 token 3.1 / 3.5, 1024 3.4 / 3.9.
 template <int DT>
 hipError_t launch(const RouteArgs &a, hipStream_t stream)
 {
     const int size = a.E / a.groups;
     if (a.groups <= 16) {
         const RouteSplit s = split_of(16, a.groups, size);
-        if (s.run <= 16)
+        if (s.run <= (a.T <= 2048 ? 4 : 16))
             return launch_v<DT, 16, 2>(a, s, stream);
     }
-    return launch_v<DT, 64, 8>(a, split_of(64, a.groups, size), stream);
+    return launch_v<DT, 64, 2>(a, split_of(64, a.groups, size), stream);
 }
 
 } // namespace

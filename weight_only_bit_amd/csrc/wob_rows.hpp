@@ -74,6 +74,21 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v)
     return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true)); // 2,3,0,1
 }
 
+// f of v and lane ^ D's v for D = 16 and 32, where f does not mind the order of its operands: the
+// swap of two copies' halves leaves both halves' values in every lane, without the way through LDS.
+template <int D, class F>
+__device__ __forceinline__ uint32_t join_halves(uint32_t v, F f)
+{
+    static_assert(D == 16 || D == 32, "rows of 16 lanes or halves of a wave");
+    if constexpr (D == 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return f((uint32_t)p[0], (uint32_t)p[1]);
+    } else {
+        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return f((uint32_t)p[0], (uint32_t)p[1]);
+    }
+}
+
 // f over the NT threads that share a row, the result in every one of them.  NT = 64: a
 // wave; more: the waves' results meet in `part` (NT / 64 words of LDS that nothing else
 // is read from until the next barrier).
@@ -84,8 +99,8 @@ __device__ __forceinline__ uint32_t row_reduce(uint32_t v, uint32_t *part, F f)
     v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));  // lane ^ 2
     v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true)); // 7 - lane of 8
     v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true)); // 15 - lane of 16
-    v = f(v, (uint32_t)__shfl_xor((int)v, 16));
-    v = f(v, (uint32_t)__shfl_xor((int)v, 32));
+    v = join_halves<16>(v, f);
+    v = join_halves<32>(v, f);
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0)
             part[threadIdx.x >> 6] = v;
