@@ -15,6 +15,8 @@
 #include "wob_rows.hpp"
 #include "wob_tile.hpp"
 
+#include <math.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -39,15 +41,12 @@ __device__ __forceinline__ void store4(void *y, int ydt, size_t at, const float4
 }
 
 // Four sums of one row, scaled: binary32 steps in the order that the contract names.
-__device__ __forceinline__ float4_t scaled4(const i32x4 &sum, float xs, const float4_t &ws, const float4_t &bias,
-                                            bool biased)
+__device__ __forceinline__ float4_t scaled4(const i32x4 &sum, float xs, const float4_t &ws)
 {
     float4_t v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 4; ++e)
         v[e] = (float)sum[e] * xs * ws[e];
-        v[e] = biased ? v[e] + bias[e] : v[e];
-    }
     return v;
 }
 
@@ -71,21 +70,22 @@ inline size_t few_lds(int M, int K, int W, int G)
 }
 
 template <int W, int G>
-__global__ __launch_bounds__(64 * W * G) void int8_few_kernel(Int8GemmArgs a, int M, int N, int K)
+__global__ __launch_bounds__(64 * W * G) void int8_few_kernel(Int8GemmArgs a, int M, int N, int K,
+                                                             int rows)
 {
     constexpr int NT = 64 * W * G;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), k = wave % W, g = wave / W;
     const int KB = K >> 4, steps = (KB + 3) >> 2, pitch = few_pitch(K);
-    const int n0 = (blockIdx.x * G + g) * FR_ROWS;
+    const int n0 = blockIdx.x * rows + FR_ROWS * g, n_end = min((blockIdx.x + 1) * rows, N); // (rows <= FR_ROWS G)
 
     // Staging of x, 16 bytes a thread, the first round's loads ahead of the weights'.
     const int nx = M * KB;
     const u32x4 *xg = reinterpret_cast<const u32x4 *>(a.x);
     const u32x4 x_first = xg[min(tid, nx - 1)];
 
-    const u32x4 *wr = reinterpret_cast<const u32x4 *>(a.w) + (size_t)min(n0 + r, N - 1) * KB;
+    const u32x4 *wr = reinterpret_cast<const u32x4 *>(a.w) + (size_t)min(n0 + r, n_end - 1) * KB;
     const int mine = FR_CH * (((steps + FR_CH - 1) / FR_CH - k + W - 1) / W); // steps of this wave
     auto block = [&](int i) __attribute__((always_inline)) { // this lane's in step i
         return 4 * (FR_CH * (k + W * (i / FR_CH)) + i % FR_CH) + q;
@@ -151,25 +151,24 @@ __global__ __launch_bounds__(64 * W * G) void int8_few_kernel(Int8GemmArgs a, in
             acc += part[(wave + j) * 64 + lane];
     }
     const int n = n0 + 4 * q;
-    if (r < M && n < N) {
-        float4_t bias = {};
+    if (r < M && n < n_end) {
+        float4_t v = scaled4(acc, a.xs[r], *reinterpret_cast<const float4_t *>(a.ws + n));
         if (a.bias)
-            bias = *reinterpret_cast<const float4_t *>(a.bias + n);
-        store4(a.y, a.ydt, (size_t)r * N + n,
-               scaled4(acc, a.xs[r], *reinterpret_cast<const float4_t *>(a.ws + n), bias, a.bias != nullptr));
+            v += *reinterpret_cast<const float4_t *>(a.bias + n);
+        store4(a.y, a.ydt, (size_t)r * N + n, v);
     }
 }
 
 template <int W, int G>
-hipError_t launch_few(const Int8GemmArgs &a, int M, int N, int K, hipStream_t stream)
+hipError_t launch_few(const Int8GemmArgs &a, int M, int N, int K, int rows, hipStream_t stream)
 {
     auto kern = int8_few_kernel<W, G>;
     static std::atomic<uint64_t> lds_set{0};
     if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), 160 * 1024, lds_set);
         e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(kern, dim3((N + FR_ROWS * G - 1) / (FR_ROWS * G)), dim3(64 * W * G),
-                       few_lds(M, K, W, G), stream, a, M, N, K);
+    hipLaunchKernelGGL(kern, dim3((N + rows - 1) / rows), dim3(64 * W * G), few_lds(M, K, W, G), stream, a, M, N, K,
+                       rows);
     return hipGetLastError();
 }
 
@@ -213,16 +212,20 @@ struct Int8Tile {
 // 32 i + 8 g + 4 h + e, m = 32 k + r) and read back 16 bytes a lane, so a store covers
 // whole runs of a row.  The LDS serves a wave's accesses in order, and no other wave uses
 // this part.  RAW: the sums themselves, as one of the K parts.
-template <class T, int DT, bool RAW>
-__device__ __forceinline__ void store_wave(const i32x16 (&acc)[T::NB][T::MB], void *y, bool biased, int M, int N,
-                                           int nw, int mw, const float *ws, const float *bias, const float *xs,
-                                           uint8_t *stage)
+template <class T, int DT, bool RAW, bool BIAS>
+__device__ __forceinline__ void store_wave(const i32x16 (&acc)[T::NB][T::MB], void *y, int M, int N, int nw, int mw,
+                                           const float *ws, const float *bias, const float *xs, uint8_t *stage)
 {
     constexpr int ES = DT == DT_F32 ? 4 : 2, ROW = 32 * T::NB * ES, PITCH = ROW + 16;
     constexpr int VECS = ROW / 16, RPI = 64 / VECS; // 16-byte pieces of a row; rows per instruction
     static_assert(32 * PITCH <= T::WSTAGE && 64 % VECS == 0, "staging space");
     const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
     const int n = nw + lane % VECS * (16 / ES);
+    float4_t wv[4 * T::NB]; // scales of this lane's columns, for all its rows
+    if constexpr (!RAW)
+#pragma unroll
+        for (int i = 0; i < 4 * T::NB; ++i)
+            wv[i] = *reinterpret_cast<const float4_t *>(ws + 8 * i + 4 * h);
 #pragma unroll
     for (int k = 0; k < T::MB; ++k) {
         const float x = RAW ? 0.f : xs[32 * k + r];
@@ -242,8 +245,9 @@ __device__ __forceinline__ void store_wave(const i32x16 (&acc)[T::NB][T::MB], vo
                 if constexpr (RAW) {
                     *reinterpret_cast<i32x4 *>(to) = sum;
                 } else {
-                    const float4_t v = scaled4(sum, x, *reinterpret_cast<const float4_t *>(ws + at),
-                                               *reinterpret_cast<const float4_t *>(bias + at), biased);
+                    float4_t v = scaled4(sum, x, wv[4 * i + g]);
+                    if constexpr (BIAS)
+                        v += *reinterpret_cast<const float4_t *>(bias + at);
                     if constexpr (DT == DT_F32)
                         *reinterpret_cast<float4_t *>(to) = v;
                     else
@@ -475,8 +479,7 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
     uint8_t *const stage = smem + T::SCALES + wave * T::WSTAGE;
     const int nw = n0 + 32 * T::NB * wn, mw = m0 + 32 * T::MB * wm;
     if (raw) {
-        store_wave<T, DT_F32, true>(acc, part + (size_t)split * M * N, false, M, N, nw, mw, nullptr, nullptr, nullptr,
-                                    stage);
+        store_wave<T, DT_F32, true, false>(acc, part + (size_t)split * M * N, M, N, nw, mw, nullptr, nullptr, nullptr, stage);
         return;
     }
     if (tid < T::TN) {
@@ -487,12 +490,19 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
         sx[tid] = tile_xs;
     __syncthreads();
     const float *const pw = sws + 32 * T::NB * wn, *const pb = sb + 32 * T::NB * wn, *const px = sx + 32 * T::MB * wm;
-    if (a.ydt == DT_F32)
-        store_wave<T, DT_F32, false>(acc, a.y, a.bias != nullptr, M, N, nw, mw, pw, pb, px, stage);
-    else if (a.ydt == DT_F16)
-        store_wave<T, DT_F16, false>(acc, a.y, a.bias != nullptr, M, N, nw, mw, pw, pb, px, stage);
+    auto store = [&](auto biased) __attribute__((always_inline)) {
+        constexpr bool B = decltype(biased)::value;
+        if (a.ydt == DT_F32)
+            store_wave<T, DT_F32, false, B>(acc, a.y, M, N, nw, mw, pw, pb, px, stage);
+        else if (a.ydt == DT_F16)
+            store_wave<T, DT_F16, false, B>(acc, a.y, M, N, nw, mw, pw, pb, px, stage);
+        else
+            store_wave<T, DT_BF16, false, B>(acc, a.y, M, N, nw, mw, pw, pb, px, stage);
+    };
+    if (a.bias)
+        store(std::true_type{});
     else
-        store_wave<T, DT_BF16, false>(acc, a.y, a.bias != nullptr, M, N, nw, mw, pw, pb, px, stage);
+        store(std::false_type{});
 }
 
 // y from the sum of the K parts; n4 = N / 4.
@@ -521,7 +531,18 @@ __global__ __launch_bounds__(256) void int8_sum_kernel(Int8GemmArgs a, const i32
             if (s0 + j < splits)
                 v += p[j];
     }
-    store4(a.y, a.ydt, (size_t)i * 4, scaled4(v, xs, ws, bias, a.bias != nullptr));
+    float4_t y = scaled4(v, xs, ws);
+    if (a.bias)
+        y += bias;
+    store4(a.y, a.ydt, (size_t)i * 4, y);
+}
+
+hipError_t launch_sum(const Int8GemmArgs &a, const int *part, int M, int N, int splits, hipStream_t stream)
+{
+    const int64_t total4 = (int64_t)M * N / 4;
+    hipLaunchKernelGGL(int8_sum_kernel, dim3((unsigned)((total4 + 255) / 256)), dim3(256), 0, stream, a,
+                       reinterpret_cast<const i32x4 *>(part), total4, N / 4, splits);
+    return hipGetLastError();
 }
 
 template <class T>
@@ -541,60 +562,88 @@ hipError_t launch_tile(const Int8GemmArgs &a, int M, int N, int K, int splits, v
     int *part = static_cast<int *>(workspace);
     hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), (size_t)T::LDS, stream, a, part, M, N, K, tiles_m,
                        (int)tiles, splits, nxcd);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || splits == 1)
-        return e;
-    const int64_t total4 = (int64_t)M * N / 4;
-    hipLaunchKernelGGL(int8_sum_kernel, dim3((unsigned)((total4 + 255) / 256)), dim3(256), 0, stream, a,
-                       reinterpret_cast<const i32x4 *>(part), total4, N / 4, splits);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || splits == 1 ? e : launch_sum(a, part, M, N, splits, stream);
 }
 
-using TileL = Int8Tile<2, 4, 4, 2, 5>; // 256 x 256
-using TileM = Int8Tile<2, 2, 2, 2, 6>; // 128 x 128
-using TileS = Int8Tile<2, 1, 2, 2, 6>; // 64 weight rows x 128 activation rows
-using TileN = Int8Tile<2, 1, 1, 2, 6>; // 64 x 64
+using TileL = Int8Tile<2, 4, 4, 2, 5>;  // 256 x 256
+using TileW = Int8Tile<4, 2, 4, 2, 6>;  // 256 weight rows x 128 activation rows
+using TileM = Int8Tile<2, 2, 2, 2, 8>;  // 128 x 128
+using TileS = Int8Tile<2, 1, 2, 2, 12>; // 64 weight rows x 128 activation rows
+using TileN = Int8Tile<2, 1, 1, 2, 10>; // 64 x 64
 
-bool few_rows(int64_t M, int64_t K) { return M <= 16 && M * few_pitch((int)K) <= 80 * 1024; }
-enum class Path { Few, Large, Medium, Small, Narrow };
+// ---- Choice ----------------------------------------------------------------
+//
+// The form and its K parts are the ones with the smallest estimate, in us, which is linear in
+// what was measured (graph replays over copies larger than the caches, 618 pairs of a shape
+// and a form, M 1 to 1536, N x K of 1024 x 8192 to 43008 x 5376):
+//   tiles: rounds of 256 workgroups, each `start` and `per_k` a 1000 k of a part, the latter a fifth
+//          less on an empty card;
+//   parts: their sum's launch and its bytes;
+//   few rows: the weights' bytes and the staging of x by a CU's workgroups.
+// On average the choice is 0.2 % slower than the best form measured from 20 rows on, and 2 %
+// below; at worst 17 % (16 x 4096 x 4096, 10.5 us, 9.0 with four parts of the 64 x 64 tile).  Best
+// and next form, us: 2048 x 5376 x 5376 256 x 256 67, 256 x 128 78; 512 x 16384 x 5376 256 x 128 50,
+// 128 x 128 63; 200 x 16384 x 5376 128 x 128 34, 64 x 128 37; 100 x 16384 x 5376 64 x 128 27, 64 x 64
+// 30; 64 x 16384 x 5376 64 x 64 24, 64 x 128 26; 96 x 5376 x 21504 256 x 128 in 8 parts 35.9, 128 x 128
+// in 6 36.3; 13 x 5760 x 2880 few rows 7.0, 64 x 64 9.5; 2 x 5376 x 21504 64 x 64 in 3 parts 24.6, few
+// rows 27.
+enum class Path { Few, Large, Wide, Medium, Small, Narrow };
 
 struct Plan {
     Path path;
-    int splits;
+    int splits; // Few: weight rows of a workgroup
 };
 
-template <class T>
-int64_t tile_count(int64_t M, int64_t N) { return ((M + T::TM - 1) / T::TM) * ((N + T::TN - 1) / T::TN); }
+struct TileCost {
+    Path path;
+    int tn, tm;
+    float start, per_k;
+};
+constexpr TileCost TILE_COSTS[] = {
+    {Path::Large, TileL::TN, TileL::TM, 20.f, 10.f}, {Path::Wide, TileW::TN, TileW::TM, 12.f, 7.f},
+    {Path::Medium, TileM::TN, TileM::TM, 9.f, 4.6f}, {Path::Small, TileS::TN, TileS::TM, 7.f, 3.5f},
+    {Path::Narrow, TileN::TN, TileN::TM, 5.5f, 2.6f},
+};
+constexpr int MOST_PARTS = 16, PART_K = 512; // parts, at most; k of a part, at least
 
-// K parts for `tiles` tiles so that up to one workgroup reaches each CU, in units of 256 k.
-int k_parts(int64_t tiles, int64_t K)
+// Weight rows of a workgroup so that every CU gets the same number of them: 8 to 32 (1 x 5376 x
+// 21504 24 rows, 224 workgroups, 26 us; 32 28, 16 30).
+int few_block(int64_t N)
 {
-    const int64_t spans = (K + 255) / 256;
-    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({256 / tiles, spans / 2, 16}));
-    return spans - (spans + parts - 1) / parts >= 5 ? (int)parts : 1;
-}
-
-bool large_tile(int64_t M, int64_t N)
-{
-    const int64_t large = (tile_count<TileL>(M, N) + 255) / 256, medium = (tile_count<TileM>(M, N) + 255) / 256;
-    return 2 * medium >= 5 * large;
+    for (int64_t per = 1;; ++per) {
+        const int64_t rows = 8 * ((N + 2048 * per - 1) / (2048 * per));
+        if (rows <= 2 * FR_ROWS)
+            return (int)rows;
+    }
 }
 
 Plan plan(int64_t M, int64_t N, int64_t K)
 {
-    if (few_rows(M, K))
-        return {Path::Few, 1};
-    if (large_tile(M, N))
-        return {Path::Large, 1};
-    const int64_t spans = (K + 255) / 256;
-    const int small = k_parts(tile_count<TileS>(M, N), K);
-    const int64_t medium = tile_count<TileM>(M, N);
-    const bool fills = tile_count<TileS>(M, N) > 256 && (medium <= 256 || medium > 384);
-    if (M > 64 && (spans > 11 * (int64_t)small || fills))
-        return {Path::Medium, k_parts(medium, K)};
-    if (M <= 64)
-        return {Path::Narrow, k_parts(tile_count<TileN>(M, N), K)};
-    return {Path::Small, small};
+    Plan best = {Path::Narrow, 1};
+    float least = INFINITY;
+    for (const TileCost &t : TILE_COSTS) {
+        const int64_t tiles = ((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn);
+        const int64_t most = std::min<int64_t>({256 / tiles, K / PART_K, MOST_PARTS});
+        for (int64_t parts = 1; parts == 1 || parts <= most; ++parts) {
+            const int64_t rounds = (tiles * parts + 255) / 256, k = (K + parts - 1) / parts;
+            const float busy = (float)(tiles * parts) / (float)(256 * rounds);
+            float us = (float)rounds * (t.start + t.per_k * 1e-3f * (float)k * (0.8f + 0.2f * busy));
+            if (parts > 1)
+                us += 2.5f + 0.3f * ((float)parts + 0.5f) * (float)(M * N) * 4e-6f;
+            if (us < least) {
+                least = us;
+                best = {t.path, (int)parts};
+            }
+        }
+    }
+    if (M <= 16 && M * few_pitch((int)K) <= 80 * 1024) { // x leaves the LDS room for a second workgroup
+        const int rows = few_block(N);
+        const int64_t per_cu = ((N + rows - 1) / rows + 255) / 256;
+        if (3.0f + 0.18e-6f * (float)(N * K) + 0.04e-3f * (float)(M * K * per_cu) < least)
+            best = {Path::Few, rows};
+    }
+    return best;
 }
 
 } // namespace
@@ -604,27 +653,32 @@ size_t int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K)
     if (M == 0 || N == 0)
         return 0;
     const Plan p = plan(M, N, K);
-    return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(int) : 0;
+    return p.path != Path::Few && p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(int) : 0;
 }
 
 hipError_t launch_int8_gemm(const Int8GemmArgs &a, int M, int N, int K, void *workspace, hipStream_t stream)
 {
     const Plan p = plan(M, N, K);
-    if (p.path == Path::Few) {
-        const int groups = (N + FR_ROWS - 1) / FR_ROWS;
-        if (groups > 256 && (K >= 2048 || (K > 1024 && M > 8)))
-            return launch_few<8, 2>(a, M, N, K, stream);
-        if (K >= 2048)
-            return launch_few<8, 1>(a, M, N, K, stream);
-        return launch_few<4, 1>(a, M, N, K, stream);
-    }
-    if (p.path == Path::Large)
-        return launch_tile<TileL>(a, M, N, K, 1, workspace, stream);
-    if (p.path == Path::Medium)
+    switch (p.path) {
+    case Path::Few:
+        // Two groups of 16 rows, of eight waves each (one or two rows of x: four, 1 x 5376 x 21504 25.7 us
+        // and 26.3, but 4 x 5376 x 5376 9.5 and 9.3), or one, of eight (M K up to 4096: four, 1 x 4096 x
+        // 4096 5.9 and 6.6, but 2 x 4096 x 4096 6.8 and 6.6).
+        if (p.splits > FR_ROWS)
+            return M <= 2 ? launch_few<4, 2>(a, M, N, K, p.splits, stream) : launch_few<8, 2>(a, M, N, K, p.splits, stream);
+        return M * K <= 4096 ? launch_few<4, 1>(a, M, N, K, p.splits, stream)
+                             : launch_few<8, 1>(a, M, N, K, p.splits, stream);
+    case Path::Large:
+        return launch_tile<TileL>(a, M, N, K, p.splits, workspace, stream);
+    case Path::Wide:
+        return launch_tile<TileW>(a, M, N, K, p.splits, workspace, stream);
+    case Path::Medium:
         return launch_tile<TileM>(a, M, N, K, p.splits, workspace, stream);
-    if (p.path == Path::Narrow)
+    case Path::Small:
+        return launch_tile<TileS>(a, M, N, K, p.splits, workspace, stream);
+    default:
         return launch_tile<TileN>(a, M, N, K, p.splits, workspace, stream);
-    return launch_tile<TileS>(a, M, N, K, p.splits, workspace, stream);
+    }
 }
 
 } // namespace wob
