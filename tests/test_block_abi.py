@@ -93,6 +93,9 @@ def test_residual_norm_refusals(L):
                 dict(gate=F.odd), dict(w=F.odd), dict(n=F.odd), dict(out=F.odd), dict(quant=1, ns=F.odd)):
         assert r(**bad) == L.INVALID_ARG, bad
     assert r(T=0) == L.OK and r(T=0, w=None, n=None) == L.OK
+    # tensors without rows have no address
+    assert r(T=0, y=None, post=F.p, gate=F.p, res=None, out=None, n=None, quant=2) == L.OK
+    assert r(T=0, H=60) == L.INVALID_ARG and r(T=0, dt=2) == L.DTYPE
 
 
 def test_moe_route_refusals(L):
@@ -154,8 +157,10 @@ def test_residual_norm_binding_checks(wob):
                         ((None, y, w), dict(post_weight=w), "without y"),
                         ((None, y, w), dict(residual_out=y), "without y"),
                         ((y, y, None), dict(quant=1), "without weight"), ((y, y, w), dict(quant=5), "quant"),
-                        ((y, y, w), dict(out_scale=w), "out_scale"), ((y.t(), y.t(), w), {}, "weight|H="),
+                        ((y, y, w), dict(out_scale=w), "out_scale"), ((y.t(), y.t(), w), {}, "contiguous"),
                         ((y[:, :48].contiguous(), y[:, :48].contiguous(), w[:48]), dict(quant=2), "multiple of 32"),
+                        ((y, y, w), dict(eps=-1.0), "eps"), ((y, y, w), dict(eps=float("nan")), "eps"),
+                        ((y, y, w), dict(alpha=float("inf")), "alpha"),
                         ((y, y, w), dict(out=y[:2]), "out"), ((y, y, w), {}, "device")):
         with pytest.raises(ValueError, match=word):
             wob.residual_norm(*a, **kw)

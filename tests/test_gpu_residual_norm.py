@@ -209,3 +209,7 @@ def test_empty(wob):
     d = inputs(2, 64, "bf16", "fp32", 2)
     n, h = wob.residual_norm(d["y"][:0], d["r"][:0], d["w"])
     assert n.shape == (0, 64) and h.shape == (0, 64) and h.dtype == torch.float32
+    for quant, width in ((wob.QUANT_INT8, 64), (wob.QUANT_MXFP4, 32)):
+        c, s, h = wob.residual_norm(d["y"][:0], d["r"][:0], d["w"], post_weight=d["post"], gate=d["rows"][:0], quant=quant)
+        assert c.shape == (0, width) and s.shape[0] == 0 and h.shape == (0, 64)
+    assert wob.residual_norm(None, d["r"][:0], d["w"])[0].shape == (0, 64)

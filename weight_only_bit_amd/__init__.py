@@ -23,6 +23,7 @@ Layouts are those of ``include/weight_only_bit.h``.
 from __future__ import annotations
 
 import functools
+import math
 
 from . import _lib
 from ._lib import (ACT_NONE, ACT_SILU_MUL, BF16, DTYPE, F16, F32, INVALID_ARG, OK, PATH_AUTO,
@@ -446,6 +447,22 @@ def mxfp4_moe_layer(x, logits, topk: int, w1_fp4, w1_scale, w2_fp4, w2_scale, bi
     return out
 
 
+def _operand(t, name, shape, dtypes, index):
+    """_want, and t is contiguous and lives where the call's first operand does (index: its
+    get_device(), below 0 for the host, which the caller refuses once all shapes are right)."""
+    if t is None or t.shape != shape or t.dtype not in dtypes:
+        _want(t, name, shape, dtypes)
+    if not t.is_contiguous():
+        raise ValueError("all operands must be contiguous")
+    if t.get_device() != index:
+        raise ValueError("operands live on different devices")
+
+
+def _on_device(index):
+    if index < 0:
+        raise ValueError("all operands must be device tensors")
+
+
 def _row_count(lead):
     R = 1
     for n in lead:
@@ -464,6 +481,15 @@ def _row_stride(x, name):
     raise ValueError(f"{name} must be contiguous, or a 2-D column slice of a contiguous tensor")
 
 
+def _rows_like(t, name, shape, dtypes, index):
+    """_operand for rows that may be a column slice; elements from one row to the next."""
+    if t.shape != shape or t.dtype not in dtypes:
+        _want(t, name, shape, dtypes)
+    if t.get_device() != index:
+        raise ValueError("operands live on different devices")
+    return _row_stride(t, name)
+
+
 def int8_quantize(x, act: int = ACT_NONE, out=None, out_scale=None):
     """Rows in 8 bits: x [..., K] fp16/bf16/fp32 -> (codes [..., K] int8, scale [...]
     float32), scale = amax / 127 of each row, the operands of int8_gemm.  act=ACT_SILU_MUL:
@@ -473,7 +499,8 @@ def int8_quantize(x, act: int = ACT_NONE, out=None, out_scale=None):
     torch = _torch()
     if x.dim() < 1:
         raise ValueError("x must be [..., K]")
-    _want(x, "x", x.shape, _values)
+    if x.dtype not in _values:
+        _want(x, "x", x.shape, _values)
     if act not in (ACT_NONE, ACT_SILU_MUL):
         raise ValueError(f"unknown activation {act}")
     K = x.shape[-1]
@@ -483,13 +510,12 @@ def int8_quantize(x, act: int = ACT_NONE, out=None, out_scale=None):
         K //= 2
     if not 16 <= K <= 65536 or K % 16 != 0:
         raise ValueError(f"K={K} must be a multiple of 16, up to 65536")
-    lead = x.shape[:-1]
+    lead = tuple(x.shape[:-1])
     ldx = _row_stride(x, "x")
+    _on_device(x.get_device())
     dev = x.device
     out = _output(out, "out", (*lead, K), torch.int8, dev)
-    out_scale = _output(out_scale, "out_scale", tuple(lead), torch.float32, dev)
-    if x.get_device() < 0:
-        raise ValueError("all operands must be device tensors")
+    out_scale = _output(out_scale, "out_scale", lead, torch.float32, dev)
     st = _run(_lib.lib().int8_quantize, dev, x.data_ptr(), _tags[x.dtype], ldx, act, out.data_ptr(),
               out_scale.data_ptr(), _row_count(lead), K)
     _lib.check(st, "int8_quantize")
@@ -502,18 +528,20 @@ def int8_dequant(codes, scale, out_dtype=None, out=None):
     torch = _torch()
     if codes.dim() < 1:
         raise ValueError("codes must be [..., K]")
-    _want(codes, "codes", codes.shape, _int8)
-    lead, K = codes.shape[:-1], codes.shape[-1]
+    shape = tuple(codes.shape)
+    lead, K = shape[:-1], shape[-1]
+    index = codes.get_device()
+    _operand(codes, "codes", shape, _int8, index)
     if not 16 <= K <= 65536 or K % 16 != 0:
         raise ValueError(f"K={K} must be a multiple of 16, up to 65536")
-    _want(scale, "scale", lead, _fp32)
+    _operand(scale, "scale", lead, _fp32, index)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
     if out_dtype not in _values:
         raise TypeError(f"out_dtype {out_dtype} must be float16, bfloat16 or float32")
+    _on_device(index)
     dev = codes.device
-    out = _output(out, "out", tuple(codes.shape), out_dtype, dev)
-    _check_device(codes, scale)
+    out = _output(out, "out", shape, out_dtype, dev)
     st = _run(_lib.lib().int8_dequant, dev, codes.data_ptr(), scale.data_ptr(), out.data_ptr(),
               _tags[out_dtype], _row_count(lead), K)
     _lib.check(st, "int8_dequant")
@@ -536,20 +564,23 @@ def int8_gemm(x_q, x_scale, w_q, w_scale, bias=None, out=None, out_dtype=None, w
         raise ValueError("x_q must be [M, K] and w_q [N, K]")
     M, K = x_q.shape
     N = w_q.shape[0]
-    _want(x_q, "x_q", (M, K), _int8)
-    _want(x_scale, "x_scale", (M,), _fp32)
-    _want(w_q, "w_q", (N, K), _int8)
-    _want(w_scale, "w_scale", (N,), _fp32)
+    index = x_q.get_device()
+    _operand(x_q, "x_q", (M, K), _int8, index)
+    _operand(x_scale, "x_scale", (M,), _fp32, index)
+    _operand(w_q, "w_q", (N, K), _int8, index)
+    _operand(w_scale, "w_scale", (N,), _fp32, index)
     if bias is not None:
-        _want(bias, "bias", (N,), _fp32)
+        _operand(bias, "bias", (N,), _fp32, index)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
     if out_dtype not in _values:
         raise TypeError(f"out_dtype {out_dtype} must be float16, bfloat16 or float32")
     dev = x_q.device
     out = _output(out, "out", (M, N), out_dtype, dev)
+    _on_device(index)
     workspace, ws_bytes = _workspace(workspace, int8_gemm_workspace_size(M, N, K), dev)
-    _check_device(x_q, x_scale, w_q, w_scale, bias, workspace)
+    if workspace is not None:
+        _check_device(workspace, x_q)
     st = _run(_lib.lib().int8_gemm, dev, x_q.data_ptr(), x_scale.data_ptr(), w_q.data_ptr(),
               w_scale.data_ptr(), _ptr(bias), out.data_ptr(), _tags[out_dtype], M, N, K,
               _ptr(workspace), ws_bytes)
@@ -574,37 +605,35 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: float
     torch = _torch()
     if residual.dim() != 2:
         raise ValueError("residual must be [T, H]")
-    T, H = residual.shape
+    T, H = shape = tuple(residual.shape)
     block = y if y is not None else weight
     if block is None:
         raise ValueError("y and weight are both missing: there is nothing to compute")
-    dt = block.dtype
+    dt, rdt = block.dtype, residual.dtype
     if dt not in _values:
         raise TypeError(f"dtype {dt} must be float16, bfloat16 or float32")
-    own, shape = (dt,), (T, H)
-    _want(residual, "residual", shape, (dt, torch.float32))
+    own = (dt,)
+    index, dev = residual.get_device(), residual.device
+    _operand(residual, "residual", shape, own if rdt == dt else _fp32, index)
     if quant not in (QUANT_NONE, QUANT_INT8, QUANT_MXFP4):
         raise ValueError(f"unknown quant {quant}")
     whole = 32 if quant == QUANT_MXFP4 else 16 if quant == QUANT_INT8 else 8
     if not whole <= H <= 32768 or H % whole != 0:
         raise ValueError(f"H={H} must be a multiple of {whole}, up to 32768")
+    if not (math.isfinite(alpha) and math.isfinite(eps) and eps >= 0):
+        raise ValueError(f"alpha={alpha} must be finite, eps={eps} finite and not negative")
     ldy = ldg = 0
-    dev = residual.device
     if y is not None:
-        _want(y, "y", shape, own)
-        ldy = _row_stride(y, "y")
+        ldy = _rows_like(y, "y", shape, own, index)
         if post_weight is not None:
-            _want(post_weight, "post_weight", (H,), own)
+            _operand(post_weight, "post_weight", (H,), own, index)
         if gate is not None:
             if gate.dim() == 1:
-                _want(gate, "gate", (H,), own)
-                if not gate.is_contiguous():
-                    raise ValueError("gate [H] must be contiguous")
+                _operand(gate, "gate", (H,), own, index)
             else:
-                _want(gate, "gate", shape, own)
-                ldg = _row_stride(gate, "gate")
+                ldg = _rows_like(gate, "gate", shape, own, index)
         if residual_out is not residual:
-            residual_out = _output(residual_out, "residual_out", shape, residual.dtype, dev)
+            residual_out = _output(residual_out, "residual_out", shape, rdt, dev)
     elif post_weight is not None or gate is not None:
         raise ValueError("without y there is no post_weight and no gate")
     elif residual_out is not None:
@@ -613,7 +642,7 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: float
         if quant != QUANT_NONE or out is not None or out_scale is not None:
             raise ValueError("without weight there are no normed rows")
     else:
-        _want(weight, "weight", (H,), own)
+        _operand(weight, "weight", (H,), own, index)
         if quant == QUANT_NONE:
             if out_scale is not None:
                 raise ValueError("out_scale without quantised rows")
@@ -624,12 +653,9 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: float
         else:
             out = _output(out, "out", (T, H // 2), torch.uint8, dev)
             out_scale = _output(out_scale, "out_scale", (T, H // 32), torch.uint8, dev)
-    _check_device(residual, weight, post_weight)
-    for t in (y, gate):  # these may be column slices
-        if t is not None and t.device != dev:
-            raise ValueError("operands live on different devices")
+    _on_device(index)
     st = _run(_lib.lib().residual_norm, dev, _ptr(y), _tags[dt], ldy, residual.data_ptr(),
-              _tags[residual.dtype], _ptr(post_weight), _ptr(gate), ldg, alpha, _ptr(weight), eps,
+              _tags[rdt], _ptr(post_weight), _ptr(gate), ldg, alpha, _ptr(weight), eps,
               quant, _ptr(out), _ptr(out_scale), _ptr(residual_out), T, H)
     _lib.check(st, "residual_norm")
     h = residual if y is None else residual_out
@@ -648,8 +674,9 @@ def moe_route(logits, topk: int, bias=None, score: int = SCORE_SIGMOID, groups: 
     torch = _torch()
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
-    _want(logits, "logits", logits.shape, _values)
-    T, E = logits.shape
+    T, E = shape = tuple(logits.shape)
+    index = logits.get_device()
+    _operand(logits, "logits", shape, _values, index)
     if score not in (SCORE_SIGMOID, SCORE_SOFTMAX):
         raise ValueError(f"unknown score {score}")
     if not 1 <= groups <= 64 or not 1 <= E <= 1024 or E % groups != 0:
@@ -661,11 +688,11 @@ def moe_route(logits, topk: int, bias=None, score: int = SCORE_SIGMOID, groups: 
     if group_top not in (1, 2):
         raise ValueError(f"group_top={group_top} must be 1 or 2")
     if bias is not None:
-        _want(bias, "bias", (E,), _fp32)
+        _operand(bias, "bias", (E,), _fp32, index)
     dev = logits.device
     ids = _output(ids, "ids", (T, topk), torch.int32, dev)
     weights = _output(weights, "weights", (T, topk), torch.float32, dev)
-    _check_device(logits, bias)
+    _on_device(index)
     st = _run(_lib.lib().moe_route, dev, logits.data_ptr(), _tags[logits.dtype], _ptr(bias),
               ids.data_ptr(), weights.data_ptr(), T, E, topk, score, groups, topk_groups, group_top,
               1 if renormalize else 0, scale)

@@ -732,10 +732,6 @@ int residual_norm(const void *y, int dtype, int64_t ldy, const void *residual, i
         return fail(WOB_INVALID_ARG, "shape too large");
     if (!(eps >= 0.0f) || !isfinite(eps) || !isfinite(alpha))
         return fail(WOB_INVALID_ARG, "eps must be finite and not negative, alpha finite");
-    if (!y && (post_weight || gate || !weight))
-        return fail(WOB_INVALID_ARG, "without y there is no post_weight and no gate, and weight is required");
-    if (!weight && (quant != WOB_QUANT_NONE || n || n_scale))
-        return fail(WOB_INVALID_ARG, "without weight there are no normed rows");
     if (y && !row_stride(ldy, H, dtype))
         return fail(WOB_INVALID_ARG, "row stride %lld of y is below H=%lld, too large or leaves rows unaligned",
                     (long long)ldy, (long long)H);
@@ -744,8 +740,12 @@ int residual_norm(const void *y, int dtype, int64_t ldy, const void *residual, i
                     (long long)ldg, (long long)H);
     if (T && ((y && ldy > ((int64_t)1 << 60) / T) || (gate && ldg > ((int64_t)1 << 60) / T)))
         return fail(WOB_INVALID_ARG, "shape too large");
-    if (T == 0)
+    if (T == 0) // (operands without elements may have no address, so which ones are there does not show)
         return ok();
+    if (!y && (post_weight || gate || !weight))
+        return fail(WOB_INVALID_ARG, "without y there is no post_weight and no gate, and weight is required");
+    if (!weight && (quant != WOB_QUANT_NONE || n || n_scale))
+        return fail(WOB_INVALID_ARG, "without weight there are no normed rows");
     if (!residual || (y && !residual_out) || (weight && !n) || (quant != WOB_QUANT_NONE && !n_scale))
         return fail(WOB_INVALID_ARG, "null operand pointer");
     if (quant == WOB_QUANT_NONE && n_scale)
