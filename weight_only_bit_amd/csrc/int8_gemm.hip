@@ -58,6 +58,10 @@ __device__ __forceinline__ float4_t scaled4(const i32x4 &sum, float xs, const fl
 // LDS.  A workgroup has G such groups of rows.  The weights go from memory into registers,
 // FR_D loads of a lane ahead; only x passes through LDS (pitch 16 mod 128 bytes, which makes
 // its reads conflict-free), with its loads ahead of the weights' so that they land first.
+//
+// Bound by the weights' bytes: 1 x 16384 x 5376 (88 MB) 17.8 us, a plain read of as many bytes 15.2;
+// 1 x 43008 x 5376 (231 MB) 43.2, a read 33.5; 13 x 5760 x 2880 (17 MB) 7.0, a read 3.9 (graph
+// replays over copies larger than the caches).
 constexpr int FR_ROWS = 16;
 constexpr int FR_D = 6;  // loads ahead
 constexpr int FR_CH = 2; // neighbouring steps of a wave
@@ -191,6 +195,19 @@ hipError_t launch_few(const Int8GemmArgs &a, int M, int N, int K, int rows, hipS
 // places (every wave has its last operands in registers), and the last step reads group
 // g + 1's first operands and starts the copies into group g's places while it multiplies;
 // the steps of group g + 1 go on with them.
+//
+// Copies cost one cache look-up a row and instruction, so whole lines (GS = 2) are copied, and the
+// 256 x 256 tile, of which two groups fit, gets half a third.  2048 x 16384 x 5376, us: four groups of
+// 64 bytes a row 175 to 191, five 179, two of 128 bytes 174 to 187, two and a half 158 to 160.  The
+// other tiles are bound by bytes, and by how many are under way: 32 x 5376 x 21504 three groups a
+// part 35.0, five 25.8, eight 26.2; 100 x 5376 x 21504 in the 128 x 128 tile three 33 to 34.5, four 31.8 to
+// 32.9, five 33.2 to 34.8.
+//
+// 2048 x 16384 x 5376, 150 to 165 us (2.2 to 2.4 POPS; the library's product of the operands without
+// scales 164): the power limit.  MFMA busy 63 % at 1.7 GHz; with zero codes, which switch nothing,
+// the same launches take 117, and an order of reads and copies that takes 4 off that takes
+// nothing off this.  Timing-only forms: no stores 148 to 158, no copies 142 to 149, neither 121 to
+// 127, the MFMAs alone, from registers, 108 (72 at 2.4 GHz).
 template <int WN_, int NB_, int MB_, int GS_, int NH_>
 struct Int8Tile {
     static constexpr int WN = WN_, WM = 4 / WN_, NB = NB_, MB = MB_, GS = GS_, NH = NH_;
@@ -211,7 +228,8 @@ struct Int8Tile {
 // time: rows of 32 NB n are written as the accumulators hold them (acc[i][k][4 g + e] is n =
 // 32 i + 8 g + 4 h + e, m = 32 k + r) and read back 16 bytes a lane, so a store covers
 // whole runs of a row.  The LDS serves a wave's accesses in order, and no other wave uses
-// this part.  RAW: the sums themselves, as one of the K parts.
+// this part.  RAW: the sums themselves, as one of the K parts.  (The columns' scales in registers:
+// 2048 x 16384 x 5376 with zero codes 122 us to 117.)
 template <class T, int DT, bool RAW, bool BIAS>
 __device__ __forceinline__ void store_wave(const i32x16 (&acc)[T::NB][T::MB], void *y, int M, int N, int nw, int mw,
                                            const float *ws, const float *bias, const float *xs, uint8_t *stage)
@@ -505,7 +523,8 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
         store(std::false_type{});
 }
 
-// y from the sum of the K parts; n4 = N / 4.
+// y from the sum of the K parts; n4 = N / 4.  100 x 5376 in six parts 4.5 us (14 MB; all parts loaded
+// at once instead of four at a time 4.5).
 __global__ __launch_bounds__(256) void int8_sum_kernel(Int8GemmArgs a, const i32x4 *__restrict__ part, int64_t total4,
                                                        int n4, int splits)
 {

@@ -119,6 +119,7 @@ hipError_t launch(const void *x, int64_t ldx, int8_t *codes, float *scale, int64
     return launch_rows<DT, ACT, 1024, 8>(x, ldx, codes, scale, R, K, stream);
 }
 
+// Eight elements a thread: 2048 x 21504 into bf16 (132 MB) 20 us, 6.5 TB/s.
 template <int DT>
 __global__ __launch_bounds__(256) void int8_dequant_kernel(const uint2 *__restrict__ codes,
                                                            const float *__restrict__ scale,

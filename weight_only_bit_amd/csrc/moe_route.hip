@@ -15,6 +15,12 @@
 // ascend with (lane, register) and a group's best two meet by cross-lane operands within
 // its lanes.  c is held as an unsigned key of the same order, 0 for an expert that cannot
 // be chosen.
+//
+// Bound by the vector ALU: 16384 tokens of 256 experts 14.4 us (17 MB, a read of which takes 3.9),
+// about 1000 operations of four tokens, 420 of them the 64-bit scores; 4096 of 160 6.8; one
+// token 3.8, the chain of its places.  A wave a token with library exponentials and divisions, groups
+// through LDS and the places searched in all registers 27 us, four tokens a wave 16.2, sorted lists
+// 13.9 to 14.4.
 #include "moe_choice.hpp"
 #include "weight_only_bit.h"
 #include "wob_rows.hpp"
