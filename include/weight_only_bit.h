@@ -451,8 +451,8 @@ int residual_norm(const void *y, int dtype, int64_t ldy, const void *residual, i
  * Group-limited choice of experts.  For each of T tokens, with E experts in `groups`
  * groups of E / groups consecutive ones:
  *   s_e = 1 / (1 + e^-l_e) (WOB_SCORE_SIGMOID), or exp(l_e - max l) / sum exp(l - max l)
- *         (WOB_SCORE_SOFTMAX, over all experts), rounded correctly to fp32 (but for
- *         one value in about 2^28, which may be its neighbour)
+ *         (WOB_SCORE_SOFTMAX, over all experts), rounded to the nearest fp32 (but for
+ *         one value in 2^23 or fewer, which may be the nearest's neighbour)
  *   c_e = s_e + bias_e in fp32 (bias NULL: s_e); it decides the choice alone
  *   kept groups: the topk_groups with the largest value, the value being the sum (fp32)
  *         of the group's group_top (1 or 2) largest c; ties to the lowest group

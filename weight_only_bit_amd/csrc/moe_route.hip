@@ -6,9 +6,10 @@
 //     ids: the topk largest c of the kept groups, ties to the lowest index
 //     weights = scale * s (over the sum of the chosen s)
 //
-// s is formed in 64 bits and rounded once to binary32, so c, and with it the order, is a
-// function of the scores that does not depend on how an exponential is approximated: two
-// experts whose c differ in the last place are ordered the same everywhere.
+// s is formed in 64 bits, to 2^-48 of its value, and rounded once to binary32, so c, and with it
+// the order, is a function of the scores that does not depend on how an exponential is
+// approximated: two experts whose c differ in the last place are ordered the same everywhere.
+// (An error of 2^-48 moves the rounding of one value in 2^23 at most.)
 //
 // L lanes share a token (16 of them: four tokens a wave).  A group has `span` of them, a
 // power of two, and each holds a run of consecutive experts in V registers, so experts
@@ -39,36 +40,28 @@ struct RouteSplit { // how a token's experts lie in its lanes
     int span, run;  // lanes of a group, experts of a lane
 };
 
-// 2^x for |x| <= 1000: n = round(x), f = x - n in [-1/2, 1/2], the series of exp(f ln 2) up to
-// f^11 (the rest is below 2^-46 of it).
+// 2^x for |x| <= 1000: n = round(x), f = x - n in [-1/2, 1/2], and 2^f = 1 + f q(f) with the polynomial
+// of degree 9 that meets (2^f - 1) / f at ten Chebyshev nodes: off by 2^-50 of the value at most,
+// and by nothing at f = 0.
 __device__ __forceinline__ double exp2_64(double x)
 {
-    // (ln 2)^k / k!
-    constexpr double C[12] = {1.0,
-                              0.693147180559945309417,
-                              0.240226506959100712334,
-                              0.0555041086648215799531,
-                              0.00961812910762847716197,
-                              0.00133335581464284434234,
-                              0.000154035303933816099544,
-                              0.0000152527338040598402800,
-                              0.00000132154867901443094884,
-                              0.000000101780860092396997275,
-                              0.00000000705491162080112332987,
-                              0.000000000444553827187081149760};
+    constexpr double Q[10] = {0.6931471805599462,    0.24022650695910075,   0.05550410866465167,
+                              0.009618129107618665,  0.0013333558200794592, 0.00015403530424776529,
+                              1.5252672924850737e-05, 1.3215451633221434e-06, 1.0205905413765595e-07,
+                              7.070977866508138e-09};
     const double n = __builtin_rint(x), f = x - n;
-    double p = C[11];
+    double q = Q[9];
 #pragma unroll
-    for (int i = 10; i >= 0; --i)
-        p = __builtin_fma(p, f, C[i]);
-    return __builtin_amdgcn_ldexp(p, (int)n);
+    for (int i = 8; i >= 0; --i)
+        q = __builtin_fma(q, f, Q[i]);
+    return __builtin_amdgcn_ldexp(__builtin_fma(q, f, 1.0), (int)n);
 }
 
-// 1 / d for d in [1, 2^1000]: the instruction's estimate and two Newton steps.
+// 1 / d for d in [1, 2^1000]: the instruction's estimate (off by 2^-24.3 at most over 2^30 arguments)
+// and a Newton step (2^-48.6).
 __device__ __forceinline__ double recip_64(double d)
 {
-    double r = __builtin_amdgcn_rcp(d);
-    r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+    const double r = __builtin_amdgcn_rcp(d);
     return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
 
