@@ -44,25 +44,30 @@ __all__ = [
 _torch_mod = None
 _tags = None
 _raw_stream = _get_device = _empty_here = _values = _bytes = _int8 = _fp32 = None
+_value_tags = None
+_loaded = None  # the library, once an operator has been called
 
 
 def _torch():
     """torch, imported on first use; the dtype tags and the device and stream queries with it."""
     global _torch_mod, _tags, _values, _bytes, _int8, _fp32, _raw_stream, _get_device, _empty_here
+    global _value_tags
     if _torch_mod is None:
         import torch
         _tags = {torch.float16: F16, torch.bfloat16: BF16, torch.int32: U4X8_I32,
                  torch.float32: F32}
         _values, _bytes = (torch.float16, torch.bfloat16, torch.float32), (torch.uint8,)
         _int8, _fp32 = (torch.int8,), (torch.float32,)
+        _value_tags = {t: _tags[t] for t in _values}
         # the current stream's handle without building a Stream object: 0.1
         # against 1.9 us, in calls whose launch takes 3
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-        # a contiguous tensor on the current device: 0.8 against 1.7 us
+        # a tensor (shape, strides, dtype) on the current device: 0.8 against 1.7 us
         guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
-        _empty_here = getattr(guards, "_empty_strided_cuda", None)
+        _empty_here = getattr(guards, "_empty_strided_cuda", None) or (
+            lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype, device="cuda"))
         _torch_mod = torch
     return _torch_mod
 
@@ -289,8 +294,7 @@ def _output(t, name, shape, dtype, device):
     """A caller's output on `device`, checked, or a new one, which needs no check."""
     if t is None:
         index = device.index  # None: the host, which the caller refuses
-        if index is not None and _empty_here is not None and len(shape) <= 2 and 0 not in shape \
-                and _get_device() == index:
+        if index is not None and len(shape) <= 2 and 0 not in shape and _get_device() == index:
             return _empty_here(shape, (shape[1], 1) if len(shape) == 2 else (1,) * len(shape), dtype)
         return _torch_mod.empty(shape, dtype=dtype, device=device)
     _want(t, name, shape, (dtype,))
@@ -447,9 +451,13 @@ def mxfp4_moe_layer(x, logits, topk: int, w1_fp4, w1_scale, w2_fp4, w2_scale, bi
     return out
 
 
+# The operators below are called for single tokens, where the host's time is the call's: their
+# operands are checked in one pass each, outputs made on the current device, and a call for another
+# device is made again with that one current.
+
 def _operand(t, name, shape, dtypes, index):
     """_want, and t is contiguous and lives where the call's first operand does (index: its
-    get_device(), below 0 for the host, which the caller refuses once all shapes are right)."""
+    get_device(), below 0 for the host, which is refused once all shapes are right)."""
     if t is None or t.shape != shape or t.dtype not in dtypes:
         _want(t, name, shape, dtypes)
     if not t.is_contiguous():
@@ -458,16 +466,29 @@ def _operand(t, name, shape, dtypes, index):
         raise ValueError("operands live on different devices")
 
 
-def _on_device(index):
+def _elsewhere(index):
+    """Whether the call has to be made again with device `index` current."""
     if index < 0:
         raise ValueError("all operands must be device tensors")
+    return _get_device() != index
 
 
-def _row_count(lead):
-    R = 1
-    for n in lead:
-        R *= n
-    return R
+def _library():
+    global _loaded
+    _loaded = _lib.lib()
+    return _loaded
+
+
+def _contiguous_strides(shape):
+    if len(shape) == 2:
+        return (shape[1] or 1, 1)
+    if len(shape) == 1:
+        return (1,)
+    strides, n = [], 1
+    for d in reversed(shape):
+        strides.append(n)
+        n *= max(d, 1)
+    return tuple(reversed(strides))
 
 
 def _row_stride(x, name):
@@ -496,55 +517,71 @@ def int8_quantize(x, act: int = ACT_NONE, out=None, out_scale=None):
     x [..., 2K] holds gate and up halves, and silu(gate) * up is quantised.  x is
     contiguous, or 2-D with contiguous elements in each row and rows any 16-byte aligned
     distance apart (a column slice)."""
-    torch = _torch()
-    if x.dim() < 1:
+    torch = _torch_mod or _torch()
+    shape = tuple(x.shape)
+    if not shape:
         raise ValueError("x must be [..., K]")
-    if x.dtype not in _values:
-        _want(x, "x", x.shape, _values)
-    if act not in (ACT_NONE, ACT_SILU_MUL):
-        raise ValueError(f"unknown activation {act}")
-    K = x.shape[-1]
+    tag = _value_tags.get(x.dtype)
+    if tag is None:
+        _want(x, "x", shape, _values)
+    K = shape[-1]
     if act == ACT_SILU_MUL:
         if K % 2 != 0:
             raise ValueError(f"x has {K} columns; gate and up halves make an even number")
         K //= 2
+        shape = (*shape[:-1], K)
+    elif act != ACT_NONE:
+        raise ValueError(f"unknown activation {act}")
     if not 16 <= K <= 65536 or K % 16 != 0:
         raise ValueError(f"K={K} must be a multiple of 16, up to 65536")
-    lead = tuple(x.shape[:-1])
-    ldx = _row_stride(x, "x")
-    _on_device(x.get_device())
-    dev = x.device
-    out = _output(out, "out", (*lead, K), torch.int8, dev)
-    out_scale = _output(out_scale, "out_scale", lead, torch.float32, dev)
-    st = _run(_lib.lib().int8_quantize, dev, x.data_ptr(), _tags[x.dtype], ldx, act, out.data_ptr(),
-              out_scale.data_ptr(), _row_count(lead), K)
-    _lib.check(st, "int8_quantize")
+    lead, ldx, index = shape[:-1], _row_stride(x, "x"), x.get_device()
+    if out is not None:
+        _operand(out, "out", shape, _int8, index)
+    if out_scale is not None:
+        _operand(out_scale, "out_scale", lead, _fp32, index)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return int8_quantize(x, act, out, out_scale)
+    if out is None:
+        out = _empty_here(shape, _contiguous_strides(shape), torch.int8)
+    if out_scale is None:
+        out_scale = _empty_here(lead, _contiguous_strides(lead), torch.float32)
+    st = (_loaded or _library()).int8_quantize(
+        x.data_ptr(), tag, ldx, act, out.data_ptr(), out_scale.data_ptr(), out.numel() // K, K,
+        _raw_stream(index))
+    if st:
+        _lib.check(st, "int8_quantize")
     return out, out_scale
 
 
 def int8_dequant(codes, scale, out_dtype=None, out=None):
     """Rows in 8 bits read back: codes [..., K] int8 and scale [...] float32 -> values
     [..., K] in out_dtype (bfloat16 when neither it nor out is given)."""
-    torch = _torch()
-    if codes.dim() < 1:
+    torch = _torch_mod or _torch()
+    shape, index = tuple(codes.shape), codes.get_device()
+    if not shape:
         raise ValueError("codes must be [..., K]")
-    shape = tuple(codes.shape)
     lead, K = shape[:-1], shape[-1]
-    index = codes.get_device()
     _operand(codes, "codes", shape, _int8, index)
     if not 16 <= K <= 65536 or K % 16 != 0:
         raise ValueError(f"K={K} must be a multiple of 16, up to 65536")
     _operand(scale, "scale", lead, _fp32, index)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
-    if out_dtype not in _values:
+    tag = _value_tags.get(out_dtype)
+    if tag is None:
         raise TypeError(f"out_dtype {out_dtype} must be float16, bfloat16 or float32")
-    _on_device(index)
-    dev = codes.device
-    out = _output(out, "out", shape, out_dtype, dev)
-    st = _run(_lib.lib().int8_dequant, dev, codes.data_ptr(), scale.data_ptr(), out.data_ptr(),
-              _tags[out_dtype], _row_count(lead), K)
-    _lib.check(st, "int8_dequant")
+    if out is not None:
+        _operand(out, "out", shape, (out_dtype,), index)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return int8_dequant(codes, scale, out_dtype, out)
+    if out is None:
+        out = _empty_here(shape, _contiguous_strides(shape), out_dtype)
+    st = (_loaded or _library()).int8_dequant(codes.data_ptr(), scale.data_ptr(), out.data_ptr(), tag,
+                                              out.numel() // K, K, _raw_stream(index))
+    if st:
+        _lib.check(st, "int8_dequant")
     return out
 
 
@@ -559,7 +596,7 @@ def int8_gemm(x_q, x_scale, w_q, w_scale, bias=None, out=None, out_dtype=None, w
     with w_scale [N] float32 (a channel's) -> y [M,N] = x_scale * w_scale * (x_q . w_q^T)
     (+ bias [N] float32) in out_dtype (bfloat16 when neither it nor out is given; float16
     and float32 too).  The sum over K is exact."""
-    torch = _torch()
+    torch = _torch_mod or _torch()
     if x_q.dim() != 2 or w_q.dim() != 2:
         raise ValueError("x_q must be [M, K] and w_q [N, K]")
     M, K = x_q.shape
@@ -573,18 +610,27 @@ def int8_gemm(x_q, x_scale, w_q, w_scale, bias=None, out=None, out_dtype=None, w
         _operand(bias, "bias", (N,), _fp32, index)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
-    if out_dtype not in _values:
+    tag = _value_tags.get(out_dtype)
+    if tag is None:
         raise TypeError(f"out_dtype {out_dtype} must be float16, bfloat16 or float32")
-    dev = x_q.device
-    out = _output(out, "out", (M, N), out_dtype, dev)
-    _on_device(index)
-    workspace, ws_bytes = _workspace(workspace, int8_gemm_workspace_size(M, N, K), dev)
+    if out is not None:
+        _operand(out, "out", (M, N), (out_dtype,), index)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return int8_gemm(x_q, x_scale, w_q, w_scale, bias, out, out_dtype, workspace)
+    need = ws_bytes = int8_gemm_workspace_size(M, N, K)
     if workspace is not None:
-        _check_device(workspace, x_q)
-    st = _run(_lib.lib().int8_gemm, dev, x_q.data_ptr(), x_scale.data_ptr(), w_q.data_ptr(),
-              w_scale.data_ptr(), _ptr(bias), out.data_ptr(), _tags[out_dtype], M, N, K,
-              _ptr(workspace), ws_bytes)
-    _lib.check(st, "int8_gemm")
+        workspace, ws_bytes = _workspace(workspace, need, x_q.device)
+        _check_device(x_q, workspace)
+    elif need:
+        workspace = _empty_here((need,), (1,), torch.uint8)
+    if out is None:
+        out = _empty_here((M, N), (max(N, 1), 1), out_dtype)
+    st = (_loaded or _library()).int8_gemm(
+        x_q.data_ptr(), x_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), _ptr(bias), out.data_ptr(),
+        tag, M, N, K, _ptr(workspace), ws_bytes, _raw_stream(index))
+    if st:
+        _lib.check(st, "int8_gemm")
     return out
 
 
@@ -602,7 +648,7 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: float
     quant=QUANT_INT8 (as int8_quantize) or QUANT_MXFP4 (as mxfp4_quantize).  residual_out
     may be residual itself.  y=None: n of the residual alone (then h is residual, and n has
     weight's dtype).  weight=None: no n (it is returned as None)."""
-    torch = _torch()
+    torch = _torch_mod or _torch()
     if residual.dim() != 2:
         raise ValueError("residual must be [T, H]")
     T, H = shape = tuple(residual.shape)
@@ -610,14 +656,15 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: float
     if block is None:
         raise ValueError("y and weight are both missing: there is nothing to compute")
     dt, rdt = block.dtype, residual.dtype
-    if dt not in _values:
+    tag = _value_tags.get(dt)
+    if tag is None:
         raise TypeError(f"dtype {dt} must be float16, bfloat16 or float32")
     own = (dt,)
-    index, dev = residual.get_device(), residual.device
+    index = residual.get_device()
     _operand(residual, "residual", shape, own if rdt == dt else _fp32, index)
-    if quant not in (QUANT_NONE, QUANT_INT8, QUANT_MXFP4):
+    whole = 8 if quant == QUANT_NONE else 16 if quant == QUANT_INT8 else 32
+    if whole == 32 and quant != QUANT_MXFP4:
         raise ValueError(f"unknown quant {quant}")
-    whole = 32 if quant == QUANT_MXFP4 else 16 if quant == QUANT_INT8 else 8
     if not whole <= H <= 32768 or H % whole != 0:
         raise ValueError(f"H={H} must be a multiple of {whole}, up to 32768")
     if not (math.isfinite(alpha) and math.isfinite(eps) and eps >= 0):
@@ -632,8 +679,8 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: float
                 _operand(gate, "gate", (H,), own, index)
             else:
                 ldg = _rows_like(gate, "gate", shape, own, index)
-        if residual_out is not residual:
-            residual_out = _output(residual_out, "residual_out", shape, rdt, dev)
+        if residual_out is not None and residual_out is not residual:
+            _operand(residual_out, "residual_out", shape, (rdt,), index)
     elif post_weight is not None or gate is not None:
         raise ValueError("without y there is no post_weight and no gate")
     elif residual_out is not None:
@@ -646,18 +693,34 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: float
         if quant == QUANT_NONE:
             if out_scale is not None:
                 raise ValueError("out_scale without quantised rows")
-            out = _output(out, "out", shape, dt, dev)
+            width, kind = H, dt
         elif quant == QUANT_INT8:
-            out = _output(out, "out", shape, torch.int8, dev)
-            out_scale = _output(out_scale, "out_scale", (T,), torch.float32, dev)
+            width, kind = H, torch.int8
+            if out_scale is not None:
+                _operand(out_scale, "out_scale", (T,), _fp32, index)
         else:
-            out = _output(out, "out", (T, H // 2), torch.uint8, dev)
-            out_scale = _output(out_scale, "out_scale", (T, H // 32), torch.uint8, dev)
-    _on_device(index)
-    st = _run(_lib.lib().residual_norm, dev, _ptr(y), _tags[dt], ldy, residual.data_ptr(),
-              _tags[rdt], _ptr(post_weight), _ptr(gate), ldg, alpha, _ptr(weight), eps,
-              quant, _ptr(out), _ptr(out_scale), _ptr(residual_out), T, H)
-    _lib.check(st, "residual_norm")
+            width, kind = H // 2, torch.uint8
+            if out_scale is not None:
+                _operand(out_scale, "out_scale", (T, H // 32), _bytes, index)
+        if out is not None:
+            _operand(out, "out", (T, width), (kind,), index)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return residual_norm(y, residual, weight, post_weight, gate, alpha, eps, quant, out, out_scale,
+                                 residual_out)
+    if y is not None and residual_out is None:
+        residual_out = _empty_here(shape, (H, 1), rdt)
+    if weight is not None:
+        if out is None:
+            out = _empty_here((T, width), (width, 1), kind)
+        if out_scale is None and quant != QUANT_NONE:
+            out_scale = (_empty_here((T,), (1,), torch.float32) if quant == QUANT_INT8 else
+                         _empty_here((T, H // 32), (H // 32, 1), torch.uint8))
+    st = (_loaded or _library()).residual_norm(
+        _ptr(y), tag, ldy, residual.data_ptr(), _value_tags[rdt], _ptr(post_weight), _ptr(gate), ldg, alpha,
+        _ptr(weight), eps, quant, _ptr(out), _ptr(out_scale), _ptr(residual_out), T, H, _raw_stream(index))
+    if st:
+        _lib.check(st, "residual_norm")
     h = residual if y is None else residual_out
     return (out, h) if quant == QUANT_NONE else (out, out_scale, h)
 
@@ -671,7 +734,7 @@ def moe_route(logits, topk: int, bias=None, score: int = SCORE_SIGMOID, groups: 
     topk_groups groups with the largest sum of their group_top (1 or 2) best, then the topk
     best experts in them, ties to the lowest index.  weights: scale * s, over the chosen
     experts' sum with renormalize.  Places without an expert hold id -1 and weight 0."""
-    torch = _torch()
+    torch = _torch_mod or _torch()
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     T, E = shape = tuple(logits.shape)
@@ -683,20 +746,29 @@ def moe_route(logits, topk: int, bias=None, score: int = SCORE_SIGMOID, groups: 
         raise ValueError(f"E={E} (up to 1024) must be a multiple of groups={groups} (up to 64)")
     if not 1 <= topk_groups <= groups:
         raise ValueError(f"topk_groups={topk_groups} must be between 1 and groups={groups}")
-    if not 1 <= topk <= min(64, topk_groups * (E // groups)):
+    if not 1 <= topk <= 64 or topk > topk_groups * (E // groups):
         raise ValueError(f"topk={topk} must be between 1 and 64 and at most the kept groups' experts")
     if group_top not in (1, 2):
         raise ValueError(f"group_top={group_top} must be 1 or 2")
     if bias is not None:
         _operand(bias, "bias", (E,), _fp32, index)
-    dev = logits.device
-    ids = _output(ids, "ids", (T, topk), torch.int32, dev)
-    weights = _output(weights, "weights", (T, topk), torch.float32, dev)
-    _on_device(index)
-    st = _run(_lib.lib().moe_route, dev, logits.data_ptr(), _tags[logits.dtype], _ptr(bias),
-              ids.data_ptr(), weights.data_ptr(), T, E, topk, score, groups, topk_groups, group_top,
-              1 if renormalize else 0, scale)
-    _lib.check(st, "moe_route")
+    if ids is not None:
+        _operand(ids, "ids", (T, topk), (torch.int32,), index)
+    if weights is not None:
+        _operand(weights, "weights", (T, topk), _fp32, index)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return moe_route(logits, topk, bias, score, groups, topk_groups, group_top, renormalize, scale,
+                             ids, weights)
+    if ids is None:
+        ids = _empty_here((T, topk), (topk, 1), torch.int32)
+    if weights is None:
+        weights = _empty_here((T, topk), (topk, 1), torch.float32)
+    st = (_loaded or _library()).moe_route(
+        logits.data_ptr(), _value_tags[logits.dtype], _ptr(bias), ids.data_ptr(), weights.data_ptr(), T, E, topk,
+        score, groups, topk_groups, group_top, 1 if renormalize else 0, scale, _raw_stream(index))
+    if st:
+        _lib.check(st, "moe_route")
     return ids, weights
 
 
