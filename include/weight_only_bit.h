@@ -20,6 +20,10 @@
  *    byte is the binary32 exponent of the scale; the store guard keeps
  *    out-of-range tiles from writing into neighbouring token-slot rows.
  *
+ * Beside them stand the operators around these products in a decoder: MXFP4
+ * quantisation and product, 8-bit rows and product, the norms around a block, the
+ * choice of experts (plain and group-limited) and the mixture-of-experts layer.
+ *
  * Layouts (all row-major, contiguous, device memory unless stated):
  *   x        [M][K]        activation dtype (WOB_F16 or WOB_BF16)
  *   qweight  [N][K/8]      int32; code of (n, k) is bits 4*(k%8) of word (n, k/8)
@@ -71,9 +75,9 @@ extern "C" {
 #define WOB_U4X8_I32 2 /* eight 4-bit values packed in an int32 */
 #define WOB_F32 3
 
-/* MoE stage-1 activation (the `act` argument of mxfp4_moe_gemm). */
-#define WOB_ACT_NONE 0     /* pre-activation output [T][topk][N] */
-#define WOB_ACT_SILU_MUL 1 /* silu(gate) * up: output [T][topk][N/2] */
+/* Activation of gate and up halves (the `act` argument of mxfp4_moe_gemm and int8_quantize). */
+#define WOB_ACT_NONE 0     /* none: mxfp4_moe_gemm's output is [T][topk][N] */
+#define WOB_ACT_SILU_MUL 1 /* silu(gate) * up: mxfp4_moe_gemm's output is [T][topk][N/2] */
 
 /* What residual_norm writes its normed rows as (the `quant` argument). */
 #define WOB_QUANT_NONE 0  /* values of the block's type */
@@ -402,8 +406,8 @@ size_t int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
  *  x_q [M][K], w_q [N][K] int8 (all 256 values); x_scale [M], w_scale [N] fp32; bias
  *  [N] fp32 or NULL; y [M][N] of y_dtype WOB_F16, WOB_BF16 or WOB_F32 (else WOB_DTYPE).
  *  The sum is exact in 32 bits.  It is rounded to fp32, multiplied with x_scale[m],
- *  then with w_scale[n], the bias is added, each in fp32, and y is rounded once more,
- *  to nearest even.  A NaN scale makes every output of its row or column NaN.
+ *  then with w_scale[n], the bias is added, each in fp32 (the last product and the
+ *  bias as one operation or two), and y is rounded once more, to nearest even.  A NaN scale makes every output of its row or column NaN.
  *  K % 16 == 0, 16 <= K <= 131056, N % 8 == 0, M >= 0, N >= 0, M*K and N*K below
  *  2^32, M and N below 2^27 (else WOB_INVALID_ARG).  M == 0 or N == 0 is a no-op
  *  returning WOB_OK.
@@ -421,8 +425,9 @@ int int8_gemm(const int8_t *x_q, const float *x_scale, const int8_t *w_q, const 
  *   t = y, or y / sqrt(mean(y^2) + eps) * post_weight   (post_weight != NULL)
  *   h = residual + alpha * gate * t                     (gate NULL: 1)
  *   n = h / sqrt(mean(h^2) + eps) * weight
- * in fp32.  residual_out = h rounded once to the residual's type; n, from the
- * unrounded h, as `quant` says: rounded once to `dtype`, in 8-bit rows as by
+ * in fp32 (a row whose squares sum past fp32's range is divided by infinity).
+ * residual_out = h rounded once to the residual's type; n, from the unrounded h, as
+ * `quant` says: rounded once to `dtype`, in 8-bit rows as by
  * int8_quantize, or in MXFP4 blocks as by mxfp4_quantize.
  *
  *  dtype (of y, post_weight, gate, weight and n): WOB_F16, WOB_BF16 or WOB_F32;

@@ -111,6 +111,40 @@ def test_values_next_to_a_border(wob):
     check(wob, l.cuda(), 8, b.float().cuda() * 2.0 ** -8, False, 8, 4, 2)
 
 
+@pytest.mark.parametrize("sigmoid", (True, False))
+@pytest.mark.parametrize("E,groups,kept,topk", SIZES)
+def test_many_rows_of_every_kind(wob, sigmoid, E, groups, kept, topk):
+    """Past 2048 tokens up to 16 lanes share a token: random, tied, masked and infinite rows,
+    many times over, so that every row meets every place of a wave."""
+    torch = torch_mod()
+    g = torch.Generator().manual_seed(3 * E + topk)
+    base = torch.randn((41, E), generator=g) * 1.5
+    base[5:15] = torch.randint(-1, 2, (10, E), generator=g).float()
+    base[15] = 0
+    base[16] = -np.inf
+    base[17, ::2] = -np.inf
+    base[18, : E - 1] = np.nan
+    base[19, E // 2:] = np.inf
+    base[20] = 50.0
+    base[21] = -300.0
+    base[22:26] = (0.7 + torch.randint(-9, 10, (4, E), generator=g) * 2.0 ** -23)
+    reps = 53
+    for dtype, biased, top, renormalize in (("fp32", True, 2, True), ("bf16", False, 1, False), ("fp16", True, 1, True)):
+        logits = base.to(_dt(dtype)).cuda()
+        bias = (torch.randint(-4, 5, (E,), generator=g).float() * 0.0625) if biased else None
+        ids, w = R.route(logits.float().cpu().numpy(), topk, None if bias is None else bias.numpy(), sigmoid, groups, kept,
+                         top, renormalize, 1.0)
+        bias = None if bias is None else bias.cuda()
+        got = wob.moe_route(logits.repeat(reps, 1), topk, bias=bias,
+                            score=wob.SCORE_SIGMOID if sigmoid else wob.SCORE_SOFTMAX, groups=groups, topk_groups=kept,
+                            group_top=top, renormalize=renormalize)
+        assert reps * 41 > 2048
+        i = got[0].view(reps, 41, topk).cpu().numpy()
+        assert (i == ids).all(), (dtype, np.argwhere((i != ids).any(-1))[:4])
+        off = np.abs(got[1].view(reps, 41, topk).double().cpu().numpy() - w)
+        assert (off <= R.route_bound(w, topk)).all()
+
+
 def test_one_group_and_kept_all_are_the_same(wob):
     torch = torch_mod()
     l = torch.randn((300, 96), device="cuda")
