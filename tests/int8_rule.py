@@ -4,15 +4,24 @@ import numpy as np
 
 F = np.float32
 # path, weight rows, activation rows, us a round, us a round and 1000 k
-TILES = (("large", 256, 256, 20.0, 10.0), ("wide", 256, 128, 12.0, 7.0), ("medium", 128, 128, 9.0, 4.6),
-         ("small", 64, 128, 7.0, 3.5), ("narrow", 64, 64, 5.5, 2.6))
+TILES = (("large", 256, 256, 8.3, 11.0), ("wide", 256, 128, 6.5, 8.2), ("medium", 128, 128, 5.4, 5.0),
+         ("small", 64, 128, 4.4, 3.5), ("narrow", 64, 64, 3.6, 2.1))
 
 
-def few_block(N):
+def few_form(M, N, K):
+    """(waves that share rows, groups of rows) of a workgroup"""
+    if M > 8:
+        return (8, 1) if N <= 4096 else (4, 2)
+    if N <= 4096:
+        return 4, 1
+    return (8, 1) if M <= 2 and N > 8192 and K > 4096 else (2, 4)
+
+
+def few_block(M, N, K):
     per = 1
     while 8 * -(-N // (2048 * per)) > 32:
         per += 1
-    return 8 * -(-N // (2048 * per))
+    return min(8 * -(-N // (2048 * per)), few_form(M, N, K)[1] * (16 if M > 8 else 8))
 
 
 def plan(M, N, K):
@@ -24,15 +33,16 @@ def plan(M, N, K):
         while parts == 1 or parts <= min(256 // tiles, K // 512, 16):
             rounds, k = -(-tiles * parts // 256), -(-K // parts)
             busy = F(tiles * parts) / F(256 * rounds)
-            us = F(rounds) * (F(start) + F(per_k) * F(1e-3) * F(k) * (F(0.8) + F(0.2) * busy))
+            us = F(rounds) * F(start) + max(F(rounds) * F(per_k) * F(1e-3) * F(k) * (F(0.75) + F(0.25) * busy),
+                                            F(0.155e-6) * F(N * K))
             if parts > 1:
-                us += F(2.5) + F(0.3) * (F(parts) + F(0.5)) * F(M * N) * F(4e-6)
+                us += F(1.8) + F(0.42) * (F(parts) + F(0.5)) * F(M * N) * F(4e-6)
             if us < least:
                 least, best = us, (path, parts)
             parts += 1
     if M <= 16 and M * ((K + 111) // 128 * 128 + 16) <= 80 * 1024:
-        rows = few_block(N)
+        rows = few_block(M, N, K)
         per_cu = -(-(-(-N // rows)) // 256)
-        if F(3.0) + F(0.18e-6) * F(N * K) + F(0.04e-3) * F(M * K * per_cu) < least:
+        if F(2.9) + F(0.145e-6) * F(N * K) + F(0.034e-3) * F(M * K * per_cu) < least:
             best = ("few", rows)
     return best

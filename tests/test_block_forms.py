@@ -17,8 +17,10 @@ import pytest
 
 from tests.test_kernel_forms import CSRC, HIPCC, ROOT, main_loop, needs_hipcc, tile_events, waits_of
 
-TILES = {(2, 4, 4, 2, 5), (4, 2, 4, 2, 6), (2, 2, 2, 2, 8), (2, 1, 2, 2, 12), (2, 1, 1, 2, 10)}
-FEW = {(4, 1), (8, 1), (4, 2), (8, 2)}
+# waves along n, blocks, stages of a group, half groups of the ring, nontemporal weights
+TILES = {(2, 4, 4, 2, 5, 0), (4, 2, 4, 2, 6, 0)} | {(2, *t, nt) for t in ((2, 2, 2, 9), (1, 2, 2, 10), (1, 1, 2, 11))
+                                                    for nt in (0, 1)}
+FEW = {(4, 1, 0), (8, 1, 0), (2, 4, 0), (8, 1, 1), (4, 2, 1)}
 F16, BF16, F32 = 0, 1, 3
 TYPES = (F16, BF16, F32)
 # threads of a row, pieces of eight elements a thread -> a row's length that takes them
@@ -51,14 +53,14 @@ def forms(text, kernel, count):
     return {tuple(map(int, m.groups())) for m in re.finditer(pattern + r"\S*:\s*;", text, re.M)}
 
 
-TILE = re.compile(r"^\S*int8_tile_kernelINS0_8Int8TileILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)EEE\S*:\s*;", re.M)
+TILE = re.compile(r"^\S*int8_tile_kernelINS0_8Int8TileILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)EEELb([01])EE\S*:\s*;", re.M)
 
 
 @needs_hipcc
 def test_product_forms(assembly):
     text = assembly["int8_gemm.hip"]
     assert {tuple(map(int, m.groups())) for m in TILE.finditer(text)} == TILES
-    assert forms(text, "int8_few_kernel", 2) == FEW
+    assert forms(text, "int8_few_kernel", 3) == FEW
 
 
 @needs_hipcc
@@ -94,7 +96,7 @@ def test_route_forms(assembly):
     assert forms(assembly["moe_route.hip"], "moe_route_kernel", 4) == {(t,) + f for t in TYPES for f in reached}
 
 
-def tile_faults(body, wn, nb, mb, gs, nh):
+def tile_faults(body, wn, nb, mb, gs, nh, nt):
     """What is wrong with a tile kernel's waits, as a list of texts."""
     copies = (32 * nb * wn + 32 * mb * (4 // wn)) * 64 * gs // 4096  # of a wave and group
     faults, events = [], tile_events(body)
@@ -125,7 +127,7 @@ def tile_faults(body, wn, nb, mb, gs, nh):
 def test_tiles_wait_for_the_group_they_read_next(assembly):
     text, seen = assembly["int8_gemm.hip"], 0
     for m in TILE.finditer(text):
-        wn, nb, mb, gs, nh = geometry = tuple(map(int, m.groups()))
+        wn, nb, mb, gs, nh, _ = geometry = tuple(map(int, m.groups()))
         body = text[m.end():text.index(".Lfunc_end", m.end())]
         assert tile_faults(body, *geometry) == [], geometry
         # the check sees a wait that lets one copy more stay in flight

@@ -3,7 +3,7 @@ so a lost piece, part, row or column shows."""
 import pytest
 
 from tests.gpu_util import require_gpu, torch_mod
-from tests.int8_rule import plan
+from tests.int8_rule import few_form, plan
 from tests.test_gpu_int8 import guarded, guards_whole
 
 pytestmark = pytest.mark.gpu
@@ -17,20 +17,30 @@ def wob():
     return w
 
 
-# (path, in parts): sizes, ragged in M and N
+# (path, in parts; few rows: waves x groups, weight rows of a workgroup): sizes, ragged in M and N
 FORMS = {
-    ("few", 8): [(1, 8, 16), (1, 2048, 1024), (5, 2040, 1040), (16, 1016, 4160)],
-    ("few", 16): [(1, 4088, 4096), (3, 4096, 4112), (16, 3000, 2896)],
-    ("few", 24): [(1, 6000, 2000), (2, 5384, 5392), (7, 6000, 2000)],
-    ("few", 32): [(2, 8192, 1040), (1, 16376, 5376), (16, 8184, 1040)],
+    ("few 4 x 1", 8): [(1, 8, 16), (1, 2048, 1024), (5, 2040, 1040), (8, 4088, 4112), (3, 64, 48), (3, 1000, 22800)],
+    ("few 8 x 1", 8): [(1, 8200, 4112), (2, 11032, 7696)],
+    ("few 2 x 4", 24): [(1, 6000, 2000), (2, 5384, 5392), (7, 6000, 2000), (4, 4104, 16)],
+    ("few 2 x 4", 32): [(2, 8192, 1040), (8, 8184, 2000), (5, 6952, 688)],
+    ("few 8 x 1 wide", 8): [(16, 1016, 4160), (9, 8, 16), (13, 40, 1232)],
+    ("few 8 x 1 wide", 16): [(16, 3000, 2896), (9, 2056, 144), (11, 3464, 256)],
+    ("few 4 x 2 wide", 24): [(13, 5760, 2880), (9, 4136, 16), (11, 4768, 464)],
+    ("few 4 x 2 wide", 32): [(16, 8184, 1040), (10, 6416, 80), (12, 15392, 240)],
     ("narrow", False): [(17, 8, 16), (40, 2048, 496), (64, 16328, 656)],
     ("narrow", True): [(17, 8, 2016), (17, 72, 1936), (33, 5000, 2896), (100, 2000, 4112), (16, 5376, 21504), (40, 2000, 8192), (33, 1000, 16400)],
     ("small", False): [(71, 9064, 16), (100, 16000, 1040), (129, 8100 // 8 * 8, 2064)],
-    ("small", True): [(2790, 8, 9616), (120, 5376, 5392)],
+    ("small", True): [(1094, 264, 7728), (126, 3240, 19808)],
     ("medium", False): [(17, 18136, 16), (200, 16376, 1040), (500, 8184, 2000)],
     ("medium", True): [(100, 5368, 21520), (250, 5376, 8208)],
+    # weights that are copied nontemporally
+    ("narrow once", False): [(33, 65584, 2064), (61, 11952, 11232)],
+    ("narrow once", True): [(17, 6056, 22224)],
+    ("small once", False): [(110, 14424, 9440)],
+    ("medium once", False): [(100, 27120, 4960)],
+    ("medium once", True): [(105, 5728, 23440)],
     ("wide", False): [(133, 18512, 16), (511, 16376, 1040), (1000, 8184, 2064)],
-    ("wide", True): [(400, 5376, 21520), (1, 5360, 27984)],
+    ("wide", True): [(351, 3024, 20176), (501, 4232, 13504)],
     ("large", False): [(276, 22800, 16), (2047, 16376, 1040), (1500, 5752, 2896)],
     ("large", True): [(140, 16680, 7184), (760, 5376, 21520)],
 }
@@ -39,7 +49,10 @@ SMALL_SETS = [(form, size) for form, sizes in FORMS.items() for size in sizes]
 
 def named(M, N, K):
     path, parts = plan(M, N, K)
-    return (path, parts) if path == "few" else (path, parts > 1)
+    if path == "few":
+        return "few %d x %d%s" % (*few_form(M, N, K), " wide" if M > 8 else ""), parts
+    once = M <= {"narrow": 64, "small": 128, "medium": 128}.get(path, 0) and N * K > 128 << 20
+    return path + " once" * once, parts > 1
 
 
 def exact(x, xs, w, ws, bias=None):

@@ -5,7 +5,7 @@ import random
 
 import pytest
 
-from tests.int8_rule import few_block, plan
+from tests.int8_rule import few_block, few_form, plan
 
 
 @pytest.fixture(scope="module")
@@ -40,6 +40,10 @@ def test_a_part_has_a_group_at_least():
 
 def test_few_rows_blocks():
     for N in (8, 16, 2048, 2056, 4096, 4104, 5376, 6144, 8192, 8200, 16384, 43008, 131072):
-        rows = few_block(N)
-        assert rows % 8 == 0 and 8 <= rows <= 32
-    assert [few_block(N) for N in (2048, 4096, 5376, 5760, 16384)] == [8, 16, 24, 24, 32]
+        for M in (1, 2, 3, 8, 9, 16):
+            for K in (16, 4096, 4112):
+                rows, (_, groups) = few_block(M, N, K), few_form(M, N, K)
+                assert rows % 8 == 0 and 8 <= rows <= groups * (16 if M > 8 else 8) <= 32
+    assert [few_block(4, N, 5376) for N in (2048, 4096, 5376, 5760, 16384)] == [8, 8, 24, 24, 32]
+    assert [few_block(13, N, 2880) for N in (2048, 4096, 5376, 5760, 16384)] == [8, 16, 24, 24, 32]
+    assert few_block(1, 16384, 5376) == 8

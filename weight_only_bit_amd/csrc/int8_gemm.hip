@@ -52,56 +52,57 @@ __device__ __forceinline__ float4_t scaled4(const i32x4 &sum, float xs, const fl
 
 // ---- Few rows --------------------------------------------------------------
 //
-// M <= 16.  A wave owns 16 weight rows; W waves share them and split K, in pairs of steps
-// of 64 k (in a step lane (r, q) = (lane % 16, lane / 16) holds the 16 k of block 4 j + q of
-// row r, so a pair is one whole cache line of each row), and their sums are joined in
-// LDS.  A workgroup has G such groups of rows.  The weights go from memory into registers,
-// FR_D loads of a lane ahead; only x passes through LDS (pitch 16 mod 128 bytes, which makes
-// its reads conflict-free), with its loads ahead of the weights' so that they land first.
+// M <= 16.  A wave owns 8 weight rows, with M > 8 (WIDE) 16; W waves share them and split K,
+// and their sums are joined in LDS.  A workgroup has G such groups of rows.  The weights go from
+// memory into registers, FR_D loads of a lane ahead; only x passes through LDS (pitch 16 mod 128
+// bytes, which makes its reads conflict-free), with its loads ahead of the weights' so that they
+// land first.
 //
-// Bound by the weights' bytes: 1 x 16384 x 5376 (88 MB) 17.8 us, a plain read of as many bytes 15.2;
-// 1 x 43008 x 5376 (231 MB) 43.2, a read 33.5; 13 x 5760 x 2880 (17 MB) 7.0, a read 3.9 (graph
-// replays over copies larger than the caches).
-constexpr int FR_ROWS = 16;
-constexpr int FR_D = 6;  // loads ahead
-constexpr int FR_CH = 2; // neighbouring steps of a wave
+// A load is one whole cache line of each of 8 weight rows: lane (r, q) = (lane % 16, lane / 16)
+// holds piece 4 (r / 8) + q of the line of row r % 8.  With up to 8 activation rows that is the
+// instruction's first operand as it is: its rows 0 to 7 and 8 to 15 are the same weight rows with
+// the two halves of 128 k, its column j is activation row j % 8 with half j / 8, and of
+// its sums the two 8 x 8 blocks of equal halves are used.  WIDE: the second load holds rows 8 + r %
+// 8 with the halves swapped, so lanes r < 8 of the one and r >= 8 of the other are rows 0 to 15 with the
+// first half, and the rest are rows r ^ 8 with the second.
+//
+// Nothing reads a line twice, so the loads are nontemporal.
+constexpr int FR_D = 6; // loads ahead
 
 __host__ __device__ inline int few_pitch(int K) { return (K + 127 - 16) / 128 * 128 + 16; }
-inline size_t few_lds(int M, int K, int W, int G)
-{
-    const size_t sums = W > 1 ? (size_t)W * G * 1024 : 0;
-    return std::max((size_t)M * few_pitch(K), sums);
-}
 
-template <int W, int G>
+template <int W, int G, bool WIDE>
 __global__ __launch_bounds__(64 * W * G) void int8_few_kernel(Int8GemmArgs a, int M, int N, int K,
                                                              int rows)
 {
-    constexpr int NT = 64 * W * G;
+    constexpr int NT = 64 * W * G, L = WIDE ? 2 : 1, U = FR_D / L; // loads of a line, lines ahead
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), k = wave % W, g = wave / W;
-    const int KB = K >> 4, steps = (KB + 3) >> 2, pitch = few_pitch(K);
-    const int n0 = blockIdx.x * rows + FR_ROWS * g, n_end = min((blockIdx.x + 1) * rows, N); // (rows <= FR_ROWS G)
+    const int KB = K >> 4, lines = (KB + 7) >> 3, pitch = few_pitch(K);
+    const int n0 = blockIdx.x * rows + 8 * L * g, n_end = min((blockIdx.x + 1) * rows, N); // (rows <= 8 L G)
 
     // Staging of x, 16 bytes a thread, the first round's loads ahead of the weights'.
     const int nx = M * KB;
     const u32x4 *xg = reinterpret_cast<const u32x4 *>(a.x);
     const u32x4 x_first = xg[min(tid, nx - 1)];
 
-    const u32x4 *wr = reinterpret_cast<const u32x4 *>(a.w) + (size_t)min(n0 + r, n_end - 1) * KB;
-    const int mine = FR_CH * (((steps + FR_CH - 1) / FR_CH - k + W - 1) / W); // steps of this wave
-    auto block = [&](int i) __attribute__((always_inline)) { // this lane's in step i
-        return 4 * (FR_CH * (k + W * (i / FR_CH)) + i % FR_CH) + q;
-    };
-    u32x4 ring[FR_D];
-    auto load = [&](int i, u32x4 &s) __attribute__((always_inline)) {
-        int b = min(block(i), KB - 1);
-        asm volatile("" : "+v"(b)); // one address per load, not one pointer kept per slot
-        s = wr[b];
+    const u32x4 *wr[L];
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+        wr[l] = reinterpret_cast<const u32x4 *>(a.w) + (size_t)min(n0 + 8 * l + r % 8, n_end - 1) * KB;
+    const int mine = (lines - k + W - 1) / W; // lines of this wave
+    u32x4 ring[U][L];
+    auto load = [&](int i, u32x4 (&s)[L]) __attribute__((always_inline)) { // line i of this wave
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            int b = min(8 * (k + W * i) + 4 * (r / 8 ^ l) + q, KB - 1);
+            asm volatile("" : "+v"(b)); // one address per load, not one pointer kept per slot
+            s[l] = __builtin_nontemporal_load(wr[l] + b);
+        }
     };
 #pragma unroll
-    for (int d = 0; d < FR_D; ++d)
+    for (int d = 0; d < U; ++d)
         load(min(d, max(mine - 1, 0)), ring[d]);
     __builtin_amdgcn_sched_barrier(0);
 
@@ -115,64 +116,68 @@ __global__ __launch_bounds__(64 * W * G) void int8_few_kernel(Int8GemmArgs a, in
         put_x(i, xg[i]);
     __syncthreads();
 
-    const uint8_t *xrow = smem + (size_t)min(r, M - 1) * pitch;
-    i32x4 acc = {0, 0, 0, 0};
-    auto multiply = [&](int i, u32x4 wv) __attribute__((always_inline)) {
-        const int b = block(i);
-        const bool in = b < KB; // the last steps may leave some lanes without a block
-        const u32x4 xv = *reinterpret_cast<const u32x4 *>(xrow + 16 * min(b, KB - 1));
+    const uint8_t *xrow = smem + (size_t)min(WIDE ? r : r % 8, M - 1) * pitch;
+    i32x4 acc[L] = {};
+    auto multiply = [&](int i, const u32x4 (&s)[L]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            wv[e] = in ? wv[e] : 0u;
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(bitcast<i32x4>(wv), bitcast<i32x4>(xv), acc, 0, 0, 0);
+        for (int l = 0; l < L; ++l) {
+            const int b = 8 * (k + W * i) + 4 * (WIDE ? l : r / 8) + q;
+            const bool in = b < KB; // the last line may leave some lanes without a piece
+            const bool first = !WIDE || (r < 8) == (l == 0); // which load has it
+            u32x4 wv;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                wv[e] = in ? (first ? s[0][e] : s[L - 1][e]) : 0u;
+            const i32x4 xv = *reinterpret_cast<const i32x4 *>(xrow + 16 * min(b, KB - 1));
+            acc[l] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bitcast<i32x4>(wv), xv, acc[l], 0, 0, 0);
+        }
     };
     int i = 0;
-    for (; i + FR_D < mine; i += FR_D) {
+    for (; i + U < mine; i += U) {
 #pragma unroll
-        for (int d = 0; d < FR_D; ++d) {
+        for (int d = 0; d < U; ++d) {
             if (i + d < mine)
                 multiply(i + d, ring[d]);
             __builtin_amdgcn_sched_barrier(0);
-            load(min(i + d + FR_D, mine - 1), ring[d]);
+            load(min(i + d + U, mine - 1), ring[d]);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
 #pragma unroll
-    for (int d = 0; d < FR_D; ++d)
+    for (int d = 0; d < U; ++d)
         if (i + d < mine)
             multiply(i + d, ring[d]);
-    // Lane (r, q) holds n = 4 q + e of output row r in acc[e]; the waves of a
-    // group are summed in order.
-    if constexpr (W > 1) {
-        __syncthreads();
-        i32x4 *part = reinterpret_cast<i32x4 *>(smem);
-        part[wave * 64 + lane] = acc;
-        __syncthreads();
-        if (k != 0)
-            return;
+    // Lane (r, q) holds the instruction's rows 4 q + e of its column r: the sums of both halves
+    // and of all waves of a group meet at the lane of their first half.
+    __syncthreads();
+    i32x4 *const part = reinterpret_cast<i32x4 *>(smem) + g * W * L * 64;
 #pragma unroll
-        for (int j = 1; j < W; ++j)
-            acc += part[(wave + j) * 64 + lane];
-    }
+    for (int l = 0; l < L; ++l)
+        part[(k * L + l) * 64 + (lane ^ 32 * l)] = acc[l];
+    __syncthreads();
     const int n = n0 + 4 * q;
-    if (r < M && n < n_end) {
-        float4_t v = scaled4(acc, a.xs[r], *reinterpret_cast<const float4_t *>(a.ws + n));
-        if (a.bias)
-            v += *reinterpret_cast<const float4_t *>(a.bias + n);
-        store4(a.y, a.ydt, (size_t)r * N + n, v);
-    }
+    if (k != 0 || r >= M || n >= n_end || (!WIDE && (r >= 8 || q >= 2)))
+        return;
+    i32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        sum += part[j * L * 64 + lane] + part[j * L * 64 + lane + (WIDE ? 64 : 2 * 16 + 8)];
+    float4_t v = scaled4(sum, a.xs[r], *reinterpret_cast<const float4_t *>(a.ws + n));
+    if (a.bias)
+        v += *reinterpret_cast<const float4_t *>(a.bias + n);
+    store4(a.y, a.ydt, (size_t)r * N + n, v);
 }
 
-template <int W, int G>
+template <int W, int G, bool WIDE>
 hipError_t launch_few(const Int8GemmArgs &a, int M, int N, int K, int rows, hipStream_t stream)
 {
-    auto kern = int8_few_kernel<W, G>;
+    auto kern = int8_few_kernel<W, G, WIDE>;
     static std::atomic<uint64_t> lds_set{0};
     if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), 160 * 1024, lds_set);
         e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(kern, dim3((N + rows - 1) / rows), dim3(64 * W * G), few_lds(M, K, W, G), stream, a, M, N, K,
-                       rows);
+    const size_t lds = std::max((size_t)M * few_pitch(K), (size_t)W * G * (WIDE ? 2 : 1) * 1024); // x, then the sums
+    hipLaunchKernelGGL(kern, dim3((N + rows - 1) / rows), dim3(64 * W * G), lds, stream, a, M, N, K, rows);
     return hipGetLastError();
 }
 
@@ -199,9 +204,9 @@ hipError_t launch_few(const Int8GemmArgs &a, int M, int N, int K, int rows, hipS
 // Copies cost one cache look-up a row and instruction, so whole lines (GS = 2) are copied, and the
 // 256 x 256 tile, of which two groups fit, gets half a third.  2048 x 16384 x 5376, us: four groups of
 // 64 bytes a row 175 to 191, five 179, two of 128 bytes 174 to 187, two and a half 158 to 160.  The
-// other tiles are bound by bytes, and by how many are under way: 32 x 5376 x 21504 three groups a
-// part 35.0, five 25.8, eight 26.2; 100 x 5376 x 21504 in the 128 x 128 tile three 33 to 34.5, four 31.8 to
-// 32.9, five 33.2 to 34.8.
+// other tiles are bound by bytes; rings of an odd number of halves are faster for them too, deeper ones
+// and eight waves of half the blocks are not: 64 x 16384 x 5376 in the 64 x 64 tile (nontemporal) 8 halves
+// 21.8, 9 18.7, 10 21.6, 11 18.5, 13 18.7; 100 x 5376 x 21504 in the 128 x 128 tile 6 34.6, 7 33.6, 8 34.5, 9 33.2.
 //
 // 2048 x 16384 x 5376, 150 to 165 us (2.2 to 2.4 POPS; the library's product of the operands without
 // scales 164): the power limit.  MFMA busy 63 % at 1.7 GHz; with zero codes, which switch nothing,
@@ -280,12 +285,19 @@ __device__ __forceinline__ void store_wave(const i32x16 (&acc)[T::NB][T::MB], vo
             const int row = q * RPI + lane / VECS, m = mw + 32 * k + row;
             const u32x4 v = *reinterpret_cast<const u32x4 *>(stage + row * PITCH + lane % VECS * 16);
             if (m < M && n < N) // N % 8 == 0: a piece is whole
-                *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(y) + ((size_t)m * N + n) * ES) = v;
+            {
+                u32x4 *const to = reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(y) + ((size_t)m * N + n) * ES);
+                if constexpr (RAW)
+                    *to = v;
+                else
+                    __builtin_nontemporal_store(v, to);
+            }
         }
     }
 }
 
-template <class T>
+// NT: weights are copied nontemporally.
+template <class T, bool NT>
 __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__restrict__ part, int M, int N, int K,
                                                         int tiles_m, int tiles, int splits, int nxcd)
 {
@@ -346,7 +358,10 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
         const int from = g_begin + min(g + NH / 2 + (ODD && second), groups - 1);
         const uint32_t k = min((uint32_t)from * (uint32_t)T::SEG + piece, rowb - 16u);
         const int to = (second ? p.b : p.a) + 4096 * (second ? d - (ODD ? ND / 2 : NDA) : d) + wave * 1024;
-        lds_dma16(b_rows ? a.x : a.w, row_at[i] + k, lds0 + (uint32_t)to);
+        if (b_rows)
+            lds_dma16(a.x, row_at[i] + k, lds0 + (uint32_t)to);
+        else
+            lds_dma16<NT>(a.w, row_at[i] + k, lds0 + (uint32_t)to);
     };
 
     i32x16 acc[T::NB][T::MB] = {};
@@ -564,10 +579,10 @@ hipError_t launch_sum(const Int8GemmArgs &a, const int *part, int M, int N, int 
     return hipGetLastError();
 }
 
-template <class T>
+template <class T, bool NT = false>
 hipError_t launch_tile(const Int8GemmArgs &a, int M, int N, int K, int splits, void *workspace, hipStream_t stream)
 {
-    auto kern = int8_tile_kernel<T>;
+    auto kern = int8_tile_kernel<T, NT>;
     static std::atomic<uint64_t> lds_set{0};
     if (const hipError_t e = lds_optin(reinterpret_cast<const void *>(kern), 160 * 1024, lds_set);
         e != hipSuccess)
@@ -587,26 +602,21 @@ hipError_t launch_tile(const Int8GemmArgs &a, int M, int N, int K, int splits, v
 
 using TileL = Int8Tile<2, 4, 4, 2, 5>;  // 256 x 256
 using TileW = Int8Tile<4, 2, 4, 2, 6>;  // 256 weight rows x 128 activation rows
-using TileM = Int8Tile<2, 2, 2, 2, 8>;  // 128 x 128
-using TileS = Int8Tile<2, 1, 2, 2, 12>; // 64 weight rows x 128 activation rows
-using TileN = Int8Tile<2, 1, 1, 2, 10>; // 64 x 64
+using TileM = Int8Tile<2, 2, 2, 2, 9>;  // 128 x 128
+using TileS = Int8Tile<2, 1, 2, 2, 10>; // 64 weight rows x 128 activation rows
+using TileN = Int8Tile<2, 1, 1, 2, 11>; // 64 x 64
 
 // ---- Choice ----------------------------------------------------------------
 //
-// The form and its K parts are the ones with the smallest estimate, in us, which is linear in
-// what was measured (graph replays over copies larger than the caches, 618 pairs of a shape
-// and a form, M 1 to 1536, N x K of 1024 x 8192 to 43008 x 5376):
-//   tiles: rounds of 256 workgroups, each `start` and `per_k` a 1000 k of a part, the latter a fifth
-//          less on an empty card;
+// The form and its K parts are the ones with the smallest estimate, in us, from what was measured
+// (graph replays over copies larger than the caches, 4800 triples of a shape, a form and parts, M 1 to
+// 2048, N x K of 512 x 512 to 43008 x 5376):
+//   tiles: rounds of 256 workgroups, each `start` and `per_k` a 1000 k of a part, the latter a quarter
+//          less on an empty card, but at least the weights' bytes;
 //   parts: their sum's launch and its bytes;
 //   few rows: the weights' bytes and the staging of x by a CU's workgroups.
-// On average the choice is 0.2 % slower than the best form measured from 20 rows on, and 2 %
-// below; at worst 17 % (16 x 4096 x 4096, 10.5 us, 9.0 with four parts of the 64 x 64 tile).  Best
-// and next form, us: 2048 x 5376 x 5376 256 x 256 67, 256 x 128 78; 512 x 16384 x 5376 256 x 128 50,
-// 128 x 128 63; 200 x 16384 x 5376 128 x 128 34, 64 x 128 37; 100 x 16384 x 5376 64 x 128 27, 64 x 64
-// 30; 64 x 16384 x 5376 64 x 64 24, 64 x 128 26; 96 x 5376 x 21504 256 x 128 in 8 parts 35.9, 128 x 128
-// in 6 36.3; 13 x 5760 x 2880 few rows 7.0, 64 x 64 9.5; 2 x 5376 x 21504 64 x 64 in 3 parts 24.6, few
-// rows 27.
+// On average the choice is 0.5 % slower than the best form and parts measured, at worst 16 % (48 x 4096
+// x 14336, 64 x 64 in 3 parts 20.1 us, in 4 17.3).
 enum class Path { Few, Large, Wide, Medium, Small, Narrow };
 
 struct Plan {
@@ -614,26 +624,45 @@ struct Plan {
     int splits; // Few: weight rows of a workgroup
 };
 
+// Waves that share rows and groups of rows of a workgroup.  us, 4 x 1, 8 x 1, 2 x 4: 1 x 1024 x 8192 5.3,
+// 5.3, 6.5; 1 x 2048 x 2048 3.4, 4.1, 3.9; 1 x 5376 x 5376 8.3, 8.1, 7.4; 1 x 16384 x 5376 16.9, 16.2, 17.4;
+// 1 x 43008 x 5376 38.9, 39.8, 41.4; 8 x 16384 x 5376 25.1, 24.4, 18.4.  Wide, 8 x 1 and 4 x 2: 16 x 2048 x 2048 4.4,
+// 4.7; 13 x 5760 x 2880 7.5, 6.8; 13 x 43008 x 5376 51, 48.
+struct FewForm {
+    int waves, groups;
+};
+FewForm few_form(int64_t M, int64_t N, int64_t K)
+{
+    if (M > 8)
+        return N <= 4096 ? FewForm{8, 1} : FewForm{4, 2};
+    if (N <= 4096) // few workgroups: more waves of them
+        return {4, 1};
+    if (M <= 2 && N > 8192 && K > 4096) // x is small enough for each workgroup of 8 rows to stage
+        return {8, 1};
+    return {2, 4};
+}
+
 struct TileCost {
     Path path;
     int tn, tm;
     float start, per_k;
 };
 constexpr TileCost TILE_COSTS[] = {
-    {Path::Large, TileL::TN, TileL::TM, 20.f, 10.f}, {Path::Wide, TileW::TN, TileW::TM, 12.f, 7.f},
-    {Path::Medium, TileM::TN, TileM::TM, 9.f, 4.6f}, {Path::Small, TileS::TN, TileS::TM, 7.f, 3.5f},
-    {Path::Narrow, TileN::TN, TileN::TM, 5.5f, 2.6f},
+    {Path::Large, TileL::TN, TileL::TM, 8.3f, 11.f}, {Path::Wide, TileW::TN, TileW::TM, 6.5f, 8.2f},
+    {Path::Medium, TileM::TN, TileM::TM, 5.4f, 5.f}, {Path::Small, TileS::TN, TileS::TM, 4.4f, 3.5f},
+    {Path::Narrow, TileN::TN, TileN::TM, 3.6f, 2.1f},
 };
 constexpr int MOST_PARTS = 16, PART_K = 512; // parts, at most; k of a part, at least
 
-// Weight rows of a workgroup so that every CU gets the same number of them: 8 to 32 (1 x 5376 x
-// 21504 24 rows, 224 workgroups, 26 us; 32 28, 16 30).
-int few_block(int64_t N)
+// Weight rows of a workgroup of few rows: what its groups hold, at most as many that every CU gets the
+// same number of them.
+int few_block(int64_t M, int64_t N, int64_t K)
 {
+    const int most = few_form(M, N, K).groups * (M > 8 ? 16 : 8);
     for (int64_t per = 1;; ++per) {
         const int64_t rows = 8 * ((N + 2048 * per - 1) / (2048 * per));
-        if (rows <= 2 * FR_ROWS)
-            return (int)rows;
+        if (rows <= 32)
+            return (int)std::min<int64_t>(rows, most);
     }
 }
 
@@ -647,9 +676,10 @@ Plan plan(int64_t M, int64_t N, int64_t K)
         for (int64_t parts = 1; parts == 1 || parts <= most; ++parts) {
             const int64_t rounds = (tiles * parts + 255) / 256, k = (K + parts - 1) / parts;
             const float busy = (float)(tiles * parts) / (float)(256 * rounds);
-            float us = (float)rounds * (t.start + t.per_k * 1e-3f * (float)k * (0.8f + 0.2f * busy));
+            float us = (float)rounds * t.start + std::max((float)rounds * t.per_k * 1e-3f * (float)k * (0.75f + 0.25f * busy),
+                                                          0.155e-6f * (float)(N * K));
             if (parts > 1)
-                us += 2.5f + 0.3f * ((float)parts + 0.5f) * (float)(M * N) * 4e-6f;
+                us += 1.8f + 0.42f * ((float)parts + 0.5f) * (float)(M * N) * 4e-6f;
             if (us < least) {
                 least = us;
                 best = {t.path, (int)parts};
@@ -657,12 +687,23 @@ Plan plan(int64_t M, int64_t N, int64_t K)
         }
     }
     if (M <= 16 && M * few_pitch((int)K) <= 80 * 1024) { // x leaves the LDS room for a second workgroup
-        const int rows = few_block(N);
+        const int rows = few_block(M, N, K);
         const int64_t per_cu = ((N + rows - 1) / rows + 255) / 256;
-        if (3.0f + 0.18e-6f * (float)(N * K) + 0.04e-3f * (float)(M * K * per_cu) < least)
+        if (2.9f + 0.145e-6f * (float)(N * K) + 0.034e-3f * (float)(M * K * per_cu) < least)
             best = {Path::Few, rows};
     }
     return best;
+}
+
+// Weights of more than half of the last-level cache (256 MB) that one tile of activation rows reads are
+// copied nontemporally.  us, ordinary and nontemporal, past the caches / three sets of weights: 32 x 43008
+// x 5376 54.4, 50.8 / 53.3, 48.5; 100 x 43008 x 5376 65.1, 61.4 / 64.7, 61.5; but 64 x 16384 x 5376 23.7, 22.8 /
+// 17.8, 21.4; 100 x 8192 x 5376 19.8, 21.3 / 17.2, 20.8; two tiles: 200 x 16384 x 5376 33.1, 34.7.
+template <class T>
+hipError_t launch_once(const Int8GemmArgs &a, int M, int N, int K, int splits, void *workspace, hipStream_t stream)
+{
+    return M <= T::TM && (int64_t)N * K > (int64_t)128 << 20 ? launch_tile<T, true>(a, M, N, K, splits, workspace, stream)
+                                                             : launch_tile<T>(a, M, N, K, splits, workspace, stream);
 }
 
 } // namespace
@@ -680,23 +721,27 @@ hipError_t launch_int8_gemm(const Int8GemmArgs &a, int M, int N, int K, void *wo
     const Plan p = plan(M, N, K);
     switch (p.path) {
     case Path::Few:
-        // Two groups of 16 rows, of eight waves each (one or two rows of x: four, 1 x 5376 x 21504 25.7 us
-        // and 26.3, but 4 x 5376 x 5376 9.5 and 9.3), or one, of eight (M K up to 4096: four, 1 x 4096 x
-        // 4096 5.9 and 6.6, but 2 x 4096 x 4096 6.8 and 6.6).
-        if (p.splits > FR_ROWS)
-            return M <= 2 ? launch_few<4, 2>(a, M, N, K, p.splits, stream) : launch_few<8, 2>(a, M, N, K, p.splits, stream);
-        return M * K <= 4096 ? launch_few<4, 1>(a, M, N, K, p.splits, stream)
-                             : launch_few<8, 1>(a, M, N, K, p.splits, stream);
+        switch (const FewForm f = few_form(M, N, K); 16 * f.waves + f.groups) {
+        case 16 * 8 + 1:
+            return M > 8 ? launch_few<8, 1, true>(a, M, N, K, p.splits, stream)
+                         : launch_few<8, 1, false>(a, M, N, K, p.splits, stream);
+        case 16 * 4 + 1:
+            return launch_few<4, 1, false>(a, M, N, K, p.splits, stream);
+        case 16 * 4 + 2:
+            return launch_few<4, 2, true>(a, M, N, K, p.splits, stream);
+        default:
+            return launch_few<2, 4, false>(a, M, N, K, p.splits, stream);
+        }
     case Path::Large:
         return launch_tile<TileL>(a, M, N, K, p.splits, workspace, stream);
     case Path::Wide:
         return launch_tile<TileW>(a, M, N, K, p.splits, workspace, stream);
     case Path::Medium:
-        return launch_tile<TileM>(a, M, N, K, p.splits, workspace, stream);
+        return launch_once<TileM>(a, M, N, K, p.splits, workspace, stream);
     case Path::Small:
-        return launch_tile<TileS>(a, M, N, K, p.splits, workspace, stream);
+        return launch_once<TileS>(a, M, N, K, p.splits, workspace, stream);
     default:
-        return launch_tile<TileN>(a, M, N, K, p.splits, workspace, stream);
+        return launch_once<TileN>(a, M, N, K, p.splits, workspace, stream);
     }
 }
 
