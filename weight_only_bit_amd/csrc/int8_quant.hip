@@ -9,6 +9,7 @@
 #include "wob_rows.hpp"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace wob {
 
@@ -29,8 +30,8 @@ __device__ __forceinline__ float silu_mul(float g, float u)
 // 4 46, 512 x 8 46.
 template <int DT, bool ACT, int NT, int V>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void int8_quantize_kernel(
-    const void *__restrict__ x, int64_t ldx, uint2 *__restrict__ codes, float *__restrict__ scale,
-    int64_t R, int K)
+    const void *__restrict__ x, int64_t ldx, u32x2 *__restrict__ codes, float *__restrict__ scale,
+    int64_t R, int K, bool once)
 {
     static_assert(NT == 64 || NT >= 256, "rows that share a workgroup share no barrier");
     constexpr int ROWS = NT < 256 ? 256 / NT : 1, ES = elem_size<DT>();
@@ -49,10 +50,10 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void int8_quantize_kernel(
     Raw8<DT> raw[V], up[V];
     float v[V][RV];
     uint32_t top = 0;
-    auto load = [&](int j, int p) __attribute__((always_inline)) {
-        load_raw8<DT>(row + (uint32_t)(p * RV) * ES, raw[j]);
+    auto load = [&](int j, int p, auto nt) __attribute__((always_inline)) {
+        load_raw8<DT, decltype(nt)::value>(row + (uint32_t)(p * RV) * ES, raw[j]);
         if constexpr (ACT)
-            load_raw8<DT>(ups + (uint32_t)(p * RV) * ES, up[j]);
+            load_raw8<DT, decltype(nt)::value>(ups + (uint32_t)(p * RV) * ES, up[j]);
     };
     auto values = [&](int j, int) __attribute__((always_inline)) {
         unpack8<DT>(raw[j], v[j]);
@@ -65,15 +66,21 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void int8_quantize_kernel(
         }
         top = max(top, magnitude8(v[j]));
     };
-    if constexpr (V * ES * (ACT ? 2 : 1) < 32) {
-        each(load);
-        each(values);
-    } else {
-        each([&](int j, int p) __attribute__((always_inline)) {
-            load(j, p);
-            values(j, p);
-        });
-    }
+    auto read = [&](auto nt) __attribute__((always_inline)) {
+        if constexpr (V * ES * (ACT ? 2 : 1) < 32) {
+            each([&](int j, int p) __attribute__((always_inline)) { load(j, p, nt); });
+            each(values);
+        } else {
+            each([&](int j, int p) __attribute__((always_inline)) {
+                load(j, p, nt);
+                values(j, p);
+            });
+        }
+    };
+    if (once) // x is in no cache
+        read(std::true_type{});
+    else
+        read(std::false_type{});
     const Int8Row s = int8_row(row_max<NT>(top, part));
     each([&](int j, int p) __attribute__((always_inline)) { codes[r * pieces + p] = int8_codes8(v[j], s); });
     if (t == 0)
@@ -86,12 +93,16 @@ hipError_t launch_rows(const void *x, int64_t ldx, int8_t *codes, float *scale, 
 {
     constexpr int ROWS = NT < 256 ? 256 / NT : 1;
     constexpr int64_t MOST = (int64_t)1 << 21; // rows of a launch: 2^31 threads at most
+    // Rows that the last-level cache (256 MB) cannot hold are read nontemporally, gated ones from half of it
+    // on.  us, ordinary and nontemporal, x in the caches before / not: gated 84 MB 18.5, 19.0 / 22.4, 19.8,
+    // 168 MB 33.8, 36.0 / 41.6, 36.1, 336 MB 80, 70; plain 168 MB 38, 44 / 46.4, 44.0.
+    const bool once = R * K * (ACT ? 2 : 1) * elem_size<DT>() > (int64_t)(ACT ? 128 : 256) << 20;
     for (int64_t r0 = 0; r0 < R; r0 += MOST) {
         const int64_t rows = std::min(R - r0, MOST);
         hipLaunchKernelGGL((int8_quantize_kernel<DT, ACT, NT, V>), dim3((unsigned)((rows + ROWS - 1) / ROWS)),
                            dim3(NT * ROWS), 0, stream,
                            static_cast<const uint8_t *>(x) + r0 * ldx * elem_size<DT>(), ldx,
-                           reinterpret_cast<uint2 *>(codes + r0 * K), scale + r0, rows, K);
+                           reinterpret_cast<u32x2 *>(codes + r0 * K), scale + r0, rows, K, once);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess)
             return e;
     }

@@ -13,6 +13,7 @@
 #include "wob_rows.hpp"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace wob {
 
@@ -49,18 +50,31 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_kernel(Norm
     };
     Raw8<RDT> r[V];
     Raw8<DT> y[V], gate[V], post[V], weight[V];
-    if (a.y)
-        each([&](int j, int p) { load_raw8<DT>(row_of(a.y, a.ldy, ES) + (uint32_t)(p * RV) * ES, y[j]); });
-    each([&](int j, int p) { load_raw8<RDT>(row_of(a.residual, a.H, RES) + (uint32_t)(p * RV) * RES, r[j]); });
-    auto load_gate = [&]() __attribute__((always_inline)) {
-        each([&](int j, int p) { load_raw8<DT>(row_of(a.gate, a.ldg, ES) + (uint32_t)(p * RV) * ES, gate[j]); });
+    auto load_gate = [&](auto nt) __attribute__((always_inline)) {
+        each([&](int j, int p) {
+            load_raw8<DT, decltype(nt)::value>(row_of(a.gate, a.ldg, ES) + (uint32_t)(p * RV) * ES, gate[j]);
+        });
     };
     auto load_weights = [&](const void *w, Raw8<DT> (&to)[V]) __attribute__((always_inline)) {
         each([&](int j, int p) { load_raw8<DT>(static_cast<const uint8_t *>(w) + (uint32_t)(p * RV) * ES, to[j]); });
     };
     constexpr bool EARLY = V < 4, GATE_EARLY = EARLY || DT != DT_F32; // (else they do not fit the registers)
-    if (GATE_EARLY && a.gate)
-        load_gate();
+    auto load_rows = [&](auto nt) __attribute__((always_inline)) {
+        constexpr bool NONT = decltype(nt)::value;
+        if (a.y)
+            each([&](int j, int p) { load_raw8<DT, NONT>(row_of(a.y, a.ldy, ES) + (uint32_t)(p * RV) * ES, y[j]); });
+        each([&](int j, int p) { load_raw8<RDT, NONT>(row_of(a.residual, a.H, RES) + (uint32_t)(p * RV) * RES, r[j]); });
+        if (GATE_EARLY && a.gate) {
+            if (NONT && a.ldg)
+                load_gate(std::true_type{});
+            else
+                load_gate(std::false_type{});
+        }
+    };
+    if (a.once)
+        load_rows(std::true_type{});
+    else
+        load_rows(std::false_type{});
     if (EARLY && a.post)
         load_weights(a.post, post);
     if (EARLY && a.weight)
@@ -88,7 +102,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_kernel(Norm
             });
         }
         if (!GATE_EARLY && a.gate)
-            load_gate();
+            load_gate(std::false_type{});
         each([&](int j, int) {
             float v[RV];
             unpack8<RDT>(r[j], v);
@@ -109,7 +123,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_kernel(Norm
     }
     if (a.residual_out)
         each([&](int j, int p) {
-            store8<RDT>(static_cast<uint8_t *>(a.residual_out) + (row * a.H + (uint32_t)(p * RV)) * RES, h[j]);
+            uint8_t *const to = static_cast<uint8_t *>(a.residual_out) + (row * a.H + (uint32_t)(p * RV)) * RES;
+            store8<RDT>(to, h[j]);
         });
     if (!a.weight)
         return;
@@ -130,12 +145,15 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_kernel(Norm
             h[j][i] *= rstd * w[i];
     });
     if (a.quant == WOB_QUANT_NONE) {
-        each([&](int j, int p) { store8<DT>(static_cast<uint8_t *>(a.n) + (row * a.H + (uint32_t)(p * RV)) * ES, h[j]); });
+        each([&](int j, int p) {
+            uint8_t *const to = static_cast<uint8_t *>(a.n) + (row * a.H + (uint32_t)(p * RV)) * ES;
+            store8<DT>(to, h[j]);
+        });
     } else if (a.quant == WOB_QUANT_INT8) {
         uint32_t top = 0;
         each([&](int j, int) { top = max(top, magnitude8(h[j])); });
         const Int8Row s = int8_row(row_max<NT>(top, part[2]));
-        each([&](int j, int p) { static_cast<uint2 *>(a.n)[row * pieces + p] = int8_codes8(h[j], s); });
+        each([&](int j, int p) { static_cast<u32x2 *>(a.n)[row * pieces + p] = int8_codes8(h[j], s); });
         if (t == 0)
             static_cast<float *>(a.n_scale)[row] = s.scale;
     } else {
@@ -153,6 +171,11 @@ hipError_t launch_rows(NormArgs a, hipStream_t stream)
 {
     constexpr int ROWS = NT < 256 ? 256 / NT : 1;
     constexpr int64_t MOST = (int64_t)1 << 21; // rows of a launch: 2^31 threads at most
+    // Rows that the last-level cache (256 MB) cannot hold are read nontemporally.  us, ordinary and
+    // nontemporal, operands in the caches before / not: 84 MB 28.7, 33.3 / 34.2, 33.6, 168 MB 53.7,
+    // 63.2 / 63.4, 61.4, 336 MB 120.5, 118.2 / 123.0, 120.2.
+    const int64_t operands = (a.y ? elem_size<DT>() : 0) + (a.gate && a.ldg ? elem_size<DT>() : 0) + elem_size<RDT>();
+    a.once = a.T * a.H * operands > (int64_t)256 << 20;
     for (a.row0 = 0; a.row0 < a.T; a.row0 += MOST) {
         const int64_t rows = std::min(a.T - a.row0, MOST);
         hipLaunchKernelGGL((residual_norm_kernel<DT, RDT, NT, V>), dim3((unsigned)((rows + ROWS - 1) / ROWS)),
