@@ -378,7 +378,7 @@ int mxfp4_moe_layer(const void *x, const void *logits, int logits_dtype, const f
  *
  *  x: R rows, `ldx` elements from one row's start to the next's (ldx >= K, or 2 K);
  *    x_dtype WOB_F16, WOB_BF16 or WOB_F32 (else WOB_DTYPE).
- *  codes [R][K] int8, scale [R] fp32; both contiguous.
+ *  codes [R][K] int8, scale [R] fp32; both contiguous, overlapping neither x nor each other.
  *  K % 16 == 0, 16 <= K <= 65536, R >= 0, R*K at most 2^34; rows start 16-byte
  *  aligned: ldx % 8 == 0 (% 4 for WOB_F32) (else WOB_INVALID_ARG).
  *  R == 0 is a no-op returning WOB_OK.
@@ -389,7 +389,7 @@ int int8_quantize(const void *x, int x_dtype, int64_t ldx, int act, int8_t *code
 /*
  * Rows in 8 bits read back: out[r][k] = codes[r][k] * scale[r], rounded once to
  * out_dtype (WOB_F16, WOB_BF16 or WOB_F32, else WOB_DTYPE).  codes [R][K] int8, scale
- * [R] fp32, out [R][K]; shapes as for int8_quantize.
+ * [R] fp32, out [R][K], which overlaps neither; shapes as for int8_quantize.
  */
 int int8_dequant(const int8_t *codes, const float *scale, void *out, int out_dtype, int64_t R,
                  int64_t K, void *stream);
@@ -404,10 +404,12 @@ size_t int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
  * 8-bit product with a scale for each token and each channel:
  *   y[m][n] = x_scale[m] * w_scale[n] * sum_k x_q[m][k] * w_q[n][k] + bias[n]
  *  x_q [M][K], w_q [N][K] int8 (all 256 values); x_scale [M], w_scale [N] fp32; bias
- *  [N] fp32 or NULL; y [M][N] of y_dtype WOB_F16, WOB_BF16 or WOB_F32 (else WOB_DTYPE).
+ *  [N] fp32 or NULL; y [M][N] of y_dtype WOB_F16, WOB_BF16 or WOB_F32 (else WOB_DTYPE),
+ *  overlapping no operand.
  *  The sum is exact in 32 bits.  It is rounded to fp32, multiplied with x_scale[m],
  *  then with w_scale[n], the bias is added, each in fp32 (the last product and the
- *  bias as one operation or two), and y is rounded once more, to nearest even.  A NaN scale makes every output of its row or column NaN.
+ *  bias as one operation or two), and y is rounded once more, to nearest even.  A NaN
+ *  scale makes every output of its row or column NaN.
  *  K % 16 == 0, 16 <= K <= 131056, N % 8 == 0, M >= 0, N >= 0, M*K and N*K below
  *  2^32, M and N below 2^27 (else WOB_INVALID_ARG).  M == 0 or N == 0 is a no-op
  *  returning WOB_OK.
@@ -471,7 +473,7 @@ int residual_norm(const void *y, int dtype, int64_t ldy, const void *residual, i
  * have it.
  *
  *  logits [T][E] of logits_dtype WOB_F16, WOB_BF16 or WOB_F32 (else WOB_DTYPE), bias [E]
- *  fp32 or NULL.
+ *  fp32 or NULL; ids and weights overlap no operand.
  *  T >= 0, T below 2^25, 1 <= E <= 1024, 1 <= groups <= 64, E % groups == 0,
  *  1 <= topk_groups <= groups, group_top 1 or 2, 1 <= topk <= 64, topk at most
  *  topk_groups * (E / groups), scale finite (else WOB_INVALID_ARG).  T == 0 is a no-op

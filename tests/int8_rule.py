@@ -3,9 +3,9 @@ how many K parts a shape gets, so that tests can name shapes on both sides of it
 import numpy as np
 
 F = np.float32
-# path, weight rows, activation rows, us a round, us a round and 1000 k
-TILES = (("large", 256, 256, 8.3, 11.0), ("wide", 256, 128, 6.5, 8.2), ("medium", 128, 128, 5.4, 5.0),
-         ("small", 64, 128, 4.4, 3.5), ("narrow", 64, 64, 3.6, 2.1))
+# path, weight rows, activation rows, us a round, us a round and 1000 k, us a million bytes of weights
+TILES = (("large", 256, 256, 7.9, 13.0, 0.24), ("wide", 256, 128, 6.2, 7.9, 0.21), ("medium", 128, 128, 5.4, 5.1, 0.19),
+         ("small", 64, 128, 4.6, 3.6, 0.17), ("narrow", 64, 64, 3.4, 2.4, 0.17))
 
 
 def few_form(M, N, K):
@@ -14,7 +14,7 @@ def few_form(M, N, K):
         return (8, 1) if N <= 4096 else (4, 2)
     if N <= 4096:
         return 4, 1
-    return (8, 1) if M <= 2 and N > 8192 and K > 4096 else (2, 4)
+    return (8, 1) if M <= 2 and N > 8192 and K >= 5120 else (2, 4)
 
 
 def few_block(M, N, K):
@@ -27,22 +27,23 @@ def few_block(M, N, K):
 def plan(M, N, K):
     """(path, parts); few rows: ("few", weight rows of a workgroup)."""
     best, least = None, F(np.inf)
-    for path, tn, tm, start, per_k in TILES:
+    for path, tn, tm, start, per_k, per_mb in TILES:
         tiles = -(-M // tm) * -(-N // tn)
         parts = 1
         while parts == 1 or parts <= min(256 // tiles, K // 512, 16):
             rounds, k = -(-tiles * parts // 256), -(-K // parts)
             busy = F(tiles * parts) / F(256 * rounds)
-            us = F(rounds) * F(start) + max(F(rounds) * F(per_k) * F(1e-3) * F(k) * (F(0.75) + F(0.25) * busy),
-                                            F(0.155e-6) * F(N * K))
+            us = F(rounds) * F(start) + max(F(rounds) * F(per_k) * F(1e-3) * F(k) * (F(0.65) + F(0.35) * busy),
+                                            F(per_mb) * F(1e-6) * F(N * K))
             if parts > 1:
-                us += F(1.8) + F(0.42) * (F(parts) + F(0.5)) * F(M * N) * F(4e-6)
+                us += F(1.8) + F(0.33) * (F(parts) + F(0.5)) * F(M * N) * F(4e-6)
             if us < least:
                 least, best = us, (path, parts)
             parts += 1
     if M <= 16 and M * ((K + 111) // 128 * 128 + 16) <= 80 * 1024:
         rows = few_block(M, N, K)
         per_cu = -(-(-(-N // rows)) // 256)
-        if F(2.9) + F(0.145e-6) * F(N * K) + F(0.034e-3) * F(M * K * per_cu) < least:
+        stage = F(0.005e-3) if M <= 8 and rows == 8 and N > 8192 else F(0.035e-3)
+        if F(2.8) + F(0.17e-6) * F(N * K) + stage * F(M * K * per_cu) < least:
             best = ("few", rows)
     return best

@@ -20,7 +20,7 @@ def wob():
 # (path, in parts; few rows: waves x groups, weight rows of a workgroup): sizes, ragged in M and N
 FORMS = {
     ("few 4 x 1", 8): [(1, 8, 16), (1, 2048, 1024), (5, 2040, 1040), (8, 4088, 4112), (3, 64, 48), (3, 1000, 22800)],
-    ("few 8 x 1", 8): [(1, 8200, 4112), (2, 11032, 7696)],
+    ("few 8 x 1", 8): [(1, 8392, 5312), (2, 11032, 7696)],
     ("few 2 x 4", 24): [(1, 6000, 2000), (2, 5384, 5392), (7, 6000, 2000), (4, 4104, 16)],
     ("few 2 x 4", 32): [(2, 8192, 1040), (8, 8184, 2000), (5, 6952, 688)],
     ("few 8 x 1 wide", 8): [(16, 1016, 4160), (9, 8, 16), (13, 40, 1232)],

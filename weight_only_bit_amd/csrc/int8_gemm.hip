@@ -609,14 +609,14 @@ using TileN = Int8Tile<2, 1, 1, 2, 11>; // 64 x 64
 // ---- Choice ----------------------------------------------------------------
 //
 // The form and its K parts are the ones with the smallest estimate, in us, from what was measured
-// (graph replays over copies larger than the caches, 4800 triples of a shape, a form and parts, M 1 to
-// 2048, N x K of 512 x 512 to 43008 x 5376):
-//   tiles: rounds of 256 workgroups, each `start` and `per_k` a 1000 k of a part, the latter a quarter
+// (graph replays over copies larger than the caches, 5600 triples of a shape, a form and parts, M 1 to
+// 2048, N x K of 512 x 512 to 65528 x 16384):
+//   tiles: rounds of 256 workgroups, each `start` and `per_k` a 1000 k of a part, the latter a third
 //          less on an empty card, but at least the weights' bytes;
 //   parts: their sum's launch and its bytes;
 //   few rows: the weights' bytes and the staging of x by a CU's workgroups.
-// On average the choice is 0.5 % slower than the best form and parts measured, at worst 16 % (48 x 4096
-// x 14336, 64 x 64 in 3 parts 20.1 us, in 4 17.3).
+// On average the choice is 0.4 % slower than the best form and parts measured, at worst 14 % (1 x 28672
+// x 8192, few rows 48 us, 64 x 64 42).
 enum class Path { Few, Large, Wide, Medium, Small, Narrow };
 
 struct Plan {
@@ -637,7 +637,7 @@ FewForm few_form(int64_t M, int64_t N, int64_t K)
         return N <= 4096 ? FewForm{8, 1} : FewForm{4, 2};
     if (N <= 4096) // few workgroups: more waves of them
         return {4, 1};
-    if (M <= 2 && N > 8192 && K > 4096) // x is small enough for each workgroup of 8 rows to stage
+    if (M <= 2 && N > 8192 && K >= 5120) // x is small enough for each workgroup of 8 rows to stage
         return {8, 1};
     return {2, 4};
 }
@@ -645,12 +645,12 @@ FewForm few_form(int64_t M, int64_t N, int64_t K)
 struct TileCost {
     Path path;
     int tn, tm;
-    float start, per_k;
+    float start, per_k, per_mb; // us a round, a round and 1000 k, a million bytes of weights
 };
 constexpr TileCost TILE_COSTS[] = {
-    {Path::Large, TileL::TN, TileL::TM, 8.3f, 11.f}, {Path::Wide, TileW::TN, TileW::TM, 6.5f, 8.2f},
-    {Path::Medium, TileM::TN, TileM::TM, 5.4f, 5.f}, {Path::Small, TileS::TN, TileS::TM, 4.4f, 3.5f},
-    {Path::Narrow, TileN::TN, TileN::TM, 3.6f, 2.1f},
+    {Path::Large, TileL::TN, TileL::TM, 7.9f, 13.f, 0.24f},  {Path::Wide, TileW::TN, TileW::TM, 6.2f, 7.9f, 0.21f},
+    {Path::Medium, TileM::TN, TileM::TM, 5.4f, 5.1f, 0.19f}, {Path::Small, TileS::TN, TileS::TM, 4.6f, 3.6f, 0.17f},
+    {Path::Narrow, TileN::TN, TileN::TM, 3.4f, 2.4f, 0.17f},
 };
 constexpr int MOST_PARTS = 16, PART_K = 512; // parts, at most; k of a part, at least
 
@@ -676,10 +676,10 @@ Plan plan(int64_t M, int64_t N, int64_t K)
         for (int64_t parts = 1; parts == 1 || parts <= most; ++parts) {
             const int64_t rounds = (tiles * parts + 255) / 256, k = (K + parts - 1) / parts;
             const float busy = (float)(tiles * parts) / (float)(256 * rounds);
-            float us = (float)rounds * t.start + std::max((float)rounds * t.per_k * 1e-3f * (float)k * (0.75f + 0.25f * busy),
-                                                          0.155e-6f * (float)(N * K));
+            float us = (float)rounds * t.start + std::max((float)rounds * t.per_k * 1e-3f * (float)k * (0.65f + 0.35f * busy),
+                                                          t.per_mb * 1e-6f * (float)(N * K));
             if (parts > 1)
-                us += 1.8f + 0.42f * ((float)parts + 0.5f) * (float)(M * N) * 4e-6f;
+                us += 1.8f + 0.33f * ((float)parts + 0.5f) * (float)(M * N) * 4e-6f;
             if (us < least) {
                 least = us;
                 best = {t.path, (int)parts};
@@ -689,7 +689,9 @@ Plan plan(int64_t M, int64_t N, int64_t K)
     if (M <= 16 && M * few_pitch((int)K) <= 80 * 1024) { // x leaves the LDS room for a second workgroup
         const int rows = few_block(M, N, K);
         const int64_t per_cu = ((N + rows - 1) / rows + 255) / 256;
-        if (2.9f + 0.145e-6f * (float)(N * K) + 0.034e-3f * (float)(M * K * per_cu) < least)
+        // (8 x 1 with many workgroups: the others hide it)
+        const float stage = M <= 8 && rows == 8 && N > 8192 ? 0.005e-3f : 0.035e-3f;
+        if (2.8f + 0.17e-6f * (float)(N * K) + stage * (float)(M * K * per_cu) < least)
             best = {Path::Few, rows};
     }
     return best;
