@@ -24,9 +24,10 @@ FEW = {(4, 1, 0), (8, 1, 0), (2, 4, 0), (8, 1, 1), (4, 2, 1)}
 F16, BF16, F32 = 0, 1, 3
 TYPES = (F16, BF16, F32)
 # threads of a row, pieces of eight elements a thread -> a row's length that takes them
-NORM = {(64, 1): 512, (256, 1): 2048, (512, 1): 4096, (512, 2): 8192, (1024, 2): 16384, (1024, 4): 32768}
-ROWS8 = {(64, 1): 512, (256, 1): 2048, (512, 1): 4096, (512, 2): 8192, (512, 4): 16384, (512, 6): 24576,
-         (1024, 4): 32768, (1024, 8): 65536}
+NORM = {(8, 1): 64, (16, 1): 128, (32, 1): 256, (64, 1): 512, (64, 2): 1024, (256, 1): 2048,
+        (512, 1): 4096, (512, 2): 8192, (1024, 2): 16384, (1024, 4): 32768}
+ROWS8 = {(8, 1): 64, (16, 1): 128, (32, 1): 256, (64, 1): 512, (64, 2): 1024, (256, 1): 2048,
+         (256, 2): 4096, (512, 2): 8192, (512, 4): 16384, (512, 6): 24576, (1024, 4): 32768, (1024, 8): 65536}
 
 
 @pytest.fixture(scope="module")

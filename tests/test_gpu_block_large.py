@@ -31,7 +31,7 @@ def parts(n):
 
 @pytest.mark.parametrize("gated", (False, True))
 @pytest.mark.parametrize("dtype", ("bf16", "fp16", "fp32"))
-@pytest.mark.parametrize("K", (512, 2048, 4080, 8192, 16384, 21504, 32768, 65536))
+@pytest.mark.parametrize("K", (48, 128, 256, 512, 1024, 2048, 4080, 8192, 16384, 21504, 32768, 65536))
 def test_quantise(wob, K, dtype, gated):
     torch = torch_mod()
     act, width = (wob.ACT_SILU_MUL, 2 * K) if gated else (wob.ACT_NONE, K)
@@ -46,7 +46,7 @@ def test_quantise(wob, K, dtype, gated):
 
 @pytest.mark.parametrize("gate", (None, "channel", "rows"))
 @pytest.mark.parametrize("dtype,res", (("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")))
-@pytest.mark.parametrize("H", (512, 2048, 4064, 8192, 16384, 32768))
+@pytest.mark.parametrize("H", (64, 128, 256, 512, 1024, 2048, 4064, 8192, 16384, 32768))
 def test_norm(wob, H, dtype, res, gate):
     torch = torch_mod()
     n = PAST // (H * ((2 if dtype != "fp32" else 4) + (2 if res != "fp32" else 4))) + 3

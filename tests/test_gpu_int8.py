@@ -60,7 +60,8 @@ def rows(n, K, seed, dtype):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n,K", [(1, 16), (1, 5376), (3, 64), (7, 496), (5, 512), (33, 528), (257, 160),
                                  (6, 2048), (5, 2064), (4, 8192), (3, 8208), (2, 32768), (3, 32784), (2, 65536),
-                                 (1000, 32), (300, 2880)])
+                                 (1000, 32), (300, 2880), (70, 48), (71, 128), (19, 144), (17, 256), (9, 272), (7, 768),
+                                 (5, 1024), (6, 1040), (3, 4096), (2, 4112)])
 def test_quantize_exact(wob, dtype, n, K):
     x = rows(n, K, n * K, dtype)
     codes, scale = R.int8_rows(x.float().cpu().numpy())
@@ -142,7 +143,8 @@ def test_quantize_leading_dimensions(wob):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("n,K", [(1, 16), (5, 512), (9, 528), (300, 2880), (3, 8208), (2, 21504), (2, 65536)])
+@pytest.mark.parametrize("n,K", [(1, 16), (5, 512), (9, 528), (300, 2880), (3, 8208), (2, 21504), (2, 65536), (37, 64),
+                                 (19, 112), (9, 256), (5, 1024)])
 def test_quantize_gated(wob, dtype, n, K):
     torch = torch_mod()
     g = torch.Generator().manual_seed(n + K)

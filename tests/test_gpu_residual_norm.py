@@ -48,7 +48,7 @@ def close(got, ref, bound, dtype):
 @pytest.mark.parametrize("post", (False, True))
 @pytest.mark.parametrize("gate", (None, "channel", "rows"))
 @pytest.mark.parametrize("T,H", [(1, 8), (3, 72), (5, 512), (2, 520), (70, 2048), (3, 2056), (300, 5376), (2, 8200),
-                                 (2, 32768)])
+                                 (2, 32768), (37, 64), (19, 128), (9, 136), (13, 256), (6, 264), (5, 1024), (3, 1032)])
 def test_plain(wob, dtype, res, post, gate, T, H):
     torch = torch_mod()
     d = inputs(T, H, dtype, res, T * H)
@@ -64,7 +64,7 @@ def test_plain(wob, dtype, res, post, gate, T, H):
 
 
 @pytest.mark.parametrize("dtype,res", TYPES)
-@pytest.mark.parametrize("T,H", [(1, 16), (7, 528), (3, 5376), (2, 16384), (2, 32752)])
+@pytest.mark.parametrize("T,H", [(1, 16), (7, 528), (3, 5376), (2, 16384), (2, 32752), (33, 48), (9, 112), (5, 240), (3, 1008)])
 def test_int8(wob, dtype, res, T, H):
     torch = torch_mod()
     d = inputs(T, H, dtype, res, T + H)
@@ -83,7 +83,7 @@ def test_int8(wob, dtype, res, T, H):
     assert (np.abs(c64).max(-1) == 127).all()
 
 
-@pytest.mark.parametrize("T,H", [(1, 32), (7, 544), (3, 5376), (2, 16384), (40, 2048)])
+@pytest.mark.parametrize("T,H", [(1, 32), (7, 544), (3, 5376), (2, 16384), (40, 2048), (37, 64), (9, 128), (11, 256), (5, 992)])
 def test_quantised_rows_are_those_of_the_quantisers(wob, T, H):
     """In 32 bits the normed rows are at hand: the fused codes and scales are byte for byte
     what the quantisers make of them."""

@@ -26,19 +26,22 @@ __device__ __forceinline__ float silu_mul(float g, float u)
 // NT threads share a row, V pieces of eight elements a thread: piece j of thread t is j NT + t.
 // All loads of a row are issued before the first of them is used, as far as registers reach.
 //
-// 2048 x 21504 bf16 gated (220 MB) 42 us, 5.2 TB/s, with 512 x 6; 1024 x 3 and x 4 45 to 47, 768 x
-// 4 46, 512 x 8 46.
+// 2048 x 21504 bf16 gated (220 MB) 36 us, 6.0 TB/s, with 512 x 6 (42 when read ordinarily; then 1024 x 3 and
+// x 4 45 to 47, 768 x 4 46, 512 x 8 46).  Rows too short for a wave share one: 65536 x 16 bf16 3.5 us with
+// 8 threads a row, 4.9 with 16, 12.4 with 64; 65536 x 128 7.6 with 16, 15.7 with 64.  Longer ones, us:
+// 32768 x 768 64 x 2 16.0, 256 x 1 25.9; 8192 x 2208 256 x 2 13.2, 512 x 1 17.3, one row of 2880 2.3 and
+// 2.2; 2048 x 5376 512 x 2 8.5, 256 x 3 8.4, one row 2.3 and 2.5.
 template <int DT, bool ACT, int NT, int V>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void int8_quantize_kernel(
     const void *__restrict__ x, int64_t ldx, u32x2 *__restrict__ codes, float *__restrict__ scale,
     int64_t R, int K, bool once)
 {
-    static_assert(NT == 64 || NT >= 256, "rows that share a workgroup share no barrier");
+    static_assert(NT <= 64 || NT >= 256, "rows that share a workgroup share no barrier");
     constexpr int ROWS = NT < 256 ? 256 / NT : 1, ES = elem_size<DT>();
-    __shared__ uint32_t part[NT / 64];
+    __shared__ uint32_t part[NT < 64 ? 1 : NT / 64];
     const int t = threadIdx.x % NT, pieces = K / RV;
-    const int64_t r = (int64_t)blockIdx.x * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
-    if (r >= R) // (NT < 256: waves without a row; no barrier follows there)
+    const int64_t r = (int64_t)blockIdx.x * ROWS + row_in_block<NT>();
+    if (r >= R) // (NT < 256: lanes or waves without a row; no barrier follows there)
         return;
     auto each = [&](auto f) __attribute__((always_inline)) { // f(j, p) for every piece p of this thread
 #pragma unroll
@@ -113,12 +116,20 @@ template <int DT, bool ACT>
 hipError_t launch(const void *x, int64_t ldx, int8_t *codes, float *scale, int64_t R, int K,
                   hipStream_t stream)
 {
+    if (K <= 64)
+        return launch_rows<DT, ACT, 8, 1>(x, ldx, codes, scale, R, K, stream);
+    if (K <= 128)
+        return launch_rows<DT, ACT, 16, 1>(x, ldx, codes, scale, R, K, stream);
+    if (K <= 256)
+        return launch_rows<DT, ACT, 32, 1>(x, ldx, codes, scale, R, K, stream);
     if (K <= 512)
         return launch_rows<DT, ACT, 64, 1>(x, ldx, codes, scale, R, K, stream);
+    if (K <= 1024)
+        return launch_rows<DT, ACT, 64, 2>(x, ldx, codes, scale, R, K, stream);
     if (K <= 2048)
         return launch_rows<DT, ACT, 256, 1>(x, ldx, codes, scale, R, K, stream);
     if (K <= 4096)
-        return launch_rows<DT, ACT, 512, 1>(x, ldx, codes, scale, R, K, stream);
+        return launch_rows<DT, ACT, 256, 2>(x, ldx, codes, scale, R, K, stream);
     if (K <= 8192)
         return launch_rows<DT, ACT, 512, 2>(x, ldx, codes, scale, R, K, stream);
     if (K <= 16384)
@@ -130,7 +141,8 @@ hipError_t launch(const void *x, int64_t ldx, int8_t *codes, float *scale, int64
     return launch_rows<DT, ACT, 1024, 8>(x, ldx, codes, scale, R, K, stream);
 }
 
-// Eight elements a thread: 2048 x 21504 into bf16 (132 MB) 20 us, 6.5 TB/s.
+// Eight elements a thread: 2048 x 21504 into bf16 (132 MB) 20 us, 6.5 TB/s, past the caches (26 with
+// ordinary stores).
 template <int DT>
 __global__ __launch_bounds__(256) void int8_dequant_kernel(const uint2 *__restrict__ codes,
                                                            const float *__restrict__ scale,

@@ -23,20 +23,23 @@ namespace {
 // All loads of a row are issued before the first of them is used, as far as registers reach.
 // residual_out may be residual: a thread reads its pieces before it writes them.
 //
-// 16384 x 5376 fp16 with a gate per element (881 MB) 151 us, 5.8 TB/s; 2048 x 5376 bf16 with a
-// 32-bit residual into 8 bits 28.  With y read, summed and only then the residual and the gate
-// read, and several rows a workgroup (whose addresses took 40 registers), 222 and 41.  Threads x
-// pieces for the two and one row: 256 x 3 153, 29.2, 4.5; 384 x 2 151, 29.9, 3.9; 512 x 2 152,
-// 28.2, 3.7; 1024 x 1 157, 30.4, 3.6.
+// 16384 x 5376 fp16 with a gate per element (881 MB) 138 us, 6.4 TB/s; 2048 x 5376 bf16 with a
+// 32-bit residual into 8 bits 27.  With ordinary loads and stores 151 and 28; with y read, summed
+// and only then the residual and the gate read, and several rows a workgroup (whose addresses took
+// 40 registers), 222 and 41.  Threads x pieces for the two and one row (ordinary): 256 x 3 153, 29.2, 4.5;
+// 384 x 2 151, 29.9, 3.9; 512 x 2 152, 28.2, 3.7; 1024 x 1 157, 30.4, 3.6.  Rows too short for a wave
+// share one: 65536 x 64 bf16 7.3 us with 8 threads a row, 9.5 with 16, 21.5 with 64; 65536 x 128 14.5 with
+// 16, 24.3 with 64.  32768 x 768 64 x 2 36.8, 256 x 1 45.9; 16384 x 2048 256 x 1 46.5, 64 x 4 48.5; one row of
+// 2880 512 x 1 2.7, 256 x 2 3.05.
 template <int DT, int RDT, int NT, int V>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_kernel(NormArgs a)
 {
-    static_assert(NT == 64 || NT >= 256, "rows that share a workgroup share no barrier");
+    static_assert(NT <= 64 || NT >= 256, "rows that share a workgroup share no barrier");
     constexpr int ROWS = NT < 256 ? 256 / NT : 1, ES = elem_size<DT>(), RES = elem_size<RDT>();
-    __shared__ uint32_t part[3][NT / 64];
+    __shared__ uint32_t part[3][NT < 64 ? 1 : NT / 64];
     const int t = threadIdx.x % NT, pieces = a.H / RV;
-    const int64_t row = a.row0 + (int64_t)blockIdx.x * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
-    if (row >= a.T) // (NT < 256: waves without a row; no barrier follows there)
+    const int64_t row = a.row0 + (int64_t)blockIdx.x * ROWS + row_in_block<NT>();
+    if (row >= a.T) // (NT < 256: lanes or waves without a row; no barrier follows there)
         return;
     // f(j, p) for every piece p = j NT + t of this thread
     auto each = [&](auto f) __attribute__((always_inline)) {
@@ -189,8 +192,16 @@ hipError_t launch_rows(NormArgs a, hipStream_t stream)
 template <int DT, int RDT>
 hipError_t launch(const NormArgs &a, hipStream_t stream)
 {
+    if (a.H <= 64)
+        return launch_rows<DT, RDT, 8, 1>(a, stream);
+    if (a.H <= 128)
+        return launch_rows<DT, RDT, 16, 1>(a, stream);
+    if (a.H <= 256)
+        return launch_rows<DT, RDT, 32, 1>(a, stream);
     if (a.H <= 512)
         return launch_rows<DT, RDT, 64, 1>(a, stream);
+    if (a.H <= 1024)
+        return launch_rows<DT, RDT, 64, 2>(a, stream);
     if (a.H <= 2048)
         return launch_rows<DT, RDT, 256, 1>(a, stream);
     if (a.H <= 4096)

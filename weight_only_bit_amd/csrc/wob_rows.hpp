@@ -99,8 +99,8 @@ __device__ __forceinline__ uint32_t join_halves(uint32_t v, F f)
     }
 }
 
-// f over the NT threads that share a row, the result in every one of them.  NT = 64: a
-// wave; more: the waves' results meet in `part` (NT / 64 words of LDS that nothing else
+// f over the NT threads that share a row, the result in every one of them.  NT = 16, 32, 64: lanes of
+// a wave; more: the waves' results meet in `part` (NT / 64 words of LDS that nothing else
 // is read from until the next barrier).
 template <int NT, class F>
 __device__ __forceinline__ uint32_t row_reduce(uint32_t v, uint32_t *part, F f)
@@ -108,9 +108,12 @@ __device__ __forceinline__ uint32_t row_reduce(uint32_t v, uint32_t *part, F f)
     v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));  // lane ^ 1
     v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));  // lane ^ 2
     v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true)); // 7 - lane of 8
-    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true)); // 15 - lane of 16
-    v = join_halves<16>(v, f);
-    v = join_halves<32>(v, f);
+    if constexpr (NT > 8)
+        v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true)); // 15 - lane of 16
+    if constexpr (NT > 16)
+        v = join_halves<16>(v, f);
+    if constexpr (NT > 32)
+        v = join_halves<32>(v, f);
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0)
             part[threadIdx.x >> 6] = v;
@@ -135,6 +138,14 @@ __device__ __forceinline__ float row_sum(float v, uint32_t *part)
     return bitcast<float>(row_reduce<NT>(bitcast<uint32_t>(v), part, [](uint32_t a, uint32_t b) {
         return bitcast<uint32_t>(bitcast<float>(a) + bitcast<float>(b));
     }));
+}
+
+// The row of this thread in its workgroup: uniform in a wave where a wave has no more than one.
+template <int NT>
+__device__ __forceinline__ int row_in_block()
+{
+    const int r = threadIdx.x / NT;
+    return NT < 64 ? r : __builtin_amdgcn_readfirstlane(r);
 }
 
 // The largest magnitude as a bit pattern (magnitudes order as their patterns do, NaN
