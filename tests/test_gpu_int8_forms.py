@@ -30,13 +30,13 @@ FORMS = {
     ("narrow", False): [(17, 8, 16), (40, 2048, 496), (64, 16328, 656)],
     ("narrow", True): [(17, 8, 2016), (17, 72, 1936), (33, 5000, 2896), (100, 2000, 4112), (16, 5376, 21504), (40, 2000, 8192), (33, 1000, 16400)],
     ("small", False): [(71, 9064, 16), (100, 16000, 1040), (129, 8100 // 8 * 8, 2064)],
-    ("small", True): [(1094, 264, 7728), (126, 3240, 19808)],
+    ("small", True): [(1094, 264, 7728), (103, 5320, 6768)],
     ("medium", False): [(17, 18136, 16), (200, 16376, 1040), (500, 8184, 2000)],
     ("medium", True): [(100, 5368, 21520), (250, 5376, 8208)],
     # weights that are copied nontemporally
     ("narrow once", False): [(33, 65584, 2064), (61, 11952, 11232)],
     ("narrow once", True): [(17, 6056, 22224)],
-    ("small once", False): [(110, 14424, 9440)],
+    ("small once", False): [(113, 15816, 8512)],
     ("medium once", False): [(100, 27120, 4960)],
     ("medium once", True): [(105, 5728, 23440)],
     ("wide", False): [(133, 18512, 16), (511, 16376, 1040), (1000, 8184, 2064)],

@@ -615,7 +615,7 @@ using TileN = Int8Tile<2, 1, 1, 2, 11>; // 64 x 64
 //          less on an empty card, but at least the weights' bytes;
 //   parts: their sum's launch and its bytes;
 //   few rows: the weights' bytes and the staging of x by a CU's workgroups.
-// On average the choice is 0.4 % slower than the best form and parts measured, at worst 14 % (1 x 28672
+// On average the choice is 0.6 % slower than the best form and parts measured, at worst 15 % (1 x 28672
 // x 8192, few rows 48 us, 64 x 64 42).
 enum class Path { Few, Large, Wide, Medium, Small, Narrow };
 
@@ -649,7 +649,7 @@ struct TileCost {
 };
 constexpr TileCost TILE_COSTS[] = {
     {Path::Large, TileL::TN, TileL::TM, 7.9f, 13.f, 0.24f},  {Path::Wide, TileW::TN, TileW::TM, 6.2f, 7.9f, 0.21f},
-    {Path::Medium, TileM::TN, TileM::TM, 5.4f, 5.1f, 0.19f}, {Path::Small, TileS::TN, TileS::TM, 4.6f, 3.6f, 0.17f},
+    {Path::Medium, TileM::TN, TileM::TM, 5.4f, 5.1f, 0.17f}, {Path::Small, TileS::TN, TileS::TM, 4.6f, 3.6f, 0.17f},
     {Path::Narrow, TileN::TN, TileN::TM, 3.4f, 2.4f, 0.17f},
 };
 constexpr int MOST_PARTS = 16, PART_K = 512; // parts, at most; k of a part, at least
