@@ -8,7 +8,7 @@
 // instruction is free as long as both operands agree.
 //
 // Two kernels:
-//  * few rows (M <= 16): waves own 16 weight rows each and may split K; the weights go
+//  * few rows (M <= 16): waves own 8 or 16 weight rows each and may split K; the weights go
 //    from memory straight into registers (v_mfma_i32_16x16x64_i8); bound by their bytes.
 //  * tiles: both operands through LDS (v_mfma_i32_32x32x32_i8), K optionally split over
 //    workgroups with a sum in a second kernel.
@@ -66,7 +66,12 @@ __device__ __forceinline__ float4_t scaled4(const i32x4 &sum, float xs, const fl
 // 8 with the halves swapped, so lanes r < 8 of the one and r >= 8 of the other are rows 0 to 15 with the
 // first half, and the rest are rows r ^ 8 with the second.
 //
-// Nothing reads a line twice, so the loads are nontemporal.
+// Bound by the weights' bytes: 1 x 16384 x 5376 (88 MB) 16.3 us, a plain read of as many 14.7 to 15.2;
+// 1 x 43008 x 5376 (231 MB) 40, a read 33.6; 13 x 5760 x 2880 (17 MB) 7.0, a read 3.9 (graph replays over
+// copies larger than the caches).  With half lines of 16 rows a load 17.8, 48 and 7.3.  Nothing reads a
+// line twice, so the loads are nontemporal: past the caches / with three sets of weights 8 x 16384 x
+// 5376 19.6 / 18.3, ordinary 20.9 / 17.2; 4 x 10752 x 5376 15.2 / 14.6, 16.5 / 13.1; 13 x 5760 x 2880 7.1 /
+// 6.5, 7.8 / 6.9.
 constexpr int FR_D = 6; // loads ahead
 
 __host__ __device__ inline int few_pitch(int K) { return (K + 127 - 16) / 128 * 128 + 16; }
@@ -209,7 +214,7 @@ hipError_t launch_few(const Int8GemmArgs &a, int M, int N, int K, int rows, hipS
 // 21.8, 9 18.7, 10 21.6, 11 18.5, 13 18.7; 100 x 5376 x 21504 in the 128 x 128 tile 6 34.6, 7 33.6, 8 34.5, 9 33.2.
 //
 // 2048 x 16384 x 5376, 150 to 165 us (2.2 to 2.4 POPS; the library's product of the operands without
-// scales 164): the power limit.  MFMA busy 63 % at 1.7 GHz; with zero codes, which switch nothing,
+// scales 164): the power limit.  MFMA busy 61 % at 1.75 GHz; with zero codes, which switch nothing,
 // the same launches take 117, and an order of reads and copies that takes 4 off that takes
 // nothing off this.  Timing-only forms: no stores 148 to 158, no copies 142 to 149, neither 121 to
 // 127, the MFMAs alone, from registers, 108 (72 at 2.4 GHz).
