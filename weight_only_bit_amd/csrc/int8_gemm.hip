@@ -234,6 +234,27 @@ struct Int8Tile {
     static_assert(NH % 2 == 0 || TN == TM, "halves of one size");
 };
 
+// lds_dma16, or the same with a nontemporal load.
+template <bool NT>
+__device__ __forceinline__ void copy_weights(const int8_t *w, uint32_t at, uint32_t lds_addr)
+{
+    if constexpr (!NT) {
+        lds_dma16(w, at, lds_addr);
+    } else {
+        const uint64_t b = reinterpret_cast<uint64_t>(w); // uniform: in scalar registers
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+        uint32_t saved;
+        asm volatile("s_mov_b32 %0, m0\n\t"
+                     "s_mov_b32 m0, %1\n\t"
+                     "global_load_lds_dwordx4 %2, %3 nt\n\t"
+                     "s_mov_b32 m0, %0"
+                     : "=&s"(saved)
+                     : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(at), "s"((uint64_t)hi << 32 | lo)
+                     : "memory");
+    }
+}
+
 // A wave's outputs (n from nw, m from mw) through its part of LDS, 32 output rows at a
 // time: rows of 32 NB n are written as the accumulators hold them (acc[i][k][4 g + e] is n =
 // 32 i + 8 g + 4 h + e, m = 32 k + r) and read back 16 bytes a lane, so a store covers
@@ -366,7 +387,7 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
         if (b_rows)
             lds_dma16(a.x, row_at[i] + k, lds0 + (uint32_t)to);
         else
-            lds_dma16<NT>(a.w, row_at[i] + k, lds0 + (uint32_t)to);
+            copy_weights<NT>(a.w, row_at[i] + k, lds0 + (uint32_t)to);
     };
 
     i32x16 acc[T::NB][T::MB] = {};

@@ -154,8 +154,6 @@ __device__ __forceinline__ void barrier_only()
 // or LDS read is used, which serializes the software pipeline.  The hardware
 // tracks the DMA with vmcnt only; every caller waits for it explicitly
 // (s_waitcnt vmcnt) before the destination is read.  M0 is saved and restored.
-// NT: nontemporal, for bytes that nothing reads again.
-template <bool NT = false>
 __device__ __forceinline__ void lds_dma16(const void *sbase_any, uint32_t voff, uint32_t lds_addr)
 {
     // the base must live in scalar registers: make its (uniform) value explicit
@@ -166,22 +164,13 @@ __device__ __forceinline__ void lds_dma16(const void *sbase_any, uint32_t voff, 
     const uint64_t bu = ((uint64_t)hi << 32) | (uint64_t)lo;
     const void *sbase = reinterpret_cast<const void *>(bu);
     uint32_t saved;
-    if constexpr (NT)
-        asm volatile("s_mov_b32 %0, m0\n\t"
-                     "s_mov_b32 m0, %1\n\t"
-                     "global_load_lds_dwordx4 %2, %3 nt\n\t"
-                     "s_mov_b32 m0, %0"
-                     : "=&s"(saved)
-                     : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(voff), "s"(sbase)
-                     : "memory");
-    else
-        asm volatile("s_mov_b32 %0, m0\n\t"
-                     "s_mov_b32 m0, %1\n\t"
-                     "global_load_lds_dwordx4 %2, %3\n\t"
-                     "s_mov_b32 m0, %0"
-                     : "=&s"(saved)
-                     : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(voff), "s"(sbase)
-                     : "memory");
+    asm volatile("s_mov_b32 %0, m0\n\t"
+                 "s_mov_b32 m0, %1\n\t"
+                 "global_load_lds_dwordx4 %2, %3\n\t"
+                 "s_mov_b32 m0, %0"
+                 : "=&s"(saved)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(voff), "s"(sbase)
+                 : "memory");
 }
 
 // One MFMA of a BR x BR block: A = 8 weight values of row nl (slot g), B = 8
