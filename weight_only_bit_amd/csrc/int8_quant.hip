@@ -15,19 +15,25 @@ namespace wob {
 
 namespace {
 
-// silu(g) * u with the hardware's exponential and reciprocal (2^-22 each; a division's ten more
-// operations an element would be on the path of the loads).  exp overflows to infinity for
-// large negative g, where the result is -0.
+// silu(g) * u in binary32: e^-g by the hardware's 2^t, with the rounding of t = -g log2 e made good by one
+// term of the exponential (alone it costs 2^-24 |g|), and the hardware's reciprocal.  Both are off by 2^-23 at
+// most, the whole by 9.5 * 2^-24.  t stays below 128, past which the added term takes e to infinity.
+// 1 / (1 + e) leaves binary32's normal numbers, which the reciprocal does not, from g = -87.3 on:
+// it is taken 4 times as large, and g a quarter, which is exact from 2^-124 on.
 __device__ __forceinline__ float silu_mul(float g, float u)
 {
-    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+    const float t = __builtin_amdgcn_fmed3f(g * -1.44269504f, -200.f, 127.99999f);
+    const float rest = __builtin_fmaf(t, 1.90465421e-9f, __builtin_fmaf(t, -0.693147182f, -g)); // -g - t ln 2
+    float e = __builtin_amdgcn_exp2f(t);
+    e = __builtin_fmaf(e, rest, e);
+    return 0.25f * g * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0.25f, 0.25f)) * u;
 }
 
 // NT threads share a row, V pieces of eight elements a thread: piece j of thread t is j NT + t.
 // All loads of a row are issued before the first of them is used, as far as registers reach.
 //
-// 2048 x 21504 bf16 gated (220 MB) 36 us, 6.0 TB/s, with 512 x 6 (42 when read ordinarily; then 1024 x 3 and
-// x 4 45 to 47, 768 x 4 46, 512 x 8 46).  Rows too short for a wave share one: 65536 x 16 bf16 3.5 us with
+// 2048 x 21504 bf16 gated (220 MB) 38 to 40 us, 5.6 TB/s, with 512 x 6 (36 to 38 with the bare exponential and
+// reciprocal in silu_mul; then 42 when read ordinarily, 1024 x 3 and x 4 45 to 47, 768 x 4 46, 512 x 8 46).  Rows too short for a wave share one: 65536 x 16 bf16 3.5 us with
 // 8 threads a row, 4.9 with 16, 12.4 with 64; 65536 x 128 7.6 with 16, 15.7 with 64.  Longer ones, us:
 // 32768 x 768 64 x 2 16.0, 256 x 1 25.9; 8192 x 2208 256 x 2 13.2, 512 x 1 17.3, one row of 2880 2.3 and
 // 2.2; 2048 x 5376 512 x 2 8.5, 256 x 3 8.4, one row 2.3 and 2.5.
