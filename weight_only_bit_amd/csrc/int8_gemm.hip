@@ -322,7 +322,7 @@ __device__ __forceinline__ void store_wave(const i32x16 (&acc)[T::NB][T::MB], vo
     }
 }
 
-// NT: weights are copied nontemporally.
+// NT: weights are copied nontemporally, but for the halves that fill the ring at the start (see launch_once).
 template <class T, bool NT>
 __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__restrict__ part, int M, int N, int K,
                                                         int tiles_m, int tiles, int splits, int nxcd)
@@ -376,7 +376,7 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
     // Copy d of those into the places of group g, once they are free: the next halves of the
     // sequence that are not in LDS, A and B of group g + NH / 2 (NH odd: B of that one and A of
     // the one after it).
-    auto copy = [&](int g, const Place &p, int d) __attribute__((always_inline)) {
+    auto copy = [&](int g, const Place &p, int d, auto nt) __attribute__((always_inline)) {
         const bool second = d >= (ODD ? ND / 2 : NDA); // into place b
         const bool b_rows = ODD ? !second : second;
         const int i = ODD ? (second ? d - ND / 2 : d + ND / 2) : d;
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
         if (b_rows)
             lds_dma16(a.x, row_at[i] + k, lds0 + (uint32_t)to);
         else
-            copy_weights<NT>(a.w, row_at[i] + k, lds0 + (uint32_t)to);
+            copy_weights<decltype(nt)::value>(a.w, row_at[i] + k, lds0 + (uint32_t)to);
     };
 
     i32x16 acc[T::NB][T::MB] = {};
@@ -437,13 +437,13 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
             for (int g = 0; g < NH / 2 - 1; ++g) {
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
-                    copy(g - NH / 2, p, d);
+                    copy(g - NH / 2, p, d, std::false_type{});
                 p = following(p);
             }
         }
 #pragma unroll
         for (int d = 0; d < part_of(1); ++d)
-            copy(-1, before, d);
+            copy(-1, before, d, std::bool_constant<NT>{});
         wait_vmcnt<(NH - 4) * ND / 2 + part_of(1)>(); // group 0 has landed
     }
     barrier_only();
@@ -483,7 +483,7 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
                 if (i < READS)
                     read_operand(END ? after : now_at, END ? 0 : S + 1, i, next);
                 else
-                    copy(END ? g : g - 1, END ? now_at : before, C0 + i - READS);
+                    copy(END ? g : g - 1, END ? now_at : before, C0 + i - READS, std::bool_constant<NT>{});
             };
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
@@ -727,6 +727,10 @@ Plan plan(int64_t M, int64_t N, int64_t K)
 // copied nontemporally.  us, ordinary and nontemporal, past the caches / three sets of weights: 32 x 43008
 // x 5376 54.4, 50.8 / 53.3, 48.5; 100 x 43008 x 5376 65.1, 61.4 / 64.7, 61.5; but 64 x 16384 x 5376 23.7, 22.8 /
 // 17.8, 21.4; 100 x 8192 x 5376 19.8, 21.3 / 17.2, 20.8; two tiles: 200 x 16384 x 5376 33.1, 34.7.
+// The halves that fill the ring at the start are ordinary copies in every tile.  Past the caches, ordinary, all
+// nontemporal, all but those: 64 x 64 tile 40 x 131072 x 4096 125.2, 117.3, 107.1, 64 x 26624 x 5376 40.1, 38.1, 36.9; 128 x
+// 128 100 x 131072 x 4096 139.6, 133.9, 125.3, 100 x 262144 x 624 (lines that two groups share) 75.4, 90.7, 74.0; 64 x 128
+// 100 x 131072 x 4096 152.3, 147.2, 139.4, 100 x 262144 x 624 98.4, 113.4, 97.4.
 template <class T>
 hipError_t launch_once(const Int8GemmArgs &a, int M, int N, int K, int splits, void *workspace, hipStream_t stream)
 {
