@@ -4,7 +4,7 @@ import numpy as np
 
 F = np.float32
 # path, weight rows, activation rows, us a round, us a round and 1000 k, us a million bytes of weights
-TILES = (("large", 256, 256, 7.9, 13.0, 0.24), ("wide", 256, 128, 6.2, 7.9, 0.21), ("medium", 128, 128, 5.4, 5.1, 0.17),
+TILES = (("large", 256, 256, 7.9, 13.0, 0.24), ("wide", 256, 128, 6.2, 7.9, 0.21), ("medium", 128, 128, 5.4, 5.1, 0.19),
          ("small", 64, 128, 4.6, 3.6, 0.17), ("narrow", 64, 64, 3.4, 2.4, 0.17))
 
 

@@ -635,14 +635,15 @@ using TileN = Int8Tile<2, 1, 1, 2, 11>; // 64 x 64
 // ---- Choice ----------------------------------------------------------------
 //
 // The form and its K parts are the ones with the smallest estimate, in us, from what was measured
-// (graph replays over copies larger than the caches, 5600 triples of a shape, a form and parts, M 1 to
-// 2048, N x K of 512 x 512 to 65528 x 16384):
+// (graph replays over copies larger than the caches, 5200 triples of a shape, a form and parts, M 1 to
+// 2048, N x K of 512 x 512 to 65528 x 16384; profiles/int8_product_forms.txt):
 //   tiles: rounds of 256 workgroups, each `start` and `per_k` a 1000 k of a part, the latter a third
 //          less on an empty card, but at least the weights' bytes;
 //   parts: their sum's launch and its bytes;
 //   few rows: the weights' bytes and the staging of x by a CU's workgroups.
-// On average the choice is 0.6 % slower than the best form and parts measured, at worst 15 % (1 x 28672
-// x 8192, few rows 48 us, 64 x 64 42).
+// On average the choice is 0.9 % slower than the best form and parts measured, at worst 21 % (2 x 28672
+// x 8192, few rows 8 x 1 49 us, 4 x 1 40).  The 128 x 128 tile's bytes at 0.17, 0.18, 0.19, 0.20, 0.21 us a million: 1.3 %,
+// 1.0, 0.9, 0.9, 1.0 on average, 30 % at worst, then 21.
 enum class Path { Few, Large, Wide, Medium, Small, Narrow };
 
 struct Plan {
@@ -675,7 +676,7 @@ struct TileCost {
 };
 constexpr TileCost TILE_COSTS[] = {
     {Path::Large, TileL::TN, TileL::TM, 7.9f, 13.f, 0.24f},  {Path::Wide, TileW::TN, TileW::TM, 6.2f, 7.9f, 0.21f},
-    {Path::Medium, TileM::TN, TileM::TM, 5.4f, 5.1f, 0.17f}, {Path::Small, TileS::TN, TileS::TM, 4.6f, 3.6f, 0.17f},
+    {Path::Medium, TileM::TN, TileM::TM, 5.4f, 5.1f, 0.19f}, {Path::Small, TileS::TN, TileS::TM, 4.6f, 3.6f, 0.17f},
     {Path::Narrow, TileN::TN, TileN::TM, 3.4f, 2.4f, 0.17f},
 };
 constexpr int MOST_PARTS = 16, PART_K = 512; // parts, at most; k of a part, at least
