@@ -1,4 +1,5 @@
-"""What the assembly of the 8-bit product shows beyond its waits (CPU: compiles to gfx950 assembly)."""
+"""What the assembly of the 8-bit product, the row kernels and the group-limited choice shows beyond the
+tiles' waits (CPU: compiles to gfx950 assembly)."""
 import re
 
 from tests.test_block_forms import TILE, TILES, assembly, needs_hipcc  # noqa: F401 (a fixture)
@@ -30,3 +31,11 @@ def test_weight_copies_after_the_first_are_nontemporal(assembly):  # noqa: F811
         assert len(lines) == first + later + rows and marked == (later if nt else 0), tile
         seen += 1
     assert seen == len(TILES)
+
+
+@needs_hipcc
+def test_no_kernel_keeps_a_row_in_scratch_memory(assembly):  # noqa: F811
+    for src, text in assembly.items():
+        kernels = re.findall(r"^; Kernel info:.*?^; ScratchSize: (\d+)", text, re.M | re.S)
+        assert kernels and len(kernels) == text.count(".amdhsa_kernel "), src
+        assert all(size == "0" for size in kernels) and "scratch_" not in text, src

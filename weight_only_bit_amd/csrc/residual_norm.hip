@@ -41,13 +41,14 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_kernel(Norm
     const int64_t row = a.row0 + (int64_t)blockIdx.x * ROWS + row_in_block<NT>();
     if (row >= a.T) // (NT < 256: lanes or waves without a row; no barrier follows there)
         return;
-    // f(j, p) for every piece p = j NT + t of this thread
-    auto each = [&](auto f) __attribute__((always_inline)) {
+    // f(j, p) for every piece p = j NT + t of this thread, or for those from j0 on before j1
+    auto some = [&](int j0, int j1, auto f) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if (j * NT + t < pieces)
+            if (j >= j0 && j < j1 && j * NT + t < pieces)
                 f(j, j * NT + t);
     };
+    auto each = [&](auto f) __attribute__((always_inline)) { some(0, V, f); };
     auto row_of = [&](const void *base, int64_t ld, int size) __attribute__((always_inline)) {
         return static_cast<const uint8_t *>(base) + row * ld * size;
     };
@@ -104,23 +105,31 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_kernel(Norm
                     h[j][i] *= rstd * w[i];
             });
         }
-        if (!GATE_EARLY && a.gate)
-            load_gate(std::false_type{});
-        each([&](int j, int) {
-            float v[RV];
-            unpack8<RDT>(r[j], v);
-            if (a.gate) {
-                float g[RV];
-                unpack8<DT>(gate[j], g);
+        // A gate that is not here yet comes two pieces at a time: with all of them 24 registers went through
+        // memory (1024 x 32768 binary32 with a gate per element and both norms 155 us, now 144, one row 13.2, 10.6).
+        constexpr int STEP = GATE_EARLY ? V : 2;
 #pragma unroll
-                for (int i = 0; i < RV; ++i)
-                    h[j][i] = __builtin_fmaf(a.alpha * g[i], h[j][i], v[i]);
-            } else {
+        for (int j0 = 0; j0 < V; j0 += STEP) {
+            if (!GATE_EARLY && a.gate)
+                some(j0, j0 + STEP, [&](int j, int p) {
+                    load_raw8<DT>(row_of(a.gate, a.ldg, ES) + (uint32_t)(p * RV) * ES, gate[j]);
+                });
+            some(j0, j0 + STEP, [&](int j, int) {
+                float v[RV];
+                unpack8<RDT>(r[j], v);
+                if (a.gate) {
+                    float g[RV];
+                    unpack8<DT>(gate[j], g);
 #pragma unroll
-                for (int i = 0; i < RV; ++i)
-                    h[j][i] = __builtin_fmaf(a.alpha, h[j][i], v[i]);
-            }
-        });
+                    for (int i = 0; i < RV; ++i)
+                        h[j][i] = __builtin_fmaf(a.alpha * g[i], h[j][i], v[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < RV; ++i)
+                        h[j][i] = __builtin_fmaf(a.alpha, h[j][i], v[i]);
+                }
+            });
+        }
     } else {
         each([&](int j, int) { unpack8<RDT>(r[j], h[j]); });
     }
