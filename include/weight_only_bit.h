@@ -395,8 +395,8 @@ int int8_dequant(const int8_t *codes, const float *scale, void *out, int out_dty
                  int64_t K, void *stream);
 
 /*
- * Bytes of device workspace int8_gemm needs (0 when it needs none, and for
- * arguments it refuses on sight: a negative size, K outside 16 .. 131056).
+ * Bytes of device workspace int8_gemm needs (0 when it needs none, and for every
+ * shape that it refuses).
  */
 size_t int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
 

@@ -668,13 +668,18 @@ namespace {
 
 constexpr int64_t INT8_K = 131056; // the largest K % 16 == 0 whose sums of (-128)^2 stay below 2^31
 
+// Shapes that int8_gemm takes: whole pieces, and 32-bit in-kernel offsets into each operand's codes.
+bool int8_gemm_shape(int64_t M, int64_t N, int64_t K)
+{
+    return M >= 0 && N >= 0 && K >= 16 && K <= INT8_K && K % 16 == 0 && N % 8 == 0 && M < GEMM_ROWS &&
+           N < GEMM_ROWS && M * K <= (int64_t)UINT32_MAX && N * K <= (int64_t)UINT32_MAX;
+}
+
 } // namespace
 
 size_t int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K)
 {
-    if (M < 0 || N < 0 || K < 16 || M >= GEMM_ROWS || N >= GEMM_ROWS || K > INT8_K)
-        return 0;
-    return wob::int8_gemm_workspace_bytes(M, N, K);
+    return int8_gemm_shape(M, N, K) ? wob::int8_gemm_workspace_bytes(M, N, K) : 0;
 }
 
 int int8_gemm(const int8_t *x_q, const float *x_scale, const int8_t *w_q, const float *w_scale,
@@ -683,15 +688,15 @@ int int8_gemm(const int8_t *x_q, const float *x_scale, const int8_t *w_q, const 
 {
     if (!value_dtype(y_dtype))
         return fail(WOB_DTYPE, "y dtype tag %d is not F16, BF16 or F32", y_dtype);
-    if (M < 0 || N < 0 || K < 16 || K > INT8_K)
-        return fail(WOB_INVALID_ARG, "bad shape M=%lld N=%lld K=%lld", (long long)M, (long long)N,
-                    (long long)K);
-    if (K % 16 != 0 || N % 8 != 0)
-        return fail(WOB_INVALID_ARG, "need K %% 16 == 0 and N %% 8 == 0 (K=%lld N=%lld)",
-                    (long long)K, (long long)N);
-    // 32-bit in-kernel offsets into each operand's codes
-    if (M >= GEMM_ROWS || N >= GEMM_ROWS || M * K > (int64_t)UINT32_MAX || N * K > (int64_t)UINT32_MAX)
+    if (!int8_gemm_shape(M, N, K)) {
+        if (M < 0 || N < 0 || K < 16 || K > INT8_K)
+            return fail(WOB_INVALID_ARG, "bad shape M=%lld N=%lld K=%lld", (long long)M, (long long)N,
+                        (long long)K);
+        if (K % 16 != 0 || N % 8 != 0)
+            return fail(WOB_INVALID_ARG, "need K %% 16 == 0 and N %% 8 == 0 (K=%lld N=%lld)",
+                        (long long)K, (long long)N);
         return fail(WOB_INVALID_ARG, "shape too large");
+    }
     if (M == 0 || N == 0)
         return ok();
     if (!x_q || !x_scale || !w_q || !w_scale || !y)
