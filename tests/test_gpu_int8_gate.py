@@ -61,3 +61,15 @@ def test_gates_past_the_exponential(wob):
     assert (s[:6] == 0).all() and (codes[:6] == 0).all()
     want = np.array([float(g[6]), 2.0 ** 101, 2.0 ** -99, 2.0 ** -99]).astype(np.float32) / np.float32(127)
     assert (np.abs(s[6:] - want) <= BOUND * want).all() and (np.abs(codes[6:]) == 127).all()
+
+
+@pytest.mark.parametrize("dtype", ("fp32", "bf16", "fp16"))
+def test_gates_that_are_not_finite(wob, dtype):
+    """An infinite gate or a NaN, whatever the up value: the row reads back as NaN, its neighbours do not."""
+    torch = torch_mod()
+    x = torch.ones((7, 2 * 528), dtype=_dt(dtype), device="cuda")
+    x[1, 5], x[3, 527], x[5, 0] = float("inf"), float("-inf"), float("nan")
+    x[5, 528] = 0
+    codes, s = wob.int8_quantize(x, act=wob.ACT_SILU_MUL)
+    assert torch.isnan(s).tolist() == [False, True, False, True, False, True, False]
+    assert (codes[1::2] == 0).all() and (codes[::2] == 127).all()
