@@ -18,11 +18,13 @@
 // its lanes.  c is held as an unsigned key of the same order, 0 for an expert that cannot
 // be chosen.
 //
-// Bound by the vector ALU: 16384 tokens of 256 experts 14.4 us (17 MB, a read of which takes 3.9),
-// about 1000 operations of four tokens, 420 of them the 64-bit scores; 4096 of 160 6.8; one
-// token 3.8, the chain of its places.  A wave a token with library exponentials and divisions, groups
-// through LDS and the places searched in all registers 27 us, four tokens a wave 16.2, sorted lists
-// 13.9 to 14.4.
+// 16384 tokens of 256 experts 14.7 us (17 MB, a read of which takes 3.9): half of it is the vector ALU, about 1000
+// operations of four tokens, some 440 of them the 64-bit scores, and half is left when scores, groups, places and
+// sort are all taken out: 1024 workgroups, the four that a CU has room for, load, go through LDS (1.6
+// conflict cycles an instruction) and write at the same time, and nothing overlaps.  4096 of 160 6.5 to 6.8;
+// one token 3.8, the chain of its places.  A wave a token with library exponentials and divisions,
+// groups through LDS and the places searched in all registers 27 us, four tokens a wave 16.2, sorted
+// lists 13.9 to 14.4 (14.7 with the exponential's argument unrounded).
 #include "moe_choice.hpp"
 #include "weight_only_bit.h"
 #include "wob_rows.hpp"
@@ -46,9 +48,10 @@ struct RouteSplit { // how a token's experts lie in its lanes
 // nodes: off by 2^-50 of the value at most, and by nothing at f = 0.  f is formed with the low part of log2 e
 // and without a rounding of the product: rounded to 64 bits first, it cost up to 2^-47 of the value
 // where |x| passes 44, a rounded difference of a softmax as much again.  16384 tokens of 256 experts, binary32,
-// 14.9 us (14.5 without), softmax 15.5 (14.35 without).
+// 14.7 us (14.6 without), softmax 15.6 (14.5 without).
 constexpr double LOG2E = 1.44269504088896340736, LOG2E_LOW = 2.0355273740931033e-17;
 
+template <bool LOW = false>
 __device__ __forceinline__ double exp_64(double x, double low = 0.0)
 {
     constexpr double Q[10] = {0.6931471805599462,    0.24022650695910075,   0.05550410866465167,
@@ -56,7 +59,9 @@ __device__ __forceinline__ double exp_64(double x, double low = 0.0)
                               1.5252672924850737e-05, 1.3215451633221434e-06, 1.0205905413765595e-07,
                               7.070977866508138e-09};
     const double n = __builtin_rint(x * LOG2E);
-    const double f = __builtin_fma(low, LOG2E, __builtin_fma(x, LOG2E_LOW, __builtin_fma(x, LOG2E, -n)));
+    double f = __builtin_fma(x, LOG2E_LOW, __builtin_fma(x, LOG2E, -n));
+    if constexpr (LOW)
+        f = __builtin_fma(low, LOG2E, f);
     double q = Q[9];
 #pragma unroll
     for (int i = 8; i >= 0; --i)
@@ -185,7 +190,7 @@ struct SortNet {
 template <int DT, int L, int V, bool QUAD>
 __global__ __launch_bounds__(route_threads<V>()) void moe_route_kernel(RouteArgs a, RouteSplit split)
 {
-    constexpr int RT = route_threads<V>(), PITCH = V + (V >= 4 ? 4 : 1); // (lanes' rows in different banks)
+    constexpr int RT = route_threads<V>(), PITCH = V + (V >= 4 ? 4 : 1); // (neighbours' rows start in other banks)
     __shared__ __align__(16) uint32_t keys[RT * PITCH];
     __shared__ __align__(16) float scores[RT * PITCH];
     const int g = threadIdx.x % L, t = blockIdx.x * (RT / L) + threadIdx.x / L;
@@ -242,7 +247,7 @@ __global__ __launch_bounds__(route_threads<V>()) void moe_route_kernel(RouteArgs
             const double a = (double)l[v], d = a - (double)top, b = d - a;
             const double low = (a - (d - b)) + (-(double)top - b);
             const bool near = d > -693.0; // (not for infinities)
-            q[v] = exp_64(l[v] == top ? 0.0 : near ? d : -693.0, near ? low : 0.0);
+            q[v] = exp_64<true>(l[v] == top ? 0.0 : near ? d : -693.0, near ? low : 0.0);
             sum += q[v];
         }
         const double r = recip_64(lanes_sum64<L>(sum)); // (1 or more; of a row without an expert nothing is used)
