@@ -54,9 +54,10 @@ __device__ __forceinline__ float4_t scaled4(const i32x4 &sum, float xs, const fl
 //
 // M <= 16.  A wave owns 8 weight rows, with M > 8 (WIDE) 16; W waves share them and split K,
 // and their sums are joined in LDS.  A workgroup has G such groups of rows.  The weights go from
-// memory into registers, FR_D loads of a lane ahead; only x passes through LDS (pitch 16 mod 128
-// bytes, which makes its reads conflict-free), with its loads ahead of the weights' so that they
-// land first.
+// memory into registers, FR_D loads of a lane ahead; only x passes through LDS, with its loads ahead of the
+// weights' so that they land first.  Its pitch is 16 mod 128 bytes: the same piece of all rows lies in
+// different banks, but neighbouring pieces of neighbouring rows meet (2.3 conflict cycles a LDS instruction
+// with 13 rows, none with one, whose reads are the same in every lane).
 //
 // A load is one whole cache line of each of 8 weight rows: lane (r, q) = (lane % 16, lane / 16)
 // holds piece 4 (r / 8) + q of the line of row r % 8.  With up to 8 activation rows that is the
@@ -68,7 +69,8 @@ __device__ __forceinline__ float4_t scaled4(const i32x4 &sum, float xs, const fl
 //
 // Bound by the weights' bytes: 1 x 16384 x 5376 (88 MB) 16.3 us, a plain read of as many 14.7 to 15.2;
 // 1 x 43008 x 5376 (231 MB) 40, a read 33.6; 13 x 5760 x 2880 (17 MB) 7.0, a read 3.9 (graph replays over
-// copies larger than the caches).  With half lines of 16 rows a load 17.8, 48 and 7.3.  Nothing reads a
+// copies larger than the caches; in the last of them a workgroup stages 37 KB of x for 69 KB of weights
+// before its first product).  With half lines of 16 rows a load 17.8, 48 and 7.3.  Nothing reads a
 // line twice, so the loads are nontemporal: past the caches / with three sets of weights 8 x 16384 x
 // 5376 19.6 / 18.3, ordinary 20.9 / 17.2; 4 x 10752 x 5376 15.2 / 14.6, 16.5 / 13.1; 13 x 5760 x 2880 7.1 /
 // 6.5, 7.8 / 6.9.
@@ -564,8 +566,8 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8GemmArgs a, int *__r
         store(std::false_type{});
 }
 
-// y from the sum of the K parts; n4 = N / 4.  100 x 5376 in six parts 4.5 us (14 MB; all parts loaded
-// at once instead of four at a time 4.5).
+// y from the sum of the K parts; n4 = N / 4.  100 x 5376 in five parts 4.3 to 4.9 us (12 MB), in six 4.5 (all
+// of them loaded at once instead of four at a time 4.5).
 __global__ __launch_bounds__(256) void int8_sum_kernel(Int8GemmArgs a, const i32x4 *__restrict__ part, int64_t total4,
                                                        int n4, int splits)
 {

@@ -30,7 +30,8 @@ __device__ __forceinline__ float silu_mul(float g, float u)
 }
 
 // NT threads share a row, V pieces of eight elements a thread: piece j of thread t is j NT + t.
-// All loads of a row are issued before the first of them is used, as far as registers reach.
+// All loads of a row are issued before the first of them is used where they take fewer than 64 registers of a
+// thread, else piece by piece.
 //
 // 2048 x 21504 bf16 gated (220 MB) 38 to 40 us, 5.6 TB/s, with 512 x 6 (36 to 38 with the bare exponential and
 // reciprocal in silu_mul; then 42 when read ordinarily, 1024 x 3 and x 4 45 to 47, 768 x 4 46, 512 x 8 46).  Rows too short for a wave share one: 65536 x 16 bf16 3.5 us with
@@ -86,7 +87,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void int8_quantize_kernel(
             });
         }
     };
-    if (once) // x is in no cache
+    if (once) // nontemporally (see launch_rows)
         read(std::true_type{});
     else
         read(std::false_type{});
@@ -103,7 +104,7 @@ hipError_t launch_rows(const void *x, int64_t ldx, int8_t *codes, float *scale, 
     constexpr int ROWS = NT < 256 ? 256 / NT : 1;
     constexpr int64_t MOST = (int64_t)1 << 21; // rows of a launch: 2^31 threads at most
     // Rows that the last-level cache (256 MB) cannot hold are read nontemporally, gated ones from half of it
-    // on.  us, ordinary and nontemporal, x in the caches before / not: gated 84 MB 18.5, 19.0 / 22.4, 19.8,
+    // on, where it costs 6 % if they are in the cache and gains 13 % if they are not.  us, ordinary and nontemporal, x in the caches before / not: gated 84 MB 18.5, 19.0 / 22.4, 19.8,
     // 168 MB 33.8, 36.0 / 41.6, 36.1, 336 MB 80, 70; plain 168 MB 38, 44 / 46.4, 44.0.
     const bool once = R * K * (ACT ? 2 : 1) * elem_size<DT>() > (int64_t)(ACT ? 128 : 256) << 20;
     for (int64_t r0 = 0; r0 < R; r0 += MOST) {

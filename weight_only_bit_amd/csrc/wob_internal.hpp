@@ -137,7 +137,7 @@ struct NormArgs {
     int H, quant;
     float alpha, eps;
     int64_t row0 = 0; // the first row of this launch
-    bool once = false; // rows are read and written nontemporally
+    bool once = false; // rows are read nontemporally (values are written so always)
 };
 hipError_t launch_residual_norm(const NormArgs &a, int dt, int residual_dt, hipStream_t stream);
 

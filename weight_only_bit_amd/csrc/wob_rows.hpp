@@ -99,7 +99,7 @@ __device__ __forceinline__ uint32_t join_halves(uint32_t v, F f)
     }
 }
 
-// f over the NT threads that share a row, the result in every one of them.  NT = 16, 32, 64: lanes of
+// f over the NT threads that share a row, the result in every one of them.  NT = 8, 16, 32, 64: lanes of
 // a wave; more: the waves' results meet in `part` (NT / 64 words of LDS that nothing else
 // is read from until the next barrier).
 template <int NT, class F>
